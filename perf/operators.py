@@ -310,7 +310,8 @@ def _own_run(s):
         w4.kv_cache_read(s["cache"], form, case["page"], s["slots"], s["out_k"], s["out_v"])
         return {"k": s["out_k"], "v": s["out_v"]}
     if "ws" not in s:       # kept between calls, as a serving loop does
-        need = w4.kv_cache_attention_workspace(*s["q"].shape, case["kv_heads"], s["table"].shape[1], case["page"])
+        seqs, hq, dim = s["q"].shape
+        need = w4.kv_cache_attention_workspace(seqs, hq, case["kv_heads"], dim, s["table"].shape[1], case["page"])
         s["ws"] = torch.empty(max(16, need), dtype=torch.uint8, device=_DEV)
     w4.kv_cache_attention(s["q"], s["cache"], form, case["page"], case["kv_heads"], s["table"], s["lens"],
                           1.0 / math.sqrt(case["head_dim"]), s["out"], case["window"], s["lse"], s["ws"])
