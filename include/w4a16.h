@@ -487,6 +487,149 @@ int w8a8_moe_layer(const uint16_t* x, const float* logits, int64_t T, int32_t E,
                    const uint8_t* w1q, const float* w1_scale, const uint8_t* w2q, const float* w2_scale,
                    int32_t activation, uint16_t* y, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------- around the matmuls (decode)
+ * What a decoder layer runs between the library's matmuls: the norm in front
+ * of each projection or MoE call, and the key-value cache with the attention
+ * over it ([VG] "Compression Without Regret", section "2. What you can
+ * quantize": weights, activations and the KV cache).  The cache is held in the
+ * library's own two quantized formats (E4M3 with a scale per row, Q4_0 levels
+ * in groups of 32 with bf16 scales) or in bf16.
+ */
+
+/*
+ * w4a16_add_rmsnorm -- the residual addition and the RMS norm in front of a
+ * W4A16 call:
+ *   r = bf16(x + residual)   (fp32 sum; r = x when residual is null)
+ *   y = bf16( r * fl32(weight_offset + weight) / sqrt(mean(r^2) + eps) )
+ *   x         in  [rows][d] bf16
+ *   residual  in, nullable  [rows][d] bf16
+ *   weight    in  [d] bf16; weight_offset 1 for weights stored around zero
+ *   sum_out   out, nullable (needs residual)  [rows][d] bf16: r
+ *   y         out [rows][d] bf16
+ * Sums and products are 64-bit; y is rounded once.  A NaN or an infinity in a
+ * row makes the row's y NaN where the formula does.  y may be x or residual,
+ * sum_out may be x or residual (the same pointer); any other overlap of an
+ * output with another argument is W4_ERR_ARG.
+ * Requires d % 32 == 0, d <= 2^20, rows*d <= 2^40, finite eps >= 0.
+ */
+int w4a16_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t d,
+                      float eps, float weight_offset, uint16_t* sum_out, uint16_t* y, hipStream_t stream);
+
+/*
+ * w8a8_add_rmsnorm_quantize -- the same with the output as E4M3 rows for
+ * w8a8_moe_gmm: y unrounded, amax = max |y| of the row,
+ *   scale = fl32(amax / 448) (1 where that is 0),
+ *   q = E4M3(clamp(fl32(y / scale), -448, 448)), nearest, ties to even.
+ * A row with a NaN or an infinite y: scale NaN, codes 0.
+ *   q      out [rows][d] E4M3 codes (overlaps nothing)
+ *   scale  out [rows] fp32, 4-byte aligned
+ * Other arguments, limits and errors as above.
+ */
+int w8a8_add_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows,
+                              int64_t d, float eps, float weight_offset, uint16_t* sum_out, uint8_t* q, float* scale,
+                              hipStream_t stream);
+
+/*
+ * Key-value cache formats.  A row is one token's keys (or values) of one kv head.
+ *   W4_KV_BF16  the row as it is
+ *   W4_KV_E4M3  per row: amax = max |x|, s = fl32(amax / 448) (1 for zeros),
+ *               codes E4M3(clamp(fl32(x / s), -448, 448)): w8a8_quantize_rows
+ *   W4_KV_Q4    per group of 32: s = bf16(fl32(amax / 7)), codes
+ *               clamp(round-half-even(fl32(x / s)), -8, 7) (0 where s is 0)
+ * A row (E4M3) or group (Q4) with a NaN or an infinity: s NaN, codes 0.
+ *
+ * Layout (this library's own, for gfx950): one buffer of n_pages pages,
+ * page_size tokens each, kv_cache_page_bytes bytes a page:
+ *   [page][kv head][K block, V block],  a block: codes, then scales.
+ * With tiles of 16 tokens, NG = head_dim/32 groups, U groups to a unit (bf16 1,
+ * E4M3 2, Q4 4, or 2 at head_dim 64) and a unit of 64 lanes x 16 bytes (8 bytes
+ * for Q4 at head_dim 64), token r = 4a + j of tile t:
+ *   K  dimensions 32g + 8c .. +7 (c = 0..3): unit t*NG/U + g/U, lane 16c + r,
+ *      part g%U; Q4 words hold their 8 codes as tile16 words do
+ *   V  dimension 32g + 2m + b (m = 0..15, b = 0, 1): unit t*NG/U + g/U, lane
+ *      16a + m, part g%U, element [b][j]; Q4: byte j, b = 0 in the low nibble
+ *   scales  E4M3: fp32 [token]; Q4: bf16 [t][a][g][j]
+ * so that a wave's load is 1 KiB of consecutive bytes and each lane's piece is
+ * a matrix-core operand: 8 dimensions of one token for K, 4 tokens of one
+ * dimension for V.
+ *
+ * A slot is page * page_size + position in the page.
+ * Common limits: head_dim 64, 128 or 256; page_size a power of two from 16 to
+ * 65536; kv_heads <= 1024; n_pages < 2^31 (W4_ERR_SHAPE).
+ */
+enum { W4_KV_BF16 = 0, W4_KV_E4M3 = 1, W4_KV_Q4 = 2 };
+
+/* Bytes of one page; 0 for sizes outside the limits. */
+size_t kv_cache_page_bytes(int32_t format, int32_t page_size, int32_t kv_heads, int32_t head_dim);
+
+/*
+ * kv_cache_write -- quantize new tokens' keys and values into their slots.
+ *   k, v       in  [tokens] rows of kv_heads*head_dim bf16, k_stride / v_stride
+ *              elements apart (multiples of 8, at least the row's width): slices
+ *              of one fused projection's output will do
+ *   slots      in  [tokens] int64, 8-byte aligned; negative: the token is
+ *              skipped (padding).  Slots have to be distinct within a call: a
+ *              slot named twice holds a mixture of its tokens afterwards.
+ *   cache      in/out, 16-byte aligned, n_pages * kv_cache_page_bytes bytes;
+ *              rows of other slots stay as they are
+ *   counters   in/out, nullable, 8-byte aligned, two values (the caller zeroes
+ *              them): counters[0] += tokens whose slot lies past the cache
+ *              (skipped too), counters[1] += rows (E4M3) or groups (Q4) with a
+ *              NaN or an infinity
+ * Requires tokens < 2^28.
+ */
+int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                   const int64_t* slots, int32_t format, void* cache, int64_t n_pages, int32_t page_size,
+                   int32_t kv_heads, int32_t head_dim, unsigned long long* counters, hipStream_t stream);
+
+/*
+ * kv_cache_read -- the rows of given slots as bf16 (code times scale rounded
+ * once) or fp32 (W4_OUT_F32; exact for Q4, rounded once for E4M3).  Rows of
+ * negative slots and of slots past the cache (counted as above) are left as
+ * they were; a slot may be named any number of times.
+ *   k, v  out [tokens] rows of kv_heads*head_dim of out_dtype, strides in
+ *         elements (multiples of 8), 16-byte aligned, not overlapping
+ */
+int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads,
+                  int32_t head_dim, const int64_t* slots, int64_t tokens, void* k, void* v, int64_t k_stride,
+                  int64_t v_stride, int32_t out_dtype, unsigned long long* counters, hipStream_t stream);
+
+/*
+ * kv_cache_attention -- attention of one new token per sequence over the cache.
+ * Sequence i attends to the positions t in [max(0, n - window), n), n =
+ * seq_lens[i] (window 0: all of [0, n)), whose rows are those of slot
+ * block_table[i][t / page_size] * page_size + t % page_size.  Query head h
+ * reads kv head h / (heads / kv_heads):
+ *   s_t = scale * (q . k_t)
+ *   out = sum_t softmax(s)_t v_t,   lse = log sum_t exp(s_t)
+ * over the dequantized (unrounded) rows, in fp32; out is rounded once.  A
+ * sequence without positions gives out = 0 and lse = -infinity.  Cache rows
+ * outside the positions may hold anything.  Lengths are cut to [0,
+ * table_width * page_size]; positions in pages outside [0, n_pages) count as
+ * absent.
+ *   q            in  [seqs] rows of heads*head_dim bf16, q_stride elements apart
+ *   block_table  in  [seqs][table_width] int32
+ *   seq_lens     in  [seqs] int32
+ *   out          out [seqs][heads][head_dim] bf16
+ *   lse          out, nullable  [seqs][heads] fp32
+ *   counters     in/out, nullable, 8-byte aligned: counters[0] += table entries
+ *                of attended positions that lie outside the cache
+ *   ws           kv_cache_attention_workspace(...) bytes, 16-byte aligned (it may
+ *                be null where that is 0); its contents do not matter.  Calls
+ *                that overlap in time need one each.
+ * The results do not depend on what else runs (no atomics in the sums); they
+ * depend on table_width through the split of the length.
+ * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, table_width *
+ * page_size < 2^31, n_pages >= 1, window >= 0, finite scale.
+ */
+size_t kv_cache_attention_workspace(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    int64_t table_width, int32_t page_size);
+int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_t heads, const void* cache,
+                       int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                       const int32_t* block_table, int64_t table_width, const int32_t* seq_lens, float scale,
+                       int32_t window, uint16_t* out, float* lse, unsigned long long* counters, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

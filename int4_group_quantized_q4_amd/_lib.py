@@ -24,6 +24,10 @@ W4_EPI_SWIGLU = 2
 W4_OUT_BF16 = 0
 W4_OUT_F32 = 1
 
+W4_KV_BF16 = 0
+W4_KV_E4M3 = 1
+W4_KV_Q4 = 2
+
 W4_KERNEL_AUTO = 0
 W4_KERNEL_STREAM = 1
 W4_KERNEL_TILED = 2
@@ -37,6 +41,7 @@ W4_GROUP_NONFINITE = 255
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/w4a16.h
@@ -70,6 +75,14 @@ SIGNATURES = {
     "w8a8_moe_layer_workspace": (ctypes.c_size_t, [_i64, _i32, _i32, _i64, _i64]),
     "w8a8_moe_layer": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i64, _i64, _p, _p, _p, _p, _i32, _p, _p,
                                       ctypes.c_size_t, _p]),
+    "w4a16_add_rmsnorm": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f32, _f32, _p, _p, _p]),
+    "w8a8_add_rmsnorm_quantize": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f32, _f32, _p, _p, _p, _p]),
+    "kv_cache_page_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "kv_cache_write": (ctypes.c_int, [_p, _p, _i64, _i64, _i64, _p, _i32, _p, _i64, _i32, _i32, _i32, _p, _p]),
+    "kv_cache_read": (ctypes.c_int, [_p, _i32, _i64, _i32, _i32, _i32, _p, _i64, _p, _p, _i64, _i64, _i32, _p, _p]),
+    "kv_cache_attention_workspace": (_sz, [_i64, _i32, _i32, _i32, _i64, _i32]),
+    "kv_cache_attention": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _i32, _i64, _i32, _i32, _i32, _p, _i64, _p, _f32,
+                                          _i32, _p, _p, _p, _p, _sz, _p]),
 }
 
 

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "kv_layout.h"
 #include "w4a16.h"
 
 namespace {
@@ -683,6 +684,214 @@ int w8a8_moe_layer(const uint16_t* x, const float* logits, int64_t T, int32_t E,
   w4::launch_fp8_quant_rows(act, R, I, aq, as, stream);
   w4::launch_fp8_gemm(a2, stream);
   w4::launch_combine(o, W4_OUT_F32, r2s, wts, T, k, d, y, stream);
+  return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Residual addition + RMS norm.
+
+static bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + qn && b < a + pn;
+}
+
+// Shared by both forms: W4_OK to run, kLayerEmpty for nothing to do, else the
+// error.  An output may be exactly one of the inputs (each element is read
+// before it is written, by the same thread), but no other overlap is allowed.
+static int check_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t d,
+                      float eps, const uint16_t* sum_out, const void* y, size_t y_row_bytes) {
+  if (rows < 0 || d < 0 || !(eps >= 0.f) || !(eps < INFINITY)) return W4_ERR_ARG;
+  if (d % 32 != 0) return W4_ERR_SHAPE;
+  if (rows == 0 || d == 0) return kLayerEmpty;
+  if (d > ((int64_t)1 << 20) || rows > ((int64_t)1 << 40) / d) return W4_ERR_SHAPE;
+  if (!x || !weight || !y || (sum_out && !residual)) return W4_ERR_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(y) || (residual && !aligned16(residual)) ||
+      (sum_out && !aligned16(sum_out)))
+    return W4_ERR_ARG;
+  const size_t n = (size_t)rows * (size_t)d * 2, yn = (size_t)rows * y_row_bytes;
+  const bool same_ok = y_row_bytes == (size_t)d * 2;   // the E4M3 rows have another pitch
+  if (overlap(y, yn, x, n) && !(same_ok && y == x)) return W4_ERR_ARG;
+  if (overlap(y, yn, residual, n) && !(same_ok && y == residual)) return W4_ERR_ARG;
+  if (overlap(sum_out, n, x, n) && sum_out != x) return W4_ERR_ARG;
+  if (overlap(sum_out, n, residual, n) && sum_out != residual) return W4_ERR_ARG;
+  if (overlap(y, yn, sum_out, n) || overlap(y, yn, weight, (size_t)d * 2) || overlap(sum_out, n, weight, (size_t)d * 2))
+    return W4_ERR_ARG;
+  return W4_OK;
+}
+
+int w4a16_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t d,
+                      float eps, float weight_offset, uint16_t* sum_out, uint16_t* y, hipStream_t stream) {
+  const int st = check_norm(x, residual, weight, rows, d, eps, sum_out, y, (size_t)(d < 0 ? 0 : d) * 2);
+  if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
+  w4::launch_add_rmsnorm(x, residual, weight, rows, d, eps, weight_offset, sum_out, y, nullptr, nullptr, stream);
+  return launch_status();
+}
+
+int w8a8_add_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows,
+                              int64_t d, float eps, float weight_offset, uint16_t* sum_out, uint8_t* q, float* scale,
+                              hipStream_t stream) {
+  const int st = check_norm(x, residual, weight, rows, d, eps, sum_out, q, (size_t)(d < 0 ? 0 : d));
+  if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
+  if (!scale || (reinterpret_cast<uintptr_t>(scale) & 3u)) return W4_ERR_ARG;
+  const size_t n = (size_t)rows * (size_t)d;
+  if (overlap(scale, (size_t)rows * 4, q, n) || overlap(scale, (size_t)rows * 4, x, 2 * n) ||
+      overlap(scale, (size_t)rows * 4, residual, 2 * n) || overlap(scale, (size_t)rows * 4, sum_out, 2 * n) ||
+      overlap(scale, (size_t)rows * 4, weight, (size_t)d * 2))
+    return W4_ERR_ARG;
+  w4::launch_add_rmsnorm(x, residual, weight, rows, d, eps, weight_offset, sum_out, nullptr, q, scale, stream);
+  return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Key-value cache.
+
+static int log2_of(int64_t v) {
+  int s = 0;
+  while (((int64_t)1 << s) < v) ++s;
+  return s;
+}
+
+static int check_kv_shape(int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
+  if (format != W4_KV_BF16 && format != W4_KV_E4M3 && format != W4_KV_Q4) return W4_ERR_ARG;
+  if (n_pages < 0 || page_size < 1 || kv_heads < 1 || head_dim < 1) return W4_ERR_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return W4_ERR_SHAPE;
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return W4_ERR_SHAPE;
+  if (kv_heads > 1024 || n_pages > INT32_MAX) return W4_ERR_SHAPE;
+  return W4_OK;
+}
+
+size_t kv_cache_page_bytes(int32_t format, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
+  if (check_kv_shape(format, 0, page_size, kv_heads, head_dim) != W4_OK) return 0;
+  return (size_t)kv_heads * 2 * (size_t)w4::kv_block_bytes(format, page_size, head_dim);
+}
+
+static w4::KvArgs kv_args(int32_t format, void* cache, int64_t n_pages, int32_t page_size, int32_t kv_heads,
+                          int32_t head_dim, const int64_t* slots, int64_t tokens, unsigned long long* counters) {
+  w4::KvArgs a{};
+  a.format = format;
+  a.cache = static_cast<uint8_t*>(cache);
+  a.n_pages = n_pages;
+  a.page_shift = log2_of(page_size);
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.block_bytes = w4::kv_block_bytes(format, page_size, head_dim);
+  a.page_bytes = a.block_bytes * 2 * kv_heads;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.counters = counters;
+  return a;
+}
+
+// Rows of the caller's k / v / q: 16-byte aligned, `stride` elements apart.
+static int check_rows(const void* p, int64_t stride, int64_t width) {
+  if (!p || !aligned16(p)) return W4_ERR_ARG;
+  if (stride < width || stride % 8 != 0) return W4_ERR_ARG;
+  return W4_OK;
+}
+
+static int check_kv_rows(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                         const int64_t* slots, int32_t format, const void* cache, int64_t n_pages, int32_t page_size,
+                         int32_t kv_heads, int32_t head_dim, const unsigned long long* counters) {
+  if (tokens < 0) return W4_ERR_ARG;
+  int st = check_kv_shape(format, n_pages, page_size, kv_heads, head_dim);
+  if (st != W4_OK) return st;
+  if (tokens >= ((int64_t)1 << 28)) return W4_ERR_SHAPE;
+  if (tokens == 0) return kLayerEmpty;
+  if (!slots || !aligned8(slots) || !cache || !aligned16(cache) || (counters && !aligned8(counters))) return W4_ERR_ARG;
+  st = check_rows(k, k_stride, (int64_t)kv_heads * head_dim);
+  if (st != W4_OK) return st;
+  return check_rows(v, v_stride, (int64_t)kv_heads * head_dim);
+}
+
+int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                   const int64_t* slots, int32_t format, void* cache, int64_t n_pages, int32_t page_size,
+                   int32_t kv_heads, int32_t head_dim, unsigned long long* counters, hipStream_t stream) {
+  const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
+                               head_dim, counters);
+  if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
+  w4::KvArgs a = kv_args(format, cache, n_pages, page_size, kv_heads, head_dim, slots, tokens, counters);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  w4::launch_kv_write(a, stream);
+  return launch_status();
+}
+
+int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads,
+                  int32_t head_dim, const int64_t* slots, int64_t tokens, void* k, void* v, int64_t k_stride,
+                  int64_t v_stride, int32_t out_dtype, unsigned long long* counters, hipStream_t stream) {
+  if (out_dtype != W4_OUT_BF16 && out_dtype != W4_OUT_F32) return W4_ERR_ARG;
+  const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
+                               head_dim, counters);
+  if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
+  w4::KvArgs a = kv_args(format, const_cast<void*>(cache), n_pages, page_size, kv_heads, head_dim, slots, tokens, counters);
+  a.k_out = k;
+  a.v_out = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  w4::launch_kv_read(a, out_dtype, stream);
+  return launch_status();
+}
+
+static int check_attention(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t table_width,
+                           int32_t page_size) {
+  const int st = check_kv_shape(W4_KV_BF16, 0, page_size, kv_heads, head_dim);
+  if (st != W4_OK) return st;
+  if (seqs < 0 || heads < 1 || table_width < 0) return W4_ERR_ARG;
+  if (heads % kv_heads != 0 || heads > 16384 || seqs > 65535 || table_width > (int64_t)INT32_MAX / page_size)
+    return W4_ERR_SHAPE;
+  return W4_OK;
+}
+
+size_t kv_cache_attention_workspace(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    int64_t table_width, int32_t page_size) {
+  if (check_attention(seqs, heads, kv_heads, head_dim, table_width, page_size) != W4_OK || seqs == 0) return 0;
+  return w4::kv_attention_workspace_bytes(seqs, heads, kv_heads, head_dim, table_width * page_size);
+}
+
+int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_t heads, const void* cache,
+                       int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                       const int32_t* block_table, int64_t table_width, const int32_t* seq_lens, float scale,
+                       int32_t window, uint16_t* out, float* lse, unsigned long long* counters, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
+  int st = check_kv_shape(format, n_pages, page_size, kv_heads, head_dim);
+  if (st != W4_OK) return st;
+  st = check_attention(seqs, heads, kv_heads, head_dim, table_width, page_size);
+  if (st != W4_OK) return st;
+  if (window < 0 || !(scale > -INFINITY && scale < INFINITY)) return W4_ERR_ARG;
+  if (seqs == 0) return W4_OK;
+  if (n_pages < 1 || !cache || !seq_lens || !out || (table_width > 0 && !block_table)) return W4_ERR_ARG;
+  if (!aligned16(cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (counters && !aligned8(counters)))
+    return W4_ERR_ARG;
+  st = check_rows(q, q_stride, (int64_t)heads * head_dim);
+  if (st != W4_OK) return st;
+  const size_t need = kv_cache_attention_workspace(seqs, heads, kv_heads, head_dim, table_width, page_size);
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return W4_ERR_WORKSPACE;
+  w4::AttnArgs a{};
+  a.q = q;
+  a.seqs = seqs;
+  a.q_stride = q_stride;
+  a.heads = heads;
+  a.format = format;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.n_pages = n_pages;
+  a.page_shift = log2_of(page_size);
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.block_bytes = w4::kv_block_bytes(format, page_size, head_dim);
+  a.page_bytes = a.block_bytes * 2 * kv_heads;
+  a.table = block_table;
+  a.table_width = table_width;
+  a.lens = seq_lens;
+  a.scale = scale;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  a.counters = counters;
+  w4::launch_kv_attention(a, ws, stream);
   return launch_status();
 }
 

@@ -1,0 +1,489 @@
+// Attention of one new token per sequence over the paged key-value cache.
+//
+//   s_t = scale * q . k_t,  out = sum_t softmax(s)_t v_t,  lse = log sum_t e^(s_t)
+//
+// over the positions [max(0, len - window), len) of a sequence, for the G =
+// heads / kv_heads query heads that share a kv head.  One pass over the cache
+// with the running maximum and sum of the softmax.
+//
+// Bound by the cache's bytes: a token's K and V row of a head are read once
+// for all G query heads.
+//
+// Work split: grid (splits of the length, kv head x tile of 16 query heads,
+// sequence); a workgroup of 4 waves takes one split, and a wave 32 tokens at
+// a time (two tiles of the cache), with its own running maximum, sum and
+// output.  The waves are joined through LDS, the splits by a second kernel.
+//
+// Matrix layouts (16x16x32 bf16, lane = 16c + n): the scores are formed as
+// S^T = K . Q^T with a tile's 16 tokens as rows, so lane (c, n) holds the
+// scores of head n for tokens 4c .. 4c+3 of both tiles.  Those 8 values are
+// the lane's B operand of O^T = V^T . P^T when the 32 tokens are numbered (c,
+// tile, j), and the cache keeps V so that one lane's load holds those tokens
+// of dimension 32g + 2n + b: no value crosses lanes between the two products.
+//
+// Precision: q and the codes are exact in bf16 and all sums are fp32.  The
+// probabilities (times the V scales) enter the second product as two bf16
+// terms, high and low, so they carry 16 bits and the output's only visible
+// rounding is its last one.
+
+#include "common.h"
+#include "internal.h"
+#include "kv_layout.h"
+#include "w4a16.h"
+
+namespace w4 {
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kChunk = 32;          // tokens per wave step
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
+// 4 E4M3 codes -> 4 bf16 (two words), exact
+__device__ __forceinline__ u32x2 e4m3_to_bf16(uint32_t w) {
+  u32x2 o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+  return o;
+}
+
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// 8 fp32 values -> bf16 high and low parts
+__device__ __forceinline__ void split_bf16(const float p[8], u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
+    lo[i] = pk_bf16(p[2 * i] - bf16_to_f32(hi[i] & 0xFFFFu), p[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return mfma16x16x32(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c);
+}
+
+// over the four lanes of one column n
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// The positions a sequence attends to, in 32-token chunks, and how they are
+// dealt to the splits (the same for the attention and the join kernel).
+struct Span {
+  int64_t n, lo;          // positions [lo, n)
+  int64_t first, chunks;  // chunk range
+  int64_t per;            // chunks per split
+  int live;               // splits that have any
+};
+
+__device__ __forceinline__ Span find_span(const AttnArgs& a, int64_t seq) {
+  Span s;
+  s.n = a.lens[seq];
+  const int64_t most = a.table_width << a.page_shift;
+  s.n = s.n < 0 ? 0 : s.n > most ? most : s.n;
+  s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
+  s.first = s.lo / kChunk;
+  s.chunks = (s.n + kChunk - 1) / kChunk - s.first;
+  s.per = (s.chunks + a.splits - 1) / a.splits;
+  if (s.per < kWaves) s.per = kWaves;
+  s.live = s.chunks > 0 ? (int)((s.chunks + s.per - 1) / s.per) : 0;
+  return s;
+}
+
+template <int FMT, int NG>
+__global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
+  typedef KvLayout<FMT, NG> L;
+  constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
+  __shared__ float s_o[kWaves][16][BD + 4];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n16 = lane & 15, c = lane >> 4;
+  const int split = blockIdx.x;
+  const int head = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
+  const int64_t seq = blockIdx.z;
+  const int G = a.heads / a.kv_heads;
+  const int live_heads = G - 16 * ht < 16 ? G - 16 * ht : 16;
+  const int64_t h0 = (int64_t)head * G + 16 * ht;     // first query head
+  const Span sp = find_span(a, seq);
+  if (a.counters && split == 0 && blockIdx.y == 0) {  // table entries outside the cache, once per entry
+    const int64_t p1 = (sp.n + (1 << a.page_shift) - 1) >> a.page_shift;
+    for (int64_t p = (sp.lo >> a.page_shift) + threadIdx.x; p < p1; p += 64 * kWaves) {
+      const int64_t id = a.table[seq * a.table_width + p];
+      if (id < 0 || id >= a.n_pages) atomicAdd(a.counters, 1ull);
+    }
+  }
+  if (split >= sp.live && !(split == 0 && sp.live == 0)) return;
+
+  // q of head n16: dimensions 32g + 8c ..
+  u32x4 q[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    q[g] = u32x4{0u, 0u, 0u, 0u};
+    if (n16 < live_heads)
+      q[g] = *reinterpret_cast<const u32x4*>(a.q + seq * a.q_stride + (h0 + n16) * L::D + 32 * g + 8 * c);
+  }
+  // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
+  float kbias[NG];
+  if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t += bf16_to_f32(q[g][i] & 0xFFFFu) + __uint_as_float(q[g][i] & 0xFFFF0000u);
+      kbias[g] = -136.0f * column_sum(t);
+    }
+  }
+
+  f32x4 acc[NG][2];
+  f32x4 vbias[FMT == W4_KV_Q4 ? NG : 1];
+  const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int g = 0; g < NG; ++g) acc[g][0] = acc[g][1] = zero4;
+#pragma unroll
+  for (int g = 0; g < (FMT == W4_KV_Q4 ? NG : 1); ++g) vbias[g] = zero4;
+  float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's tokens only
+  const float scale2 = a.scale * kLog2e;
+
+  const int64_t begin = sp.first + split * sp.per;
+  const int64_t end = begin + sp.per < sp.first + sp.chunks ? begin + sp.per : sp.first + sp.chunks;
+  const int tile_shift = a.page_shift - 4;
+  for (int64_t ch = begin + wv; ch < end; ch += kWaves) {
+    // the two tiles' places; a tile past the table is masked as a whole below
+    const uint8_t* kp[2];
+    bool good[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t tile = 2 * ch + t;
+      const int64_t pi = tile >> tile_shift;
+      const int64_t id = pi < a.table_width ? (int64_t)a.table[seq * a.table_width + pi] : -1;
+      good[t] = id >= 0 && id < a.n_pages;
+      kp[t] = a.cache + (good[t] ? id : 0) * a.page_bytes + (int64_t)head * 2 * a.block_bytes;
+    }
+    int tip[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) tip[t] = (int)((2 * ch + t) & ((1 << tile_shift) - 1));
+    const int64_t scale_off = ((int64_t)L::kTileBytes << a.page_shift) / kKvTile;
+
+    u32x4 kr[2][L::NU], vr[2][L::NU];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < L::NU; ++u) {
+        const int off = tip[t] * L::kTileBytes + (u * 64 + lane) * L::kUnitBytes;
+        if constexpr (L::kUnitBytes == 16) {
+          kr[t][u] = load16(kp[t] + off);
+          vr[t][u] = load16(kp[t] + a.block_bytes + off);
+        } else {
+          const u32x2 k2 = *reinterpret_cast<const u32x2*>(kp[t] + off);
+          const u32x2 v2 = *reinterpret_cast<const u32x2*>(kp[t] + a.block_bytes + off);
+          kr[t][u] = u32x4{k2[0], k2[1], 0u, 0u};
+          vr[t][u] = u32x4{v2[0], v2[1], 0u, 0u};
+        }
+      }
+    // scales of tokens 4c .. 4c+3: one (E4M3) or NG (Q4) for each token
+    constexpr int NS = FMT == W4_KV_BF16 ? 1 : FMT == W4_KV_E4M3 ? 1 : NG;
+    float ks[2][NS][4], vs[2][NS][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if constexpr (FMT == W4_KV_E4M3) {
+        const f32x4 k4 = *reinterpret_cast<const f32x4*>(kp[t] + scale_off + tip[t] * 64 + 16 * c);
+        const f32x4 v4 = *reinterpret_cast<const f32x4*>(kp[t] + a.block_bytes + scale_off + tip[t] * 64 + 16 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ks[t][0][j] = k4[j];
+          vs[t][0][j] = v4[j];
+        }
+      } else if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int so = tip[t] * 32 * NG + (c * NG + g) * 8;
+          const u32x2 k2 = *reinterpret_cast<const u32x2*>(kp[t] + scale_off + so);
+          const u32x2 v2 = *reinterpret_cast<const u32x2*>(kp[t] + a.block_bytes + scale_off + so);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ks[t][g][j] = (j & 1) ? __uint_as_float(k2[j >> 1] & 0xFFFF0000u) : bf16_to_f32(k2[j >> 1] & 0xFFFFu);
+            vs[t][g][j] = (j & 1) ? __uint_as_float(v2[j >> 1] & 0xFFFF0000u) : bf16_to_f32(v2[j >> 1] & 0xFFFFu);
+          }
+        }
+      }
+    }
+
+    // scores
+    float p[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 s4 = zero4;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int u = g / L::U, part = g % L::U;
+        if constexpr (FMT == W4_KV_BF16) {
+          s4 = mfma(kr[t][u], q[g], s4);
+        } else if constexpr (FMT == W4_KV_E4M3) {
+          const u32x2 a0 = e4m3_to_bf16(kr[t][u][2 * part]), a1 = e4m3_to_bf16(kr[t][u][2 * part + 1]);
+          s4 = mfma(u32x4{a0[0], a0[1], a1[0], a1[1]}, q[g], s4);
+        } else {
+          const f32x4 d = mfma(biased_pairs(kr[t][u][part]), q[g], f32x4{kbias[g], kbias[g], kbias[g], kbias[g]});
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s4[j] = fmaf(ks[t][g][j], d[j], s4[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[4 * t + j] = s4[j] * (FMT == W4_KV_E4M3 ? scale2 * ks[t][0][j] : scale2);
+    }
+
+    // Positions outside the span or in pages outside the cache: no score, and
+    // what their V rows hold (anything) is cleared, since 0 * NaN is NaN.
+    if (ch * kChunk < sp.lo || (ch + 1) * kChunk > sp.n || !good[0] || !good[1]) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t pos = ch * kChunk + 16 * t + 4 * c + j;
+          const bool in = good[t] && pos >= sp.lo && pos < sp.n;
+          if (!in) {
+            p[4 * t + j] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < NS; ++g) vs[t][g][j] = 0.f;
+          }
+          keep |= in ? 0xFFu << (8 * j) : 0u;
+        }
+        // byte masks widened to the words that hold (tokens 0 and 1) and (2 and 3)
+        const uint32_t k01 = ((keep & 0xFFu) | ((keep & 0xFF00u) << 8)) * 0x101u;
+        const uint32_t k23 = (((keep >> 16) & 0xFFu) | ((keep >> 24) << 16)) * 0x101u;
+        // operands are indexed by row (dimension) here: lane (c, m) holds tokens 4c + j too
+#pragma unroll
+        for (int u = 0; u < L::NU; ++u) {
+          if constexpr (FMT == W4_KV_BF16) {
+            vr[t][u][0] &= k01;
+            vr[t][u][1] &= k23;
+            vr[t][u][2] &= k01;
+            vr[t][u][3] &= k23;
+          } else if constexpr (FMT == W4_KV_E4M3) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[t][u][i] &= keep;
+          }
+        }
+      }
+    }
+
+    // softmax: running maximum (base-2 exponents) and this lane's sum
+    float top = p[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
+    top = column_max(top);
+    const float m_new = fmaxf(m_run, top);
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;   // nothing yet: every p is 0
+    const float alpha = __builtin_amdgcn_exp2f(m_run - m_use);
+    m_run = m_new;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(p[i] - m_use);
+      sum += p[i];
+    }
+    l_run = l_run * alpha + sum;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[g][b] *= alpha;
+    if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) vbias[g] *= alpha;
+    }
+
+    // O^T += V^T . P^T
+    u32x4 hi, lo;
+    if constexpr (FMT != W4_KV_Q4) {
+      if constexpr (FMT == W4_KV_E4M3) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] *= vs[i >> 2][0][i & 3];
+      }
+      split_bf16(p, hi, lo);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int u = g / L::U, part = g % L::U;
+      if constexpr (FMT == W4_KV_BF16) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const u32x4 av = {vr[0][u][2 * b], vr[0][u][2 * b + 1], vr[1][u][2 * b], vr[1][u][2 * b + 1]};
+          acc[g][b] = mfma(av, hi, acc[g][b]);
+          acc[g][b] = mfma(av, lo, acc[g][b]);
+        }
+      } else if constexpr (FMT == W4_KV_E4M3) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const u32x2 a0 = e4m3_to_bf16(vr[0][u][2 * part + b]), a1 = e4m3_to_bf16(vr[1][u][2 * part + b]);
+          const u32x4 av = {a0[0], a0[1], a1[0], a1[1]};
+          acc[g][b] = mfma(av, hi, acc[g][b]);
+          acc[g][b] = mfma(av, lo, acc[g][b]);
+        }
+      } else {
+        float ps[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ps[i] = p[i] * vs[i >> 2][g][i & 3];
+        split_bf16(ps, hi, lo);
+        const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
+        vbias[g] = mfma(bias, hi, vbias[g]);
+        vbias[g] = mfma(bias, lo, vbias[g]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          u32x4 av;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // byte j: token j's code of dimension 2m (low nibble), 2m + 1 (high)
+            const uint32_t w = (b ? vr[t][u][part] >> 4 : vr[t][u][part]) & 0x0F0F0F0Fu;
+            av[2 * t] = __builtin_amdgcn_perm(0x43434343u, w, 0x04010400u);
+            av[2 * t + 1] = __builtin_amdgcn_perm(0x43434343u, w, 0x04030402u);
+          }
+          acc[g][b] = mfma(av, hi, acc[g][b]);
+          acc[g][b] = mfma(av, lo, acc[g][b]);
+        }
+      }
+    }
+  }
+
+  if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[g][b] += vbias[g];
+  }
+
+  // Join the waves: lane (c, n) holds, for group g, dimensions 32g + 8c + 2i + b.
+  const float l_col = column_sum(l_run);
+  if (c == 0) {
+    s_m[wv][n16] = m_run;
+    s_l[wv][n16] = l_col;
+  }
+  __syncthreads();
+  float m_all = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m_all = fmaxf(m_all, s_m[w][n16]);
+  const float mine = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_all);
+  constexpr int ROUNDS = 32 * NG / BD;
+#pragma unroll
+  for (int rd = 0; rd < ROUNDS; ++rd) {
+    if (rd) __syncthreads();
+#pragma unroll
+    for (int g = 0; g < BD / 32; ++g) {
+      float* o = &s_o[wv][n16][32 * g + 8 * c];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[2 * i] = acc[rd * (BD / 32) + g][0][i] * mine;
+        o[2 * i + 1] = acc[rd * (BD / 32) + g][1][i] * mine;
+      }
+    }
+    __syncthreads();
+    // thread -> 4 dimensions of one head
+    for (int e = threadIdx.x; e < live_heads * (BD / 4); e += 64 * kWaves) {
+      const int h = e / (BD / 4), d = 4 * (e % (BD / 4));
+      float mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+      f32x4 o = zero4;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        // a wave without a score has l = 0 (or NaN, which passes on)
+        l += s_m[w][h] == -INFINITY ? s_l[w][h] : s_l[w][h] * __builtin_amdgcn_exp2f(s_m[w][h] - mx);
+        o += *reinterpret_cast<const f32x4*>(&s_o[w][h][d]);
+      }
+      const int64_t row = seq * a.heads + h0 + h;
+      const int dim = rd * BD + d;
+      if (sp.live <= 1) {
+        const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // l: 0 for an empty row, NaN passes on
+        u32x2 w2 = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
+        *reinterpret_cast<u32x2*>(a.out + row * L::D + dim) = w2;
+        if (a.lse && dim == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+      } else {
+        const int64_t pr = row * a.splits + split;
+        *reinterpret_cast<f32x4*>(a.part_o + pr * L::D + dim) = o;
+        if (dim == 0) {
+          a.part_ml[2 * pr] = mx;
+          a.part_ml[2 * pr + 1] = l;
+        }
+      }
+    }
+  }
+}
+
+// Joins the splits of one (sequence, query head): 4 dimensions per thread,
+// split order, fp32.
+__global__ void __launch_bounds__(64) kv_join_kernel(AttnArgs a) {
+  const int64_t seq = blockIdx.y, row = seq * a.heads + blockIdx.x;
+  const Span sp = find_span(a, seq);
+  if (sp.live <= 1) return;   // the attention kernel wrote the output
+  const float* ml = a.part_ml + 2 * row * a.splits;
+  float mx = -INFINITY;
+  for (int s = 0; s < sp.live; ++s) mx = fmaxf(mx, ml[2 * s]);
+  const int d = 4 * threadIdx.x;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int s = 0; s < sp.live; ++s) {
+    // a split without a score has l = 0 and o = 0 (or NaN, which passes on)
+    const float w = ml[2 * s] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[2 * s] - mx);
+    l += w * ml[2 * s + 1];
+    if (d < a.head_dim) o += *reinterpret_cast<const f32x4*>(a.part_o + (row * a.splits + s) * a.head_dim + d) * w;
+  }
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+  if (d < a.head_dim)
+    *reinterpret_cast<u32x2*>(a.out + row * a.head_dim + d) = u32x2{pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
+  if (a.lse && threadIdx.x == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+}
+
+template <int FMT>
+void launch_dim(const AttnArgs& a, dim3 grid, hipStream_t stream) {
+  if (a.head_dim == 64) kv_attention_kernel<FMT, 2><<<grid, 64 * kWaves, 0, stream>>>(a);
+  else if (a.head_dim == 128) kv_attention_kernel<FMT, 4><<<grid, 64 * kWaves, 0, stream>>>(a);
+  else kv_attention_kernel<FMT, 8><<<grid, 64 * kWaves, 0, stream>>>(a);
+}
+
+int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_heads + 15) / 16; }
+
+// Splits of the length: enough workgroups to fill the 256 CUs eight deep, at
+// least 128 tokens (a chunk per wave) each.
+int splits_of(int64_t seqs, int32_t heads, int32_t kv_heads, int64_t tokens) {
+  const int64_t rows = seqs * kv_heads * head_tiles_of(heads, kv_heads);
+  int64_t s = (2048 + rows - 1) / (rows > 0 ? rows : 1);
+  const int64_t most = (tokens + kWaves * kChunk - 1) / (kWaves * kChunk);
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+
+}  // namespace
+
+size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
+  const int64_t s = splits_of(seqs, heads, kv_heads, tokens);
+  return s <= 1 ? 0 : (size_t)(seqs * heads * s) * (size_t)(head_dim + 2) * sizeof(float);
+}
+
+void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {
+  a.head_tiles = (int32_t)head_tiles_of(a.heads, a.kv_heads);
+  a.splits = splits_of(a.seqs, a.heads, a.kv_heads, a.table_width << a.page_shift);
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = a.splits > 1 ? a.part_o + a.seqs * a.heads * a.splits * a.head_dim : nullptr;
+  const dim3 grid(a.splits, a.kv_heads * a.head_tiles, (unsigned)a.seqs);
+  if (a.format == W4_KV_BF16) launch_dim<W4_KV_BF16>(a, grid, stream);
+  else if (a.format == W4_KV_E4M3) launch_dim<W4_KV_E4M3>(a, grid, stream);
+  else launch_dim<W4_KV_Q4>(a, grid, stream);
+  if (a.splits > 1) kv_join_kernel<<<dim3(a.heads, (unsigned)a.seqs), 64, 0, stream>>>(a);
+}
+
+}  // namespace w4

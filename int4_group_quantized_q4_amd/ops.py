@@ -4,8 +4,9 @@ every computation runs in the library's HIP kernels on the given stream
 (default: torch's current stream).
 
 A few allocating helpers (``repack``, ``dequant``, ``pack_codes``,
-``linear``, ``moe_route``, ``moe_layer``) create the output tensors with
-torch and then make the same calls.
+``linear``, ``moe_route``, ``moe_layer``, ``add_rmsnorm``,
+``add_rmsnorm_quantize``, ``kv_cache``, ``kv_attention``) create the output
+tensors with torch and then make the same calls.
 """
 
 import contextlib
@@ -413,6 +414,151 @@ def w8a8_moe_layer(x, logits, k, I, w1q, w1_scale, w2q, w2_scale, activation, y,
     check(st, "w8a8_moe_layer")
 
 
+# ------------------------------------------------- around the matmuls
+def _call(name, device, stream, *args):
+    """One library call on `device` (the launch needs it current) and on
+    `stream` (default: that device's current stream)."""
+    fn = getattr(lib(), name)
+    with contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        st = fn(*args, _stream(stream))
+    check(st, name)
+
+
+def _check_norm(x, residual, weight, sum_out, d):
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, d], got %s" % (tuple(x.shape),))
+    n = x.shape[0] * d * 2
+    _need(residual, "residual", n, x.device)
+    _need(weight, "weight", d * 2, x.device)
+    _need(sum_out, "sum_out", n, x.device)
+    return (_ptr(x, "x", _BF16_LIKE), _ptr(residual, "residual", _BF16_LIKE, True), _ptr(weight, "weight", _BF16_LIKE))
+
+
+def w4a16_add_rmsnorm(x, residual, weight, eps, sum_out, y, weight_offset=0.0, stream=None):
+    """y = bf16(RMS norm of r = bf16(x + residual)); residual and sum_out (r)
+    may be None."""
+    d = x.shape[-1]
+    ptrs = _check_norm(x, residual, weight, sum_out, d)
+    _need(y, "y", x.shape[0] * d * 2, x.device)
+    _call("w4a16_add_rmsnorm", x.device, stream, *ptrs, x.shape[0], d, eps, weight_offset,
+          _ptr(sum_out, "sum_out", _BF16_LIKE, True), _ptr(y, "y", _BF16_LIKE))
+
+
+def w8a8_add_rmsnorm_quantize(x, residual, weight, eps, sum_out, q, scale, weight_offset=0.0, stream=None):
+    """The norm's rows as E4M3 codes q [rows, d] and fp32 row scales."""
+    d = x.shape[-1]
+    ptrs = _check_norm(x, residual, weight, sum_out, d)
+    _need(q, "q", x.shape[0] * d, x.device)
+    _need(scale, "scale", x.shape[0] * 4, x.device)
+    _call("w8a8_add_rmsnorm_quantize", x.device, stream, *ptrs, x.shape[0], d, eps, weight_offset,
+          _ptr(sum_out, "sum_out", _BF16_LIKE, True), _ptr(q, "q", (torch.uint8,)),
+          _ptr(scale, "scale", (torch.float32,)))
+
+
+def _rows(t, name, dtypes, like=None):
+    """Pointer and row stride (elements) of t [rows, heads, dim] whose rows are
+    contiguous; the rows themselves may be apart (slices of one projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must be [rows, heads, dim], got %s" % (name, tuple(t.shape)))
+    if like is not None and (t.shape != like.shape or t.device != like.device or t.dtype != like.dtype):
+        raise ValueError("%s is %s %s on %s, expected %s %s on %s" % (
+            name, tuple(t.shape), t.dtype, t.device, tuple(like.shape), like.dtype, like.device))
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    rows, heads, dim = t.shape
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError("%s: the heads of a row must be contiguous" % name)
+    if rows > 1 and t.stride(0) < heads * dim:
+        raise ValueError("%s: rows must not overlap" % name)
+    return t.data_ptr(), t.stride(0) if rows > 1 else heads * dim
+
+
+def _on_device(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+
+
+def kv_cache_page_bytes(format, page_size, kv_heads, head_dim):
+    """Bytes of one page; ValueError for sizes outside the limits."""
+    n = int(lib().kv_cache_page_bytes(format, page_size, kv_heads, head_dim))
+    if n == 0:
+        raise ValueError("no cache of format %s, page_size %s, kv_heads %s, head_dim %s"
+                         % (format, page_size, kv_heads, head_dim))
+    return n
+
+
+def _pages(cache, format, page_size, kv_heads, head_dim, device):
+    """Pointer and page count of a cache buffer."""
+    page = kv_cache_page_bytes(format, page_size, kv_heads, head_dim)
+    p = _ptr(cache, "cache", (torch.uint8,))
+    if cache.numel() % page:
+        raise ValueError("cache holds %d bytes, not a multiple of a page's %d" % (cache.numel(), page))
+    if cache.device != device:
+        raise ValueError("cache is on %s, expected %s" % (cache.device, device))
+    return p, cache.numel() // page
+
+
+def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=None):
+    """Quantize the rows k, v [tokens, kv_heads, head_dim] into their slots."""
+    tokens, heads, dim = k.shape
+    kp, ks = _rows(k, "k", _BF16_LIKE)
+    vp, vs = _rows(v, "v", _BF16_LIKE, k)
+    _on_device(k, "k")
+    d = k.device
+    _need(slots, "slots", tokens * 8, d)
+    _need(counters, "counters", 16, d)
+    cp, pages = _pages(cache, format, page_size, heads, dim, d)
+    _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs, _ptr(slots, "slots", (torch.int64,)), format, cp, pages,
+          page_size, heads, dim, _ptr(counters, "counters", (torch.int64,), True))
+
+
+def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=None):
+    """The rows of `slots` into k, v [tokens, kv_heads, head_dim] (bf16 or fp32)."""
+    tokens, heads, dim = k.shape
+    kp, ks = _rows(k, "k", (torch.float32,) + _BF16_LIKE)
+    vp, vs = _rows(v, "v", (torch.float32,) + _BF16_LIKE, k)
+    _on_device(k, "k")
+    d = k.device
+    _need(slots, "slots", tokens * 8, d)
+    _need(counters, "counters", 16, d)
+    cp, pages = _pages(cache, format, page_size, heads, dim, d)
+    _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim, _ptr(slots, "slots", (torch.int64,)),
+          tokens, kp, vp, ks, vs, W4_OUT_F32 if k.dtype == torch.float32 else W4_OUT_BF16,
+          _ptr(counters, "counters", (torch.int64,), True))
+
+
+def kv_cache_attention_workspace(seqs, heads, kv_heads, head_dim, table_width, page_size):
+    return int(lib().kv_cache_attention_workspace(seqs, heads, kv_heads, head_dim, table_width, page_size))
+
+
+def kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, out, window=0, lse=None,
+                       ws=None, counters=None, stream=None):
+    """One new token's attention per sequence: q [seqs, heads, head_dim] over
+    the cache rows that block_table [seqs, width] and seq_lens [seqs] name."""
+    seqs, heads, dim = q.shape
+    qp, qs = _rows(q, "q", _BF16_LIKE)
+    _on_device(q, "q")
+    d = q.device
+    if block_table.dim() != 2 or block_table.shape[0] != seqs:
+        raise ValueError("block_table must be [seqs=%d, width], got %s" % (seqs, tuple(block_table.shape)))
+    _need(block_table, "block_table", 0, d)
+    _need(seq_lens, "seq_lens", seqs * 4, d)
+    _need(out, "out", seqs * heads * dim * 2, d)
+    _need(lse, "lse", seqs * heads * 4, d)
+    _need(counters, "counters", 16, d)
+    _need(ws, "ws", 0, d)
+    cp, pages = _pages(cache, format, page_size, kv_heads, dim, d)
+    wp, wn = _ws(ws)
+    _call("kv_cache_attention", d, stream, qp, seqs, qs, heads, cp, format, pages, page_size, kv_heads, dim,
+          _ptr(block_table, "block_table", (torch.int32,)), block_table.shape[1],
+          _ptr(seq_lens, "seq_lens", (torch.int32,)), scale, window, _ptr(out, "out", _BF16_LIKE),
+          _ptr(lse, "lse", (torch.float32,), True), _ptr(counters, "counters", (torch.int64,), True), wp, wn)
+
+
 # -------------------------------------------------------- allocating helpers
 def repack(w, stream=None):
     """bf16 [rows, K] -> (qweight uint8 [rows*K/2], scales bf16 [rows*K/32]
@@ -537,3 +683,38 @@ def fp8_moe_layer(x, logits, k, I, w1q, w1_scale, w2q, w2_scale, activation=W4_E
         "o": view(12, R * d, torch.float32).view(R, d),
     }
     return y, views
+
+
+def add_rmsnorm(x, residual, weight, eps, weight_offset=0.0, stream=None):
+    """(y, r): the norm and, with a residual, the sum it was taken of (else x)."""
+    y = torch.empty_like(x)
+    r = torch.empty_like(x) if residual is not None else None
+    w4a16_add_rmsnorm(x, residual, weight, eps, r, y, weight_offset, stream)
+    return y, x if r is None else r
+
+
+def add_rmsnorm_quantize(x, residual, weight, eps, weight_offset=0.0, stream=None):
+    """(q, scale, r): as add_rmsnorm, with E4M3 codes and row scales."""
+    q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    r = torch.empty_like(x) if residual is not None else None
+    w8a8_add_rmsnorm_quantize(x, residual, weight, eps, r, q, scale, weight_offset, stream)
+    return q, scale, x if r is None else r
+
+
+def kv_cache(n_pages, format, page_size, kv_heads, head_dim, device="cuda"):
+    """An empty cache buffer, uint8 [n_pages, page bytes]."""
+    return torch.zeros(n_pages, kv_cache_page_bytes(format, page_size, kv_heads, head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def kv_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, window=0, stream=None):
+    """kv_cache_attention with freshly allocated outputs; returns (out, lse)."""
+    seqs, heads, dim = q.shape
+    out = torch.empty(seqs, heads, dim, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(seqs, heads, dtype=torch.float32, device=q.device)
+    need = kv_cache_attention_workspace(seqs, heads, kv_heads, dim, block_table.shape[1], page_size)
+    ws = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+    kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, out, window, lse, ws,
+                       stream=stream)
+    return out, lse
