@@ -39,6 +39,10 @@ COMMON_FLAGS = [
 ]
 
 
+# the attention kernel rescales its accumulators with vector instructions:
+# kept in VGPRs, they need no copies from and to accumulation registers
+FILE_FLAGS = {"kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+
 PROBE = os.path.join(HERE, "probe")
 PROBE_LIB = os.path.join(HERE, "libw4probe.so")
 
@@ -65,7 +69,7 @@ def build_probe(verbose=True):
 
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
-    cmd = [HIPCC] + COMMON_FLAGS + ["-c", src, "-o", obj]
+    cmd = [HIPCC] + COMMON_FLAGS + FILE_FLAGS.get(os.path.basename(src), []) + ["-c", src, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), res.stderr))

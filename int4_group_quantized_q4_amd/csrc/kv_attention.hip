@@ -39,6 +39,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kChunk = 32;          // tokens per wave step
+constexpr float kSlack = 8.0f;       // of the softmax's running reference, in powers of two
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -106,7 +107,7 @@ __device__ __forceinline__ Span find_span(const AttnArgs& a, int64_t seq) {
 }
 
 template <int FMT, int NG>
-__global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NG == 2 ? 4 : NG == 4 ? (FMT == W4_KV_E4M3 ? 3 : 2) : FMT == W4_KV_E4M3 ? 2 : 1))) kv_attention_kernel(AttnArgs a) {
   typedef KvLayout<FMT, NG> L;
   constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
   __shared__ float s_o[kWaves][16][BD + 4];
@@ -163,68 +164,76 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
   const int64_t begin = sp.first + split * sp.per;
   const int64_t end = begin + sp.per < sp.first + sp.chunks ? begin + sp.per : sp.first + sp.chunks;
   const int tile_shift = a.page_shift - 4;
-  for (int64_t ch = begin + wv; ch < end; ch += kWaves) {
-    // the two tiles' places; a tile past the table is masked as a whole below
-    const uint8_t* kp[2];
-    bool good[2];
+  const int64_t scale_off = ((int64_t)L::kTileBytes << a.page_shift) / kKvTile;
+
+  // The sequence's page ids, 64 table entries at a time, one per lane: a
+  // chunk's ids are lane reads, with no load in front of the cache's loads.
+  int64_t ids0 = 0;
+  int ids = -1;
+  auto fill_ids = [&](int64_t first) {
+    ids0 = first;
+    ids = -1;
+    if (first + lane < a.table_width) {
+      const int id = a.table[seq * a.table_width + first + lane];
+      if (id >= 0 && id < a.n_pages) ids = id;
+    }
+  };
+
+  // One chunk's K and V (codes and scales of its two tiles).  Each is reloaded
+  // as soon as its registers are free: K for the next chunk after this chunk's
+  // scores, V after its products, so one of the two is always on its way.
+  constexpr int NS = FMT == W4_KV_BF16 ? 0 : FMT == W4_KV_E4M3 ? 1 : NG / 2;   // 16-byte scale loads per tile
+  u32x4 kr[2][L::NU], vr[2][L::NU];
+  u32x4 ksr[2][NS > 0 ? NS : 1], vsr[2][NS > 0 ? NS : 1];
+  const uint8_t* next_p[2];   // K tiles (their page and head block) of the chunk that is loaded next
+  int next_tip[2];
+  bool good[2], next_good[2];
+  auto load_block = [&](bool v, u32x4 (&r)[2][L::NU], u32x4 (&sr)[2][NS > 0 ? NS : 1]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t tile = 2 * ch + t;
-      const int64_t pi = tile >> tile_shift;
-      const int64_t id = pi < a.table_width ? (int64_t)a.table[seq * a.table_width + pi] : -1;
-      good[t] = id >= 0 && id < a.n_pages;
-      kp[t] = a.cache + (good[t] ? id : 0) * a.page_bytes + (int64_t)head * 2 * a.block_bytes;
-    }
-    int tip[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) tip[t] = (int)((2 * ch + t) & ((1 << tile_shift) - 1));
-    const int64_t scale_off = ((int64_t)L::kTileBytes << a.page_shift) / kKvTile;
-
-    u32x4 kr[2][L::NU], vr[2][L::NU];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
+      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0);
 #pragma unroll
       for (int u = 0; u < L::NU; ++u) {
-        const int off = tip[t] * L::kTileBytes + (u * 64 + lane) * L::kUnitBytes;
+        const int off = next_tip[t] * L::kTileBytes + (u * 64 + lane) * L::kUnitBytes;
         if constexpr (L::kUnitBytes == 16) {
-          kr[t][u] = load16(kp[t] + off);
-          vr[t][u] = load16(kp[t] + a.block_bytes + off);
+          r[t][u] = load16(p + off);
         } else {
-          const u32x2 k2 = *reinterpret_cast<const u32x2*>(kp[t] + off);
-          const u32x2 v2 = *reinterpret_cast<const u32x2*>(kp[t] + a.block_bytes + off);
-          kr[t][u] = u32x4{k2[0], k2[1], 0u, 0u};
-          vr[t][u] = u32x4{v2[0], v2[1], 0u, 0u};
+          const u32x2 h = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + off));
+          r[t][u] = u32x4{h[0], h[1], 0u, 0u};
         }
       }
-    // scales of tokens 4c .. 4c+3: one (E4M3) or NG (Q4) for each token
-    constexpr int NS = FMT == W4_KV_BF16 ? 1 : FMT == W4_KV_E4M3 ? 1 : NG;
-    float ks[2][NS][4], vs[2][NS][4];
+      // scales of tokens 4c .. 4c+3: fp32 [j] (E4M3), bf16 [g][j] (Q4)
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        sr[t][i] = *reinterpret_cast<const u32x4*>(p + scale_off + next_tip[t] * L::kScaleTileBytes + 16 * (c * NS + i));
+    }
+  };
+  auto load_k = [&](int64_t ch) {
+    // a tile past the table or in a page outside the cache reads page 0 and is
+    // masked as a whole
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if constexpr (FMT == W4_KV_E4M3) {
-        const f32x4 k4 = *reinterpret_cast<const f32x4*>(kp[t] + scale_off + tip[t] * 64 + 16 * c);
-        const f32x4 v4 = *reinterpret_cast<const f32x4*>(kp[t] + a.block_bytes + scale_off + tip[t] * 64 + 16 * c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ks[t][0][j] = k4[j];
-          vs[t][0][j] = v4[j];
-        }
-      } else if constexpr (FMT == W4_KV_Q4) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int so = tip[t] * 32 * NG + (c * NG + g) * 8;
-          const u32x2 k2 = *reinterpret_cast<const u32x2*>(kp[t] + scale_off + so);
-          const u32x2 v2 = *reinterpret_cast<const u32x2*>(kp[t] + a.block_bytes + scale_off + so);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ks[t][g][j] = (j & 1) ? __uint_as_float(k2[j >> 1] & 0xFFFF0000u) : bf16_to_f32(k2[j >> 1] & 0xFFFFu);
-            vs[t][g][j] = (j & 1) ? __uint_as_float(v2[j >> 1] & 0xFFFF0000u) : bf16_to_f32(v2[j >> 1] & 0xFFFFu);
-          }
-        }
-      }
+      const int64_t pi = (2 * ch + t) >> tile_shift;
+      if (pi - ids0 >= 64) fill_ids(pi);
+      const int id = __builtin_amdgcn_readlane(ids, (int)(pi - ids0));
+      next_good[t] = id >= 0;
+      next_p[t] = a.cache + (int64_t)(id >= 0 ? id : 0) * a.page_bytes + (int64_t)head * 2 * a.block_bytes;
+      next_tip[t] = (int)((2 * ch + t) & ((1 << tile_shift) - 1));
     }
+    load_block(false, kr, ksr);
+  };
+  auto load_v = [&]() { load_block(true, vr, vsr); };
+  // scale i of a tile's 16-byte pieces: token j (E4M3) or group g, token j (Q4)
+  auto scale_of = [&](const u32x4 (&sr)[NS > 0 ? NS : 1], int g, int j) {
+    if constexpr (FMT == W4_KV_E4M3) return __uint_as_float(sr[0][j]);
+    const uint32_t w = sr[NS > 0 ? g >> 1 : 0][2 * (g & 1) + (j >> 1)];
+    return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
+  };
 
-    // scores
+  // One chunk; `more`: load the wave's next one meanwhile.
+  auto step = [&](int64_t ch, bool more) {
+    good[0] = next_good[0];
+    good[1] = next_good[1];
     float p[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -232,6 +241,7 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int u = g / L::U, part = g % L::U;
+        if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
         if constexpr (FMT == W4_KV_BF16) {
           s4 = mfma(kr[t][u], q[g], s4);
         } else if constexpr (FMT == W4_KV_E4M3) {
@@ -240,15 +250,18 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
         } else {
           const f32x4 d = mfma(biased_pairs(kr[t][u][part]), q[g], f32x4{kbias[g], kbias[g], kbias[g], kbias[g]});
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s4[j] = fmaf(ks[t][g][j], d[j], s4[j]);
+          for (int j = 0; j < 4; ++j) s4[j] = fmaf(scale_of(ksr[t], g, j), d[j], s4[j]);
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[4 * t + j] = s4[j] * (FMT == W4_KV_E4M3 ? scale2 * ks[t][0][j] : scale2);
+      for (int j = 0; j < 4; ++j)
+        p[4 * t + j] = s4[j] * (FMT == W4_KV_E4M3 ? scale2 * scale_of(ksr[t], 0, j) : scale2);
     }
+    __builtin_amdgcn_sched_barrier(0);   // not before the scores: K's registers are reused
+    load_k(ch + kWaves < end ? ch + kWaves : ch);
 
-    // Positions outside the span or in pages outside the cache: no score, and
-    // what their V rows hold (anything) is cleared, since 0 * NaN is NaN.
+    // Positions outside the span or in pages outside the cache have no score,
+    // and what their V rows hold (anything) is cleared, since 0 * NaN is NaN.
     if (ch * kChunk < sp.lo || (ch + 1) * kChunk > sp.n || !good[0] || !good[1]) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -257,17 +270,13 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
         for (int j = 0; j < 4; ++j) {
           const int64_t pos = ch * kChunk + 16 * t + 4 * c + j;
           const bool in = good[t] && pos >= sp.lo && pos < sp.n;
-          if (!in) {
-            p[4 * t + j] = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < NS; ++g) vs[t][g][j] = 0.f;
-          }
+          if (!in) p[4 * t + j] = -INFINITY;
           keep |= in ? 0xFFu << (8 * j) : 0u;
         }
         // byte masks widened to the words that hold (tokens 0 and 1) and (2 and 3)
         const uint32_t k01 = ((keep & 0xFFu) | ((keep & 0xFF00u) << 8)) * 0x101u;
         const uint32_t k23 = (((keep >> 16) & 0xFFu) | ((keep >> 24) << 16)) * 0x101u;
-        // operands are indexed by row (dimension) here: lane (c, m) holds tokens 4c + j too
+        // an operand's lane (c, m) holds tokens 4c + j, as the scores' lane (c, n) does
 #pragma unroll
         for (int u = 0; u < L::NU; ++u) {
           if constexpr (FMT == W4_KV_BF16) {
@@ -280,46 +289,62 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
             for (int i = 0; i < 4; ++i) vr[t][u][i] &= keep;
           }
         }
+        if constexpr (FMT == W4_KV_E4M3) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((keep >> (8 * j)) & 1u)) vsr[t][0][j] = 0u;
+        } else if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vsr[t][i][w] &= (w & 1) ? k23 : k01;
+        }
       }
     }
 
-    // softmax: running maximum (base-2 exponents) and this lane's sum
+    // Softmax against a running reference: any reference gives the same
+    // result, so it follows the maximum only when that has grown by more than
+    // 2^kSlack, and the outputs are rarely rescaled.
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
     top = column_max(top);
-    const float m_new = fmaxf(m_run, top);
-    const float m_use = m_new == -INFINITY ? 0.f : m_new;   // nothing yet: every p is 0
-    const float alpha = __builtin_amdgcn_exp2f(m_run - m_use);
-    m_run = m_new;
+    if (__any(top > m_run + kSlack)) {
+      const float m_new = fmaxf(m_run, top);
+      const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_run - m_new);
+      m_run = m_new;
+      l_run *= alpha;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[g][b] *= alpha;
+      if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) vbias[g] *= alpha;
+      }
+    }
+    const float m_use = m_run == -INFINITY ? 0.f : m_run;   // nothing yet: every p is 0
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       p[i] = __builtin_amdgcn_exp2f(p[i] - m_use);
       sum += p[i];
     }
-    l_run = l_run * alpha + sum;
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) acc[g][b] *= alpha;
-    if constexpr (FMT == W4_KV_Q4) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) vbias[g] *= alpha;
-    }
+    l_run += sum;
 
     // O^T += V^T . P^T
     u32x4 hi, lo;
     if constexpr (FMT != W4_KV_Q4) {
       if constexpr (FMT == W4_KV_E4M3) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] *= vs[i >> 2][0][i & 3];
+        for (int i = 0; i < 8; ++i) p[i] *= scale_of(vsr[i >> 2], 0, i & 3);
       }
       split_bf16(p, hi, lo);
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const int u = g / L::U, part = g % L::U;
+      if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
       if constexpr (FMT == W4_KV_BF16) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -338,7 +363,7 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
       } else {
         float ps[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ps[i] = p[i] * vs[i >> 2][g][i & 3];
+        for (int i = 0; i < 8; ++i) ps[i] = p[i] * scale_of(vsr[i >> 2], g, i & 3);
         split_bf16(ps, hi, lo);
         const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
         vbias[g] = mfma(bias, hi, vbias[g]);
@@ -358,6 +383,16 @@ __global__ void __launch_bounds__(64 * kWaves) kv_attention_kernel(AttnArgs a) {
         }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_v();
+  };
+
+  int64_t ch = begin + wv;
+  if (ch < end) {
+    fill_ids((2 * ch) >> tile_shift);
+    load_k(ch);
+    load_v();
+    for (; ch < end; ch += kWaves) step(ch, true);
   }
 
   if constexpr (FMT == W4_KV_Q4) {
