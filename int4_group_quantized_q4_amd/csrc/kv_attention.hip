@@ -60,12 +60,13 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// 8 fp32 values -> bf16 high and low parts
+// 8 fp32 values -> bf16 high (truncated) and low parts
 __device__ __forceinline__ void split_bf16(const float p[8], u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    hi[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
-    lo[i] = pk_bf16(p[2 * i] - bf16_to_f32(hi[i] & 0xFFFFu), p[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+    const uint32_t a = __float_as_uint(p[2 * i]), b = __float_as_uint(p[2 * i + 1]);
+    hi[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // the upper halves
+    lo[i] = pk_bf16(p[2 * i] - __uint_as_float(a & 0xFFFF0000u), p[2 * i + 1] - __uint_as_float(b & 0xFFFF0000u));
   }
 }
 
@@ -86,23 +87,23 @@ __device__ __forceinline__ float column_sum(float v) {
 // The positions a sequence attends to, in 32-token chunks, and how they are
 // dealt to the splits (the same for the attention and the join kernel).
 struct Span {
-  int64_t n, lo;          // positions [lo, n)
-  int64_t first, chunks;  // chunk range
-  int64_t per;            // chunks per split
-  int live;               // splits that have any
+  int n, lo;          // positions [lo, n); all positions fit 31 bits
+  int first, chunks;  // chunk range
+  int per;            // chunks per split
+  int live;           // splits that have any
 };
 
-__device__ __forceinline__ Span find_span(const AttnArgs& a, int64_t seq) {
+__device__ __forceinline__ Span find_span(const AttnArgs& a, int seq) {
   Span s;
-  s.n = a.lens[seq];
-  const int64_t most = a.table_width << a.page_shift;
-  s.n = s.n < 0 ? 0 : s.n > most ? most : s.n;
+  const int most = (int)a.table_width << a.page_shift;
+  const int len = a.lens[seq];
+  s.n = len < 0 ? 0 : len > most ? most : len;
   s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
   s.first = s.lo / kChunk;
   s.chunks = (s.n + kChunk - 1) / kChunk - s.first;
-  s.per = (s.chunks + a.splits - 1) / a.splits;
+  s.per = (int)((unsigned)(s.chunks + a.splits - 1) / (unsigned)a.splits);
   if (s.per < kWaves) s.per = kWaves;
-  s.live = s.chunks > 0 ? (int)((s.chunks + s.per - 1) / s.per) : 0;
+  s.live = s.chunks > 0 ? (int)((unsigned)(s.chunks + s.per - 1) / (unsigned)s.per) : 0;
   return s;
 }
 
@@ -116,16 +117,18 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, c = lane >> 4;
   const int split = blockIdx.x;
-  const int head = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
-  const int64_t seq = blockIdx.z;
-  const int G = a.heads / a.kv_heads;
+  const int head = (int)(blockIdx.y / (unsigned)a.head_tiles), ht = (int)blockIdx.y - head * a.head_tiles;
+  const int seq = blockIdx.z;
+  const int G = (int)((unsigned)a.heads / (unsigned)a.kv_heads);
   const int live_heads = G - 16 * ht < 16 ? G - 16 * ht : 16;
-  const int64_t h0 = (int64_t)head * G + 16 * ht;     // first query head
+  const int h0 = head * G + 16 * ht;     // first query head
+  const int32_t* table = a.table + (int64_t)seq * a.table_width;
+  const int width = (int)a.table_width;
   const Span sp = find_span(a, seq);
   if (a.counters && split == 0 && blockIdx.y == 0) {  // table entries outside the cache, once per entry
-    const int64_t p1 = (sp.n + (1 << a.page_shift) - 1) >> a.page_shift;
-    for (int64_t p = (sp.lo >> a.page_shift) + threadIdx.x; p < p1; p += 64 * kWaves) {
-      const int64_t id = a.table[seq * a.table_width + p];
+    const int p1 = (int)(((unsigned)sp.n + (1u << a.page_shift) - 1) >> a.page_shift);
+    for (int p = (sp.lo >> a.page_shift) + (int)threadIdx.x; p < p1; p += 64 * kWaves) {
+      const int id = table[p];
       if (id < 0 || id >= a.n_pages) atomicAdd(a.counters, 1ull);
     }
   }
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   for (int g = 0; g < NG; ++g) {
     q[g] = u32x4{0u, 0u, 0u, 0u};
     if (n16 < live_heads)
-      q[g] = *reinterpret_cast<const u32x4*>(a.q + seq * a.q_stride + (h0 + n16) * L::D + 32 * g + 8 * c);
+      q[g] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + n16) * L::D + 32 * g + 8 * c);
   }
   // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
   float kbias[NG];
@@ -161,20 +164,20 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's tokens only
   const float scale2 = a.scale * kLog2e;
 
-  const int64_t begin = sp.first + split * sp.per;
-  const int64_t end = begin + sp.per < sp.first + sp.chunks ? begin + sp.per : sp.first + sp.chunks;
+  const int begin = sp.first + split * sp.per;
+  const int end = begin + sp.per < sp.first + sp.chunks ? begin + sp.per : sp.first + sp.chunks;
   const int tile_shift = a.page_shift - 4;
-  const int64_t scale_off = ((int64_t)L::kTileBytes << a.page_shift) / kKvTile;
+  const uint32_t scale_off = ((uint32_t)L::kTileBytes << a.page_shift) / kKvTile;
 
   // The sequence's page ids, 64 table entries at a time, one per lane: a
   // chunk's ids are lane reads, with no load in front of the cache's loads.
-  int64_t ids0 = 0;
+  int ids0 = 0;
   int ids = -1;
-  auto fill_ids = [&](int64_t first) {
+  auto fill_ids = [&](int first) {
     ids0 = first;
     ids = -1;
-    if (first + lane < a.table_width) {
-      const int id = a.table[seq * a.table_width + first + lane];
+    if (first + lane < width) {
+      const int id = table[first + lane];
       if (id >= 0 && id < a.n_pages) ids = id;
     }
   };
@@ -191,10 +194,12 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   auto load_block = [&](bool v, u32x4 (&r)[2][L::NU], u32x4 (&sr)[2][NS > 0 ? NS : 1]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0);
+      // a uniform base and a 32-bit lane offset
+      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + (uint32_t)next_tip[t] * (uint32_t)L::kTileBytes;
+      const uint8_t* ps = next_p[t] + (v ? a.block_bytes : 0) + scale_off + (uint32_t)next_tip[t] * (uint32_t)L::kScaleTileBytes;
 #pragma unroll
       for (int u = 0; u < L::NU; ++u) {
-        const int off = next_tip[t] * L::kTileBytes + (u * 64 + lane) * L::kUnitBytes;
+        const uint32_t off = (uint32_t)(u * 64 + lane) * L::kUnitBytes;
         if constexpr (L::kUnitBytes == 16) {
           r[t][u] = load16(p + off);
         } else {
@@ -205,20 +210,20 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
       // scales of tokens 4c .. 4c+3: fp32 [j] (E4M3), bf16 [g][j] (Q4)
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        sr[t][i] = *reinterpret_cast<const u32x4*>(p + scale_off + next_tip[t] * L::kScaleTileBytes + 16 * (c * NS + i));
+        sr[t][i] = *reinterpret_cast<const u32x4*>(ps + (uint32_t)(16 * (c * NS + i)));
     }
   };
-  auto load_k = [&](int64_t ch) {
+  auto load_k = [&](int ch) {
     // a tile past the table or in a page outside the cache reads page 0 and is
     // masked as a whole
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t pi = (2 * ch + t) >> tile_shift;
+      const int pi = (2 * ch + t) >> tile_shift;
       if (pi - ids0 >= 64) fill_ids(pi);
-      const int id = __builtin_amdgcn_readlane(ids, (int)(pi - ids0));
+      const int id = __builtin_amdgcn_readlane(ids, pi - ids0);
       next_good[t] = id >= 0;
       next_p[t] = a.cache + (int64_t)(id >= 0 ? id : 0) * a.page_bytes + (int64_t)head * 2 * a.block_bytes;
-      next_tip[t] = (int)((2 * ch + t) & ((1 << tile_shift) - 1));
+      next_tip[t] = (2 * ch + t) & ((1 << tile_shift) - 1);
     }
     load_block(false, kr, ksr);
   };
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   };
 
   // One chunk; `more`: load the wave's next one meanwhile.
-  auto step = [&](int64_t ch, bool more) {
+  auto step = [&](int ch, bool more) {
     good[0] = next_good[0];
     good[1] = next_good[1];
     float p[8];
@@ -262,13 +267,15 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 
     // Positions outside the span or in pages outside the cache have no score,
     // and what their V rows hold (anything) is cleared, since 0 * NaN is NaN.
-    if (ch * kChunk < sp.lo || (ch + 1) * kChunk > sp.n || !good[0] || !good[1]) {
+    if (ch * kChunk < sp.lo || ch * kChunk > sp.n - kChunk || !good[0] || !good[1]) {
+      int rel = ch * kChunk + 4 * c;
+      asm volatile("" : "+v"(rel));   // keeps the positions' arithmetic inside this branch
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         uint32_t keep = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t pos = ch * kChunk + 16 * t + 4 * c + j;
+          const int pos = rel + 16 * t + j;
           const bool in = good[t] && pos >= sp.lo && pos < sp.n;
           if (!in) p[4 * t + j] = -INFINITY;
           keep |= in ? 0xFFu << (8 * j) : 0u;
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     if (more) load_v();
   };
 
-  int64_t ch = begin + wv;
+  int ch = begin + wv;
   if (ch < end) {
     fill_ids((2 * ch) >> tile_shift);
     load_k(ch);
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
         l += s_m[w][h] == -INFINITY ? s_l[w][h] : s_l[w][h] * __builtin_amdgcn_exp2f(s_m[w][h] - mx);
         o += *reinterpret_cast<const f32x4*>(&s_o[w][h][d]);
       }
-      const int64_t row = seq * a.heads + h0 + h;
+      const int64_t row = (int64_t)seq * a.heads + h0 + h;
       const int dim = rd * BD + d;
       if (sp.live <= 1) {
         const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // l: 0 for an empty row, NaN passes on
@@ -462,8 +469,8 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 // Joins the splits of one (sequence, query head): 4 dimensions per thread,
 // split order, fp32.
 __global__ void __launch_bounds__(64) kv_join_kernel(AttnArgs a) {
-  const int64_t seq = blockIdx.y, row = seq * a.heads + blockIdx.x;
-  const Span sp = find_span(a, seq);
+  const int64_t row = (int64_t)blockIdx.y * a.heads + blockIdx.x;
+  const Span sp = find_span(a, blockIdx.y);
   if (sp.live <= 1) return;   // the attention kernel wrote the output
   const float* ml = a.part_ml + 2 * row * a.splits;
   float mx = -INFINITY;

@@ -10,7 +10,10 @@ summed): with A = sum_t p_t |v'_t| (v' the value the matrix core multiplies:
             rounded to fp32 twice) and 2^-22 for the exponential; the running
             maximum cancels;
   p . v     p * s in two bf16 terms (2^-16), n + 40 fp32 additions (chunks,
-            waves, splits): 2^-16 + (n + 40) 2^-23, over A;
+            waves, splits): 2^-16 + (n + 40) 2^-23, over A; Q4's p and p * s
+            are rounded to fp16 (2^-11 each) instead, which the codes' offset
+            shares exactly, so over sum_t p_t |v_t|, plus 2^-35 of the largest
+            |v| for each position (p below fp16's smallest step);
   division  the sum l has the same relative errors as p;
   out       half a bf16 step, 2^-8.
 lse = m + log l: l's relative error plus 2^-22 (|lse| + |m|)."""
@@ -107,7 +110,11 @@ class Setup:
                 ep = np.max((self.D + 8) * 2.0 ** -23 * S + 2.0 ** -22 * np.abs(s[h])) + 2.0 ** -22
                 el = ep + (n + 40) * 2.0 ** -23
                 A = p[h] @ vm[:, h // self.group]
-                bound = 2.0 ** -8 * np.abs(ref[h]) + (el + ep + 2.0 ** -16 + (n + 40) * 2.0 ** -23) * A * 1.01
+                fp16 = 0.0
+                if self.form == "q4":
+                    av = np.abs(v[:, h // self.group])
+                    fp16 = 2.0 ** -10 * (p[h] @ av) + 2.0 ** -35 * n * np.max(av)
+                bound = fp16 + 2.0 ** -8 * np.abs(ref[h]) + (el + ep + 2.0 ** -16 + (n + 40) * 2.0 ** -23) * A * 1.01
                 assert (np.abs(o[i, h] - ref[h]) <= bound).all(), (i, h, np.max(np.abs(o[i, h] - ref[h]) / bound))
                 lb = 1.01 * el + 2.0 ** -22 * (abs(rlse[h]) + np.max(np.abs(s[h])) + 1)
                 assert abs(l[i, h] - rlse[h]) <= lb, (i, h, l[i, h], rlse[h], lb)
@@ -224,6 +231,28 @@ def test_poisoned_rows_pass_on(form):
         else:
             assert nan[:, :32].all() and not nan[:, 32:].any()
         assert which == 0 or torch.isfinite(lse).all()
+
+
+def test_q4_scales_far_apart():
+    """V scales that grow, shrink and vanish by many powers of two along a sequence and inside a chunk: beyond the range
+    that the fp16 product covers, up to rows that outweigh all others by 2^60."""
+    for seed, draw in enumerate((lambda r, n: r.integers(-3, 4, n), lambda r, n: r.integers(-20, 20, n),
+                                 lambda r, n: np.arange(n) // 8 - 20, lambda r, n: 20 - np.arange(n) // 4,
+                                 lambda r, n: np.where(r.random(n) < 0.02, 60, r.integers(-60, 0, n)))):
+        s = Setup("q4", [600, 33], 1, 4, 64, 16, seed=20 + seed)
+        rng = np.random.default_rng(seed)
+        codes, scales = s.v
+        f = oracle.bf16_bits_to_f64(scales).copy()
+        f[np.isnan(f)] = 1.0
+        for i, n in enumerate(s.lens):
+            pos = np.arange(n)
+            f[s.table[i, pos // 16], 0, pos % 16] *= 2.0 ** draw(rng, int(n))[:, None]
+            zero = pos[rng.random(int(n)) < 0.1]
+            f[s.table[i, zero // 16], 0, zero % 16] = 0.0
+            codes[s.table[i, zero // 16], 0, zero % 16] = 0
+        s.v = (codes, oracle.bf16_from_f64(f))
+        s.cache = to_dev(kv_layout.encode_cache(s.k, s.v, "q4"))
+        s.check(*s.run())
 
 
 def test_large_scores():
