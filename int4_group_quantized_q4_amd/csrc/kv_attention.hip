@@ -466,28 +466,67 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   }
 }
 
-// Joins the splits of one (sequence, query head): 4 dimensions per thread,
-// split order, fp32.
-__global__ void __launch_bounds__(64) kv_join_kernel(AttnArgs a) {
+// Joins the splits of one (sequence, query head): D/4 threads take 4 dimensions
+// each of one split, the workgroup's 1024/D such groups take splits in turn
+// and are added in LDS, in group order (fp32; the order depends on the split
+// count alone).  Bound by latency: lengths, then maxima and sums, then the
+// outputs, each level's loads in flight together.
+template <int NG>
+__global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
+  constexpr int D = 32 * NG, TG = D / 4, GROUPS = 256 / TG;
+  __shared__ f32x4 s_o[GROUPS][TG];
+  const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.y * a.heads + blockIdx.x;
+  const float* ml = a.part_ml + 2 * row * a.splits;
+  // every wave reduces all (m, l) pairs; the first 64 splits' are loaded
+  // before the length is known
+  float m0 = -INFINITY, l0 = 0.f;
+  if (lane < a.splits) {
+    m0 = ml[2 * lane];
+    l0 = ml[2 * lane + 1];
+  }
   const Span sp = find_span(a, blockIdx.y);
   if (sp.live <= 1) return;   // the attention kernel wrote the output
-  const float* ml = a.part_ml + 2 * row * a.splits;
-  float mx = -INFINITY;
-  for (int s = 0; s < sp.live; ++s) mx = fmaxf(mx, ml[2 * s]);
-  const int d = 4 * threadIdx.x;
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int s = 0; s < sp.live; ++s) {
-    // a split without a score has l = 0 and o = 0 (or NaN, which passes on)
-    const float w = ml[2 * s] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[2 * s] - mx);
-    l += w * ml[2 * s + 1];
-    if (d < a.head_dim) o += *reinterpret_cast<const f32x4*>(a.part_o + (row * a.splits + s) * a.head_dim + d) * w;
+  if (lane >= sp.live) {      // not written
+    m0 = -INFINITY;
+    l0 = 0.f;
   }
+  float mx = m0;
+  for (int s = lane + 64; s < sp.live; s += 64) mx = fmaxf(mx, ml[2 * s]);
+  mx = wave_max_all(mx);
+  // a split without a score has l = 0 and o = 0 (or NaN, which passes on)
+  auto weight = [&](float m) { return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx); };
+  float l = l0 * weight(m0);
+  for (int s = lane + 64; s < sp.live; s += 64) l += ml[2 * s + 1] * weight(ml[2 * s]);
+  l = wave_sum_all(l);
+
+  const int grp = threadIdx.x / TG, d = threadIdx.x % TG;
+  const f32x4* po = reinterpret_cast<const f32x4*>(a.part_o + row * a.splits * D) + d;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int s = grp; s < sp.live; s += 4 * GROUPS) {
+    f32x4 v[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = s + i * GROUPS;
+      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      w[i] = 0.f;
+      if (k < sp.live) {
+        v[i] = po[(int64_t)k * TG];
+        w[i] = weight(ml[2 * k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o += v[i] * w[i];
+  }
+  s_o[grp][d] = o;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) o += s_o[i][d];
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-  if (d < a.head_dim)
-    *reinterpret_cast<u32x2*>(a.out + row * a.head_dim + d) = u32x2{pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
-  if (a.lse && threadIdx.x == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  *reinterpret_cast<u32x2*>(a.out + row * D + 4 * d) = u32x2{pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
+  if (a.lse && d == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
 }
 
 template <int FMT>
@@ -525,7 +564,12 @@ void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {
   if (a.format == W4_KV_BF16) launch_dim<W4_KV_BF16>(a, grid, stream);
   else if (a.format == W4_KV_E4M3) launch_dim<W4_KV_E4M3>(a, grid, stream);
   else launch_dim<W4_KV_Q4>(a, grid, stream);
-  if (a.splits > 1) kv_join_kernel<<<dim3(a.heads, (unsigned)a.seqs), 64, 0, stream>>>(a);
+  if (a.splits > 1) {
+    const dim3 rows(a.heads, (unsigned)a.seqs);
+    if (a.head_dim == 64) kv_join_kernel<2><<<rows, 256, 0, stream>>>(a);
+    else if (a.head_dim == 128) kv_join_kernel<4><<<rows, 256, 0, stream>>>(a);
+    else kv_join_kernel<8><<<rows, 256, 0, stream>>>(a);
+  }
 }
 
 }  // namespace w4
