@@ -21,6 +21,13 @@
 // tile, j), and the cache keeps V so that one lane's load holds those tokens
 // of dimension 32g + 2n + b: no value crosses lanes between the two products.
 //
+// Q4's scales differ from group to group, and applying them is what its
+// vector instructions would go into.  With at most 8 (4) heads the 16 columns
+// hold R = 2 (4) replicas of each head, and replica r does the scale
+// arithmetic of the r-th part of the groups: its q is zero in the others, its
+// part of the scores is summed over the replicas by lane rotations, and of
+// the second product a group's rows count in its own replica's columns only.
+//
 // Precision: q and the codes are exact in bf16 and all sums are fp32.  The
 // probabilities (times the V scales) enter the second product as two bf16
 // terms, high and low, so they carry 16 bits and the output's only visible
@@ -37,6 +44,10 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
+#ifndef W4_KV_SHARED
+#define W4_KV_SHARED(FMT, NG) ((NG) == 8)
+#define W4_KV_EU(FMT, NG) ((NG) == 2 ? 4 : (NG) == 4 ? ((FMT) == W4_KV_E4M3 ? 3 : 2) : 2)
+#endif
 constexpr int kWaves = 4;
 constexpr int kChunk = 32;          // tokens per wave step
 constexpr float kSlack = 8.0f;       // of the softmax's running reference, in powers of two
@@ -107,15 +118,18 @@ __device__ __forceinline__ Span find_span(const AttnArgs& a, int seq) {
   return s;
 }
 
-template <int FMT, int NG>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NG == 2 ? 4 : NG == 4 ? (FMT == W4_KV_E4M3 ? 3 : 2) : FMT == W4_KV_E4M3 ? 2 : 1))) kv_attention_kernel(AttnArgs a) {
+template <int FMT, int NG, int R>
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(W4_KV_EU(FMT, NG)))) kv_attention_kernel(AttnArgs a) {
   typedef KvLayout<FMT, NG> L;
   constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
+  constexpr int HPR = 16 / R;                         // heads per replica
+  constexpr int GR = NG / R;                          // groups per replica
   __shared__ float s_o[kWaves][16][BD + 4];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, c = lane >> 4;
+  const int hl = n16 % HPR, rep = n16 / HPR;          // this column's head and replica
   const int split = blockIdx.x;
   const int head = (int)(blockIdx.y / (unsigned)a.head_tiles), ht = (int)blockIdx.y - head * a.head_tiles;
   const int seq = blockIdx.z;
@@ -134,33 +148,35 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   }
   if (split >= sp.live && !(split == 0 && sp.live == 0)) return;
 
-  // q of head n16: dimensions 32g + 8c ..
+  // q of the column's head: dimensions 32g + 8c .. of the replica's groups
   u32x4 q[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     q[g] = u32x4{0u, 0u, 0u, 0u};
-    if (n16 < live_heads)
-      q[g] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + n16) * L::D + 32 * g + 8 * c);
+    if (hl < live_heads && rep == g / GR)
+      q[g] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D + 32 * g + 8 * c);
   }
   // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
-  float kbias[NG];
+  float kbias[GR];
   if constexpr (FMT == W4_KV_Q4) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int i = 0; i < GR; ++i) {
       float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t += bf16_to_f32(q[g][i] & 0xFFFFu) + __uint_as_float(q[g][i] & 0xFFFF0000u);
-      kbias[g] = -136.0f * column_sum(t);
+      for (int r = 0; r < R; ++r)     // all but the replica's own are zero
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t += bf16_to_f32(q[r * GR + i][k] & 0xFFFFu) + __uint_as_float(q[r * GR + i][k] & 0xFFFF0000u);
+      kbias[i] = -136.0f * column_sum(t);
     }
   }
 
   f32x4 acc[NG][2];
-  f32x4 vbias[FMT == W4_KV_Q4 ? NG : 1];
+  f32x4 vbias[FMT == W4_KV_Q4 ? GR : 1];   // Q4: -136 times the replica's sum of P . scale
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < NG; ++g) acc[g][0] = acc[g][1] = zero4;
 #pragma unroll
-  for (int g = 0; g < (FMT == W4_KV_Q4 ? NG : 1); ++g) vbias[g] = zero4;
+  for (int i = 0; i < (FMT == W4_KV_Q4 ? GR : 1); ++i) vbias[i] = zero4;
   float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's tokens only
   const float scale2 = a.scale * kLog2e;
 
@@ -182,40 +198,54 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     }
   };
 
-  // One chunk's K and V (codes and scales of its two tiles).  Each is reloaded
-  // as soon as its registers are free: K for the next chunk after this chunk's
-  // scores, V after its products, so one of the two is always on its way.
-  constexpr int NS = FMT == W4_KV_BF16 ? 0 : FMT == W4_KV_E4M3 ? 1 : NG / 2;   // 16-byte scale loads per tile
-  u32x4 kr[2][L::NU], vr[2][L::NU];
-  u32x4 ksr[2][NS > 0 ? NS : 1], vsr[2][NS > 0 ? NS : 1];
-  const uint8_t* next_p[2];   // K tiles (their page and head block) of the chunk that is loaded next
-  int next_tip[2];
+  // One chunk's K and V (codes and scales of its two tiles), each unit loaded
+  // again as soon as its registers are free.  Apart (head_dim 64 and 128): K
+  // for the next chunk goes out after this chunk's scores, V after its
+  // products, so one of the two is always on its way.  Shared (head_dim 256,
+  // where two sets of registers would leave one wave per SIMD): K and V take
+  // turns in one set, V of this chunk going out unit by unit behind the
+  // scores, K of the next behind the products.
+  constexpr bool SHARED = W4_KV_SHARED(FMT, NG);
+  constexpr int NS = FMT == W4_KV_BF16 ? 0 : FMT == W4_KV_E4M3 ? 1 : (GR + 1) / 2;   // 16-byte scale loads per tile
+  constexpr int NS1 = NS > 0 ? NS : 1;
+  u32x4 kr[2][L::NU], ksr[2][NS1];
+  u32x4 v_own[SHARED ? 1 : 2][SHARED ? 1 : L::NU], vs_own[SHARED ? 1 : 2][SHARED ? 1 : NS1];
+  auto& vr = [&]() -> auto& { if constexpr (SHARED) return kr; else return v_own; }();
+  auto& vsr = [&]() -> auto& { if constexpr (SHARED) return ksr; else return vs_own; }();
+  const uint8_t* next_p[2];   // page and head block of the tiles that are loaded
+  int next_tip[2];            // their place in the page
   bool good[2], next_good[2];
-  auto load_block = [&](bool v, u32x4 (&r)[2][L::NU], u32x4 (&sr)[2][NS > 0 ? NS : 1]) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      // a uniform base and a 32-bit lane offset
-      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + (uint32_t)next_tip[t] * (uint32_t)L::kTileBytes;
-      const uint8_t* ps = next_p[t] + (v ? a.block_bytes : 0) + scale_off + (uint32_t)next_tip[t] * (uint32_t)L::kScaleTileBytes;
-#pragma unroll
-      for (int u = 0; u < L::NU; ++u) {
-        const uint32_t off = (uint32_t)(u * 64 + lane) * L::kUnitBytes;
-        if constexpr (L::kUnitBytes == 16) {
-          r[t][u] = load16(p + off);
-        } else {
-          const u32x2 h = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + off));
-          r[t][u] = u32x4{h[0], h[1], 0u, 0u};
-        }
-      }
-      // scales of tokens 4c .. 4c+3: fp32 [j] (E4M3), bf16 [g][j] (Q4)
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        sr[t][i] = *reinterpret_cast<const u32x4*>(ps + (uint32_t)(16 * (c * NS + i)));
+  // a uniform base and a 32-bit lane offset
+  auto load_unit = [&](bool v, int t, int u, u32x4& r) {
+    const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + (uint32_t)next_tip[t] * (uint32_t)L::kTileBytes;
+    const uint32_t off = (uint32_t)(u * 64 + lane) * L::kUnitBytes;
+    if constexpr (L::kUnitBytes == 16) {
+      r = load16(p + off);
+    } else {
+      const u32x2 h = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + off));
+      r = u32x4{h[0], h[1], 0u, 0u};
     }
   };
-  auto load_k = [&](int ch) {
-    // a tile past the table or in a page outside the cache reads page 0 and is
-    // masked as a whole
+  // scales of tokens 4c .. 4c+3: fp32 [j] (E4M3), bf16 [the replica's g][j] (Q4)
+  auto load_scales = [&](bool v, u32x4 (&r)[2][NS1]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + scale_off + (uint32_t)next_tip[t] * (uint32_t)L::kScaleTileBytes;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if constexpr (FMT == W4_KV_Q4 && GR == 1) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(p + (uint32_t)(8 * (c * NG + rep)));
+          r[t][0] = u32x4{w[0], w[1], 0u, 0u};
+        } else {
+          const uint32_t at = FMT == W4_KV_Q4 ? 8 * (c * NG + rep * GR) : 16 * c;
+          r[t][i] = *reinterpret_cast<const u32x4*>(p + at + 16u * i);
+        }
+      }
+    }
+  };
+  // The places of a chunk's tiles; a tile past the table or in a page outside
+  // the cache reads page 0 and is masked as a whole.
+  auto find_tiles = [&](int ch) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int pi = (2 * ch + t) >> tile_shift;
@@ -225,24 +255,40 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
       next_p[t] = a.cache + (int64_t)(id >= 0 ? id : 0) * a.page_bytes + (int64_t)head * 2 * a.block_bytes;
       next_tip[t] = (2 * ch + t) & ((1 << tile_shift) - 1);
     }
-    load_block(false, kr, ksr);
   };
-  auto load_v = [&]() { load_block(true, vr, vsr); };
-  // scale i of a tile's 16-byte pieces: token j (E4M3) or group g, token j (Q4)
-  auto scale_of = [&](const u32x4 (&sr)[NS > 0 ? NS : 1], int g, int j) {
+  auto load_k = [&](int ch) {
+    find_tiles(ch);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < L::NU; ++u) load_unit(false, t, u, kr[t][u]);
+    load_scales(false, ksr);
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < L::NU; ++u) load_unit(true, t, u, vr[t][u]);
+    load_scales(true, vsr);
+  };
+  // scale of token j (E4M3), or of token j in the replica's group i (Q4)
+  auto scale_of = [&](const u32x4 (&sr)[NS1], int i, int j) {
     if constexpr (FMT == W4_KV_E4M3) return __uint_as_float(sr[0][j]);
-    const uint32_t w = sr[NS > 0 ? g >> 1 : 0][2 * (g & 1) + (j >> 1)];
+    const uint32_t w = sr[NS > 0 ? i >> 1 : 0][2 * (i & 1) + (j >> 1)];
     return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
   };
 
-  // One chunk; `more`: load the wave's next one meanwhile.
-  auto step = [&](int ch, bool more) {
+  // One chunk, and the loads of the wave's next one.
+  auto step = [&](int ch) {
     good[0] = next_good[0];
     good[1] = next_good[1];
     float p[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       f32x4 s4 = zero4;
+      f32x4 d[GR];
+#pragma unroll
+      for (int i = 0; i < GR; ++i) d[i] = f32x4{kbias[i], kbias[i], kbias[i], kbias[i]};
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int u = g / L::U, part = g % L::U;
@@ -253,9 +299,25 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
           const u32x2 a0 = e4m3_to_bf16(kr[t][u][2 * part]), a1 = e4m3_to_bf16(kr[t][u][2 * part + 1]);
           s4 = mfma(u32x4{a0[0], a0[1], a1[0], a1[1]}, q[g], s4);
         } else {
-          const f32x4 d = mfma(biased_pairs(kr[t][u][part]), q[g], f32x4{kbias[g], kbias[g], kbias[g], kbias[g]});
+          // a column gathers its replica's groups only (its q is zero in the others)
+          d[g % GR] = mfma(biased_pairs(kr[t][u][part]), q[g], d[g % GR]);
+        }
+        if constexpr (SHARED)
+          if (part == L::U - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_unit(true, t, u, vr[t][u]);
+          }
+      }
+      if constexpr (FMT == W4_KV_Q4) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s4[j] = fmaf(scale_of(ksr[t], g, j), d[j], s4[j]);
+        for (int i = 0; i < GR; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s4[j] = fmaf(scale_of(ksr[t], i, j), d[i][j], s4[j]);
+        // over the replicas; in this order every replica gets the same bits
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (R >= 2) s4[j] += dpp_row_f32<0x128>(s4[j]);   // rotate by 8 columns
+          if constexpr (R >= 4) s4[j] += dpp_row_f32<0x124>(s4[j]);   // by 4
         }
       }
 #pragma unroll
@@ -263,7 +325,13 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
         p[4 * t + j] = s4[j] * (FMT == W4_KV_E4M3 ? scale2 * scale_of(ksr[t], 0, j) : scale2);
     }
     __builtin_amdgcn_sched_barrier(0);   // not before the scores: K's registers are reused
-    load_k(ch + kWaves < end ? ch + kWaves : ch);
+    const int next = ch + kWaves < end ? ch + kWaves : ch;   // the last chunk again, unused
+    if constexpr (SHARED) {
+      load_scales(true, vsr);
+      find_tiles(next);
+    } else {
+      load_k(next);
+    }
 
     // Positions outside the span or in pages outside the cache have no score,
     // and what their V rows hold (anything) is cleared, since 0 * NaN is NaN.
@@ -327,7 +395,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
         for (int b = 0; b < 2; ++b) acc[g][b] *= alpha;
       if constexpr (FMT == W4_KV_Q4) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) vbias[g] *= alpha;
+        for (int i = 0; i < GR; ++i) vbias[i] *= alpha;
       }
     }
     const float m_use = m_run == -INFINITY ? 0.f : m_run;   // nothing yet: every p is 0
@@ -340,41 +408,42 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     l_run += sum;
 
     // O^T += V^T . P^T
-    u32x4 hi, lo;
-    if constexpr (FMT != W4_KV_Q4) {
-      if constexpr (FMT == W4_KV_E4M3) {
+    // (Q4: times the scales of each of the replica's groups)
+    constexpr int NP = FMT == W4_KV_Q4 ? GR : 1;
+    u32x4 hi[NP], lo[NP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] *= scale_of(vsr[i >> 2], 0, i & 3);
+    for (int i = 0; i < NP; ++i) {
+      float ps[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ps[k] = FMT == W4_KV_BF16 ? p[k] : p[k] * scale_of(vsr[k >> 2], i, k & 3);
+      split_bf16(ps, hi[i], lo[i]);
+      if constexpr (FMT == W4_KV_Q4) {
+        const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
+        vbias[i] = mfma(bias, hi[i], vbias[i]);
+        vbias[i] = mfma(bias, lo[i], vbias[i]);
       }
-      split_bf16(p, hi, lo);
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const int u = g / L::U, part = g % L::U;
       if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
+      const u32x4 ph = hi[g % NP], pl = lo[g % NP];
       if constexpr (FMT == W4_KV_BF16) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const u32x4 av = {vr[0][u][2 * b], vr[0][u][2 * b + 1], vr[1][u][2 * b], vr[1][u][2 * b + 1]};
-          acc[g][b] = mfma(av, hi, acc[g][b]);
-          acc[g][b] = mfma(av, lo, acc[g][b]);
+          acc[g][b] = mfma(av, ph, acc[g][b]);
+          acc[g][b] = mfma(av, pl, acc[g][b]);
         }
       } else if constexpr (FMT == W4_KV_E4M3) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const u32x2 a0 = e4m3_to_bf16(vr[0][u][2 * part + b]), a1 = e4m3_to_bf16(vr[1][u][2 * part + b]);
           const u32x4 av = {a0[0], a0[1], a1[0], a1[1]};
-          acc[g][b] = mfma(av, hi, acc[g][b]);
-          acc[g][b] = mfma(av, lo, acc[g][b]);
+          acc[g][b] = mfma(av, ph, acc[g][b]);
+          acc[g][b] = mfma(av, pl, acc[g][b]);
         }
       } else {
-        float ps[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ps[i] = p[i] * scale_of(vsr[i >> 2], g, i & 3);
-        split_bf16(ps, hi, lo);
-        const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
-        vbias[g] = mfma(bias, hi, vbias[g]);
-        vbias[g] = mfma(bias, lo, vbias[g]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           u32x4 av;
@@ -385,28 +454,35 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
             av[2 * t] = __builtin_amdgcn_perm(0x43434343u, w, 0x04010400u);
             av[2 * t + 1] = __builtin_amdgcn_perm(0x43434343u, w, 0x04030402u);
           }
-          acc[g][b] = mfma(av, hi, acc[g][b]);
-          acc[g][b] = mfma(av, lo, acc[g][b]);
+          acc[g][b] = mfma(av, ph, acc[g][b]);
+          acc[g][b] = mfma(av, pl, acc[g][b]);
         }
       }
+      if constexpr (SHARED)
+        if (part == L::U - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) load_unit(false, t, u, kr[t][u]);
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (more) load_v();
+    if constexpr (SHARED) load_scales(false, ksr);
+    else load_v();
   };
 
   int ch = begin + wv;
   if (ch < end) {
     fill_ids((2 * ch) >> tile_shift);
     load_k(ch);
-    load_v();
-    for (; ch < end; ch += kWaves) step(ch, true);
+    if constexpr (!SHARED) load_v();
+    for (; ch < end; ch += kWaves) step(ch);
   }
 
   if constexpr (FMT == W4_KV_Q4) {
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) acc[g][b] += vbias[g];
+      for (int b = 0; b < 2; ++b) acc[g][b] += vbias[g % GR];
   }
 
   // Join the waves: lane (c, n) holds, for group g, dimensions 32g + 8c + 2i + b.
@@ -426,7 +502,8 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     if (rd) __syncthreads();
 #pragma unroll
     for (int g = 0; g < BD / 32; ++g) {
-      float* o = &s_o[wv][n16][32 * g + 8 * c];
+      if (R > 1 && rep != (rd * (BD / 32) + g) / GR) continue;   // another replica's
+      float* o = &s_o[wv][hl][32 * g + 8 * c];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         o[2 * i] = acc[rd * (BD / 32) + g][0][i] * mine;
@@ -529,11 +606,19 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
   if (a.lse && d == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
 }
 
+template <int FMT, int NG>
+void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
+  const int G = a.heads / a.kv_heads;
+  if (FMT == W4_KV_Q4 && NG >= 4 && G <= 4) kv_attention_kernel<FMT, NG, FMT == W4_KV_Q4 && NG >= 4 ? 4 : 1><<<grid, 64 * kWaves, 0, stream>>>(a);
+  else if (FMT == W4_KV_Q4 && G <= 8) kv_attention_kernel<FMT, NG, FMT == W4_KV_Q4 ? 2 : 1><<<grid, 64 * kWaves, 0, stream>>>(a);
+  else kv_attention_kernel<FMT, NG, 1><<<grid, 64 * kWaves, 0, stream>>>(a);
+}
+
 template <int FMT>
 void launch_dim(const AttnArgs& a, dim3 grid, hipStream_t stream) {
-  if (a.head_dim == 64) kv_attention_kernel<FMT, 2><<<grid, 64 * kWaves, 0, stream>>>(a);
-  else if (a.head_dim == 128) kv_attention_kernel<FMT, 4><<<grid, 64 * kWaves, 0, stream>>>(a);
-  else kv_attention_kernel<FMT, 8><<<grid, 64 * kWaves, 0, stream>>>(a);
+  if (a.head_dim == 64) launch_fmt<FMT, 2>(a, grid, stream);
+  else if (a.head_dim == 128) launch_fmt<FMT, 4>(a, grid, stream);
+  else launch_fmt<FMT, 8>(a, grid, stream);
 }
 
 int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_heads + 15) / 16; }
