@@ -619,8 +619,8 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  *                that overlap in time need one each.
  * The results do not depend on what else runs (no atomics in the sums); they
  * depend on table_width through the split of the length.
- * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, table_width *
- * page_size < 2^31, n_pages >= 1, window >= 0, finite scale.
+ * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, seqs * heads <
+ * 2^24, table_width * page_size < 2^31, n_pages >= 1, window >= 0, finite scale.
  */
 size_t kv_cache_attention_workspace(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     int64_t table_width, int32_t page_size);

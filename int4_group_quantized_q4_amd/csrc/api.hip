@@ -839,7 +839,8 @@ static int check_attention(int64_t seqs, int32_t heads, int32_t kv_heads, int32_
   const int st = check_kv_shape(W4_KV_BF16, 0, page_size, kv_heads, head_dim);
   if (st != W4_OK) return st;
   if (seqs < 0 || heads < 1 || table_width < 0) return W4_ERR_ARG;
-  if (heads % kv_heads != 0 || heads > 16384 || seqs > 65535 || table_width > (int64_t)INT32_MAX / page_size)
+  if (heads % kv_heads != 0 || heads > 16384 || seqs > 65535 || table_width > (int64_t)INT32_MAX / page_size ||
+      seqs * heads >= ((int64_t)1 << 24))   // a grid holds fewer than 2^32 threads
     return W4_ERR_SHAPE;
   return W4_OK;
 }

@@ -146,9 +146,11 @@ struct AttnArgs {
   float* lse;                // nullable, [seqs][heads]
   unsigned long long* counters;   // nullable
   // set by launch_kv_attention
-  int32_t head_tiles, splits;
-  float* part_o;             // [seqs][heads][splits][head_dim]
-  float* part_ml;            // [seqs][heads][splits][2]
+  int32_t head_tiles;
+  int32_t shares;            // equal shares that the positions are cut into; 0: no splits
+  float* part_o;             // [items][heads][head_dim]
+  float* part_ml;            // [items][heads][2]
+  int2* part_plan;           // [seqs]: first item, items
 };
 
 size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens);

@@ -9,10 +9,11 @@
 // Bound by the cache's bytes: a token's K and V row of a head are read once
 // for all G query heads.
 //
-// Work split: grid (splits of the length, kv head x tile of 16 query heads,
-// sequence); a workgroup of 4 waves takes one split, and a wave 32 tokens at
-// a time (two tiles of the cache), with its own running maximum, sum and
-// output.  The waves are joined through LDS, the splits by a second kernel.
+// Work split: grid (kv head x tile of 16 query heads, items), an item being a
+// run of a sequence's positions; a workgroup of 4 waves takes one, and a wave
+// 32 tokens at a time (two tiles of the cache), with its own running maximum,
+// sum and output.  The waves are joined through LDS, the items of a sequence
+// by a second kernel.
 //
 // Matrix layouts (16x16x32 bf16, lane = 16c + n): the scores are formed as
 // S^T = K . Q^T with a tile's 16 tokens as rows, so lane (c, n) holds the
@@ -95,27 +96,94 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// The positions a sequence attends to, in 32-token chunks, and how they are
-// dealt to the splits (the same for the attention and the join kernel).
+// The positions a sequence attends to, and their 32-token chunks.
 struct Span {
   int n, lo;          // positions [lo, n); all positions fit 31 bits
   int first, chunks;  // chunk range
-  int per;            // chunks per split
-  int live;           // splits that have any
 };
 
-__device__ __forceinline__ Span find_span(const AttnArgs& a, int seq) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int len) {
   Span s;
   const int most = (int)a.table_width << a.page_shift;
-  const int len = a.lens[seq];
   s.n = len < 0 ? 0 : len > most ? most : len;
   s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
   s.first = s.lo / kChunk;
-  s.chunks = (s.n + kChunk - 1) / kChunk - s.first;
-  s.per = (int)((unsigned)(s.chunks + a.splits - 1) / (unsigned)a.splits);
-  if (s.per < kWaves) s.per = kWaves;
-  s.live = s.chunks > 0 ? (int)((unsigned)(s.chunks + s.per - 1) / (unsigned)s.per) : 0;
+  s.chunks = (int)(((unsigned)s.n + kChunk - 1) / kChunk) - s.first;
   return s;
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
+// Work items of a call whose positions are split: a fair share is the batch's
+// chunks divided by `shares`, and a sequence is cut into equal items of about
+// one share (at most a quarter more, as an item much smaller than the others
+// costs its start and end; one item for an empty sequence), so that long and
+// short sequences get workgroups by their length.  The lengths are on the
+// device, so every wave counts the items for itself.
+struct Item {
+  int seq, index;     // sequence of the item and its place in it
+  int base, live;     // the sequence's first item and their number
+  int len;
+  bool found;
+};
+
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int want) {
+  const int lane = threadIdx.x & 63;
+  const int seqs = (int)a.seqs;
+  const bool small = (a.table_width << a.page_shift) < ((int64_t)1 << 29);   // 64 chunk counts fit 31 bits
+  int64_t total = a.shares - 1;
+  int len = 0, chunks = 0;
+  for (int b = 0; b < seqs; b += 64) {
+    const int l = b + lane < seqs ? a.lens[b + lane] : 0;
+    const int ch = span_of(a, l).chunks;
+    if (b == 0) {
+      len = l;
+      chunks = ch;
+    }
+    if (small) {
+      total += __builtin_amdgcn_readlane(wave_prefix(ch), 63);
+    } else {
+      const int lo = __builtin_amdgcn_readlane(wave_prefix(ch & 0xFFFF), 63);
+      const int hi = __builtin_amdgcn_readlane(wave_prefix(ch >> 16), 63);
+      total += ((int64_t)hi << 16) + lo;
+    }
+  }
+  unsigned per = total < ((int64_t)1 << 31) ? (unsigned)total / (unsigned)a.shares : (unsigned)(total / a.shares);
+  if (per < kWaves) per = kWaves;
+  Item it{};
+  for (int b = 0; b < seqs; b += 64) {
+    if (b > 0) {
+      len = b + lane < seqs ? a.lens[b + lane] : 0;
+      chunks = span_of(a, len).chunks;
+    }
+    // ceil(chunks / per - 1/4), at least 1
+    int cnt = (int)((4u * (unsigned)chunks + 3u * per - 1u) / (4u * per));
+    if (cnt == 0) cnt = 1;
+    if (b + lane >= seqs) cnt = 0;
+    const int upto = wave_prefix(cnt);
+    const uint64_t hit = __ballot(it.base + upto > want);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      it.seq = b + l;
+      it.live = __builtin_amdgcn_readlane(cnt, l);
+      it.len = __builtin_amdgcn_readlane(len, l);
+      it.base += __builtin_amdgcn_readlane(upto, l) - it.live;
+      it.index = want - it.base;
+      it.found = true;
+      return it;
+    }
+    it.base += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return it;
 }
 
 template <int FMT, int NG, int R>
@@ -130,23 +198,34 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, c = lane >> 4;
   const int hl = n16 % HPR, rep = n16 / HPR;          // this column's head and replica
-  const int split = blockIdx.x;
-  const int head = (int)(blockIdx.y / (unsigned)a.head_tiles), ht = (int)blockIdx.y - head * a.head_tiles;
-  const int seq = blockIdx.z;
+  // heads before items: the workgroups go round the XCDs one by one
+  const int hrow = blockIdx.x;
+  const int head = (int)((unsigned)hrow / (unsigned)a.head_tiles), ht = hrow - head * a.head_tiles;
+  int seq = blockIdx.y, index = 0, live = 1, len;
+  if (a.shares > 0) {
+    const Item it = find_item(a, blockIdx.y);
+    if (!it.found) return;
+    seq = it.seq;
+    index = it.index;
+    live = it.live;
+    len = it.len;
+    if (hrow == 0 && index == 0 && threadIdx.x == 0) a.part_plan[seq] = int2{it.base, live};   // for the join
+  } else {
+    len = a.lens[seq];
+  }
   const int G = (int)((unsigned)a.heads / (unsigned)a.kv_heads);
   const int live_heads = G - 16 * ht < 16 ? G - 16 * ht : 16;
   const int h0 = head * G + 16 * ht;     // first query head
   const int32_t* table = a.table + (int64_t)seq * a.table_width;
   const int width = (int)a.table_width;
-  const Span sp = find_span(a, seq);
-  if (a.counters && split == 0 && blockIdx.y == 0) {  // table entries outside the cache, once per entry
+  const Span sp = span_of(a, len);
+  if (a.counters && index == 0 && hrow == 0) {  // table entries outside the cache, once per entry
     const int p1 = (int)(((unsigned)sp.n + (1u << a.page_shift) - 1) >> a.page_shift);
     for (int p = (sp.lo >> a.page_shift) + (int)threadIdx.x; p < p1; p += 64 * kWaves) {
       const int id = table[p];
       if (id < 0 || id >= a.n_pages) atomicAdd(a.counters, 1ull);
     }
   }
-  if (split >= sp.live && !(split == 0 && sp.live == 0)) return;
 
   // q of the column's head: dimensions 32g + 8c .. of the replica's groups
   u32x4 q[NG];
@@ -180,8 +259,9 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's tokens only
   const float scale2 = a.scale * kLog2e;
 
-  const int begin = sp.first + split * sp.per;
-  const int end = begin + sp.per < sp.first + sp.chunks ? begin + sp.per : sp.first + sp.chunks;
+  const int size = (int)((unsigned)sp.chunks / (unsigned)live), rest = sp.chunks - size * live;
+  const int begin = sp.first + index * size + (index < rest ? index : rest);
+  const int end = begin + size + (index < rest ? 1 : 0);
   const int tile_shift = a.page_shift - 4;
   const uint32_t scale_off = ((uint32_t)L::kTileBytes << a.page_shift) / kKvTile;
 
@@ -526,13 +606,13 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
       }
       const int64_t row = (int64_t)seq * a.heads + h0 + h;
       const int dim = rd * BD + d;
-      if (sp.live <= 1) {
+      if (live == 1) {
         const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // l: 0 for an empty row, NaN passes on
         u32x2 w2 = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
         *reinterpret_cast<u32x2*>(a.out + row * L::D + dim) = w2;
         if (a.lse && dim == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
       } else {
-        const int64_t pr = row * a.splits + split;
+        const int64_t pr = (int64_t)blockIdx.y * a.heads + h0 + h;
         *reinterpret_cast<f32x4*>(a.part_o + pr * L::D + dim) = o;
         if (dim == 0) {
           a.part_ml[2 * pr] = mx;
@@ -553,34 +633,27 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
   constexpr int D = 32 * NG, TG = D / 4, GROUPS = 256 / TG;
   __shared__ f32x4 s_o[GROUPS][TG];
   const int lane = threadIdx.x & 63;
+  const int2 plan = a.part_plan[blockIdx.y];
+  const int live = plan.y;
+  if (live <= 1) return;   // the attention kernel wrote the output
   const int64_t row = (int64_t)blockIdx.y * a.heads + blockIdx.x;
-  const float* ml = a.part_ml + 2 * row * a.splits;
-  // every wave reduces all (m, l) pairs; the first 64 splits' are loaded
-  // before the length is known
-  float m0 = -INFINITY, l0 = 0.f;
-  if (lane < a.splits) {
-    m0 = ml[2 * lane];
-    l0 = ml[2 * lane + 1];
-  }
-  const Span sp = find_span(a, blockIdx.y);
-  if (sp.live <= 1) return;   // the attention kernel wrote the output
-  if (lane >= sp.live) {      // not written
-    m0 = -INFINITY;
-    l0 = 0.f;
-  }
-  float mx = m0;
-  for (int s = lane + 64; s < sp.live; s += 64) mx = fmaxf(mx, ml[2 * s]);
+  const int64_t first = (int64_t)plan.x * a.heads + blockIdx.x;    // the row's first partial result
+  const int pitch = 2 * a.heads;
+  const float* ml = a.part_ml + 2 * first;
+  // every wave reduces all (m, l) pairs
+  float mx = -INFINITY;
+  for (int s = lane; s < live; s += 64) mx = fmaxf(mx, ml[(int64_t)s * pitch]);
   mx = wave_max_all(mx);
-  // a split without a score has l = 0 and o = 0 (or NaN, which passes on)
+  // an item without a score has l = 0 and o = 0 (or NaN, which passes on)
   auto weight = [&](float m) { return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx); };
-  float l = l0 * weight(m0);
-  for (int s = lane + 64; s < sp.live; s += 64) l += ml[2 * s + 1] * weight(ml[2 * s]);
+  float l = 0.f;
+  for (int s = lane; s < live; s += 64) l += ml[(int64_t)s * pitch + 1] * weight(ml[(int64_t)s * pitch]);
   l = wave_sum_all(l);
 
   const int grp = threadIdx.x / TG, d = threadIdx.x % TG;
-  const f32x4* po = reinterpret_cast<const f32x4*>(a.part_o + row * a.splits * D) + d;
+  const f32x4* po = reinterpret_cast<const f32x4*>(a.part_o + first * D) + d;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = grp; s < sp.live; s += 4 * GROUPS) {
+  for (int s = grp; s < live; s += 4 * GROUPS) {
     f32x4 v[4];
     float w[4];
 #pragma unroll
@@ -588,9 +661,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
       const int k = s + i * GROUPS;
       v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       w[i] = 0.f;
-      if (k < sp.live) {
-        v[i] = po[(int64_t)k * TG];
-        w[i] = weight(ml[2 * k]);
+      if (k < live) {
+        v[i] = po[(int64_t)k * a.heads * TG];
+        w[i] = weight(ml[(int64_t)k * pitch]);
       }
     }
 #pragma unroll
@@ -623,33 +696,65 @@ void launch_dim(const AttnArgs& a, dim3 grid, hipStream_t stream) {
 
 int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_heads + 15) / 16; }
 
-// Splits of the length: enough workgroups to fill the 256 CUs eight deep, at
-// least 128 tokens (a chunk per wave) each.
-int splits_of(int64_t seqs, int32_t heads, int32_t kv_heads, int64_t tokens) {
-  const int64_t rows = seqs * kv_heads * head_tiles_of(heads, kv_heads);
-  int64_t s = (2048 + rows - 1) / (rows > 0 ? rows : 1);
-  const int64_t most = (tokens + kWaves * kChunk - 1) / (kWaves * kChunk);
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int)s;
+// How a call's positions are split.  The workgroups aimed at are those that
+// keep the memory busy: fewer and longer ones lose less in starts, ends and
+// partial results.  Measured (us; 256, 512, 768, 1024 workgroups): bf16 8 x
+// 32768 tokens of 8 x 128: 163, 166, 169, 170; bf16 32 x 8192 of 8 x 64: 83,
+// 90, 93, 92; bf16 16 x 8192 of 4 x 256: 92, 103, 113, 109; E4M3 32 x 32768
+// ragged of 8 x 128: 238, 141, 135, 130; E4M3 16 x 16384 of 8 x 128: 90, 92,
+// 95, 94; E4M3 16 x 16384 of 4 x 256: 91, 94, 103, 96; Q4 16 x 32768 of 8 x
+// 128: 149, 118, 114, 116; Q4 32 x 16384 of 8 x 64: 156, 100, 83, 77; Q4 16 x
+// 32768 of 4 x 256: 153, 106, 122, 111.
+int64_t target_of(int32_t format, int32_t head_dim) {
+  if (format == W4_KV_BF16) return 256;
+  if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 512;
+  return head_dim == 64 ? 1024 : head_dim == 128 ? 768 : 512;
+}
+constexpr int64_t kMostTarget = 1024;
+
+struct Plan {
+  int shares;     // 0: one workgroup per sequence and head row
+  int64_t items;  // at most
+};
+
+// `tokens`: the most a sequence attends to.  A call with enough sequences and
+// head rows is split too where a long sequence among short ones would outlast
+// the others (over kUnsplit tokens), unless counting the items takes too long.
+constexpr int64_t kUnsplit = 4096, kMostCounted = 256;
+Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int64_t tokens) {
+  const int64_t hrows = kv_heads * head_tiles_of(heads, kv_heads);
+  const int64_t most = (tokens + kWaves * kChunk - 1) / (kWaves * kChunk);   // items a sequence can have
+  const bool enough = seqs * hrows >= target;
+  if (most <= 1 || (enough && (tokens <= kUnsplit || seqs > kMostCounted))) return {0, seqs};
+  int64_t shares = (target + hrows - 1) / hrows;
+  if (shares < seqs) shares = seqs;
+  const int64_t items = shares + seqs;
+  return {(int)shares, items < seqs * most ? items : seqs * most};
 }
 
 }  // namespace
 
+// For any format and window: a smaller target or fewer attended tokens give no
+// more items.
 size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
-  const int64_t s = splits_of(seqs, heads, kv_heads, tokens);
-  return s <= 1 ? 0 : (size_t)(seqs * heads * s) * (size_t)(head_dim + 2) * sizeof(float);
+  const Plan p = plan_of(kMostTarget, seqs, heads, kv_heads, tokens);
+  return p.shares == 0 ? 0 : (size_t)(p.items * heads) * (size_t)(head_dim + 2) * sizeof(float) + (size_t)seqs * sizeof(int2);
 }
 
 void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {
   a.head_tiles = (int32_t)head_tiles_of(a.heads, a.kv_heads);
-  a.splits = splits_of(a.seqs, a.heads, a.kv_heads, a.table_width << a.page_shift);
+  int64_t tokens = a.table_width << a.page_shift;
+  if (a.window > 0 && tokens > a.window + kChunk) tokens = a.window + kChunk;
+  const Plan p = plan_of(target_of(a.format, a.head_dim), a.seqs, a.heads, a.kv_heads, tokens);
+  a.shares = p.shares;
   a.part_o = static_cast<float*>(ws);
-  a.part_ml = a.splits > 1 ? a.part_o + a.seqs * a.heads * a.splits * a.head_dim : nullptr;
-  const dim3 grid(a.splits, a.kv_heads * a.head_tiles, (unsigned)a.seqs);
+  a.part_ml = a.part_o + p.items * a.heads * a.head_dim;
+  a.part_plan = reinterpret_cast<int2*>(a.part_ml + p.items * a.heads * 2);
+  const dim3 grid(a.kv_heads * a.head_tiles, (unsigned)p.items);
   if (a.format == W4_KV_BF16) launch_dim<W4_KV_BF16>(a, grid, stream);
   else if (a.format == W4_KV_E4M3) launch_dim<W4_KV_E4M3>(a, grid, stream);
   else launch_dim<W4_KV_Q4>(a, grid, stream);
-  if (a.splits > 1) {
+  if (a.shares > 0) {
     const dim3 rows(a.heads, (unsigned)a.seqs);
     if (a.head_dim == 64) kv_join_kernel<2><<<rows, 256, 0, stream>>>(a);
     else if (a.head_dim == 128) kv_join_kernel<4><<<rows, 256, 0, stream>>>(a);
