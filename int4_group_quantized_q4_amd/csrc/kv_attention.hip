@@ -45,10 +45,16 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-#ifndef W4_KV_SHARED
-#define W4_KV_SHARED(FMT, NG) ((NG) == 8)
-#define W4_KV_EU(FMT, NG) ((NG) == 2 ? 4 : (NG) == 4 ? ((FMT) == W4_KV_E4M3 ? 3 : 2) : 2)
-#endif
+// Least waves per SIMD that the register allocator keeps: measured against one
+// more and one fewer, E4M3 48 ragged sequences of 8 x 128 55.6 (3) and 57 us
+// (2), Q4 16 x 32768 of 4 x 256 with 16 heads a kv head 192 (1) and 315 us (2,
+// spilling); the others within 3%.
+constexpr int waves_per_simd(int fmt, int ng, int r) {
+  if (ng == 2) return 4;
+  if (ng == 4) return fmt == W4_KV_E4M3 ? 3 : 2;
+  return fmt == W4_KV_Q4 && r == 1 ? 1 : 2;
+}
+
 constexpr int kWaves = 4;
 constexpr int kChunk = 32;          // tokens per wave step
 constexpr float kSlack = 8.0f;       // of the softmax's running reference, in powers of two
@@ -187,7 +193,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int want) {
 }
 
 template <int FMT, int NG, int R>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(W4_KV_EU(FMT, NG)))) kv_attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_per_simd(FMT, NG, R)))) kv_attention_kernel(AttnArgs a) {
   typedef KvLayout<FMT, NG> L;
   constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
   constexpr int HPR = 16 / R;                         // heads per replica
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   // where two sets of registers would leave one wave per SIMD): K and V take
   // turns in one set, V of this chunk going out unit by unit behind the
   // scores, K of the next behind the products.
-  constexpr bool SHARED = W4_KV_SHARED(FMT, NG);
+  constexpr bool SHARED = NG == 8;
   constexpr int NS = FMT == W4_KV_BF16 ? 0 : FMT == W4_KV_E4M3 ? 1 : (GR + 1) / 2;   // 16-byte scale loads per tile
   constexpr int NS1 = NS > 0 ? NS : 1;
   u32x4 kr[2][L::NU], ksr[2][NS1];
@@ -358,6 +364,14 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
   };
 
+  // whether group g is the last of its unit in the order (i, r), g = r GR + i
+  auto unit_done = [](int g) {
+    bool last = true;
+    for (int h = g / L::U * L::U; h < (g / L::U + 1) * L::U; ++h)
+      if (h % GR * R + h / GR > g % GR * R + g / GR) last = false;
+    return last;
+  };
+
   // One chunk, and the loads of the wave's next one.
   auto step = [&](int ch) {
     good[0] = next_good[0];
@@ -366,39 +380,40 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       f32x4 s4 = zero4;
-      f32x4 d[GR];
+      // groups in the order of their scale arithmetic: a replica's i-th for all replicas
 #pragma unroll
-      for (int i = 0; i < GR; ++i) d[i] = f32x4{kbias[i], kbias[i], kbias[i], kbias[i]};
+      for (int i = 0; i < GR; ++i) {
+        float kb = kbias[i];
+        asm volatile("" : "+v"(kb));   // spread here, not kept in four registers each over the loop
+        f32x4 d = {kb, kb, kb, kb};
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int u = g / L::U, part = g % L::U;
-        if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
-        if constexpr (FMT == W4_KV_BF16) {
-          s4 = mfma(kr[t][u], q[g], s4);
-        } else if constexpr (FMT == W4_KV_E4M3) {
-          const u32x2 a0 = e4m3_to_bf16(kr[t][u][2 * part]), a1 = e4m3_to_bf16(kr[t][u][2 * part + 1]);
-          s4 = mfma(u32x4{a0[0], a0[1], a1[0], a1[1]}, q[g], s4);
-        } else {
-          // a column gathers its replica's groups only (its q is zero in the others)
-          d[g % GR] = mfma(biased_pairs(kr[t][u][part]), q[g], d[g % GR]);
-        }
-        if constexpr (SHARED)
-          if (part == L::U - 1) {
+        for (int r = 0; r < R; ++r) {
+          const int g = r * GR + i, u = g / L::U, part = g % L::U;
+          if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
+          if constexpr (FMT == W4_KV_BF16) {
+            s4 = mfma(kr[t][u], q[g], s4);
+          } else if constexpr (FMT == W4_KV_E4M3) {
+            const u32x2 a0 = e4m3_to_bf16(kr[t][u][2 * part]), a1 = e4m3_to_bf16(kr[t][u][2 * part + 1]);
+            s4 = mfma(u32x4{a0[0], a0[1], a1[0], a1[1]}, q[g], s4);
+          } else {
+            // a column gathers its replica's groups only (its q is zero in the others)
+            d = mfma(biased_pairs(kr[t][u][part]), q[g], d);
+          }
+          if (SHARED && unit_done(g)) {
             __builtin_amdgcn_sched_barrier(0);
             load_unit(true, t, u, vr[t][u]);
           }
-      }
-      if constexpr (FMT == W4_KV_Q4) {
-#pragma unroll
-        for (int i = 0; i < GR; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s4[j] = fmaf(scale_of(ksr[t], i, j), d[i][j], s4[j]);
-        // over the replicas; in this order every replica gets the same bits
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (R >= 2) s4[j] += dpp_row_f32<0x128>(s4[j]);   // rotate by 8 columns
-          if constexpr (R >= 4) s4[j] += dpp_row_f32<0x124>(s4[j]);   // by 4
         }
+        if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s4[j] = fmaf(scale_of(ksr[t], i, j), d[j], s4[j]);
+        }
+      }
+      // Q4: over the replicas; in this order every replica gets the same bits
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (R >= 2) s4[j] += dpp_row_f32<0x128>(s4[j]);   // rotate by 8 columns
+        if constexpr (R >= 4) s4[j] += dpp_row_f32<0x124>(s4[j]);   // by 4
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -487,63 +502,51 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
     }
     l_run += sum;
 
-    // O^T += V^T . P^T
-    // (Q4: times the scales of each of the replica's groups)
-    constexpr int NP = FMT == W4_KV_Q4 ? GR : 1;
-    u32x4 hi[NP], lo[NP];
+    // O^T += V^T . P^T (Q4: P times the scales of the replicas' i-th groups)
+    u32x4 ph, pl;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      float ps[8];
+    for (int i = 0; i < GR; ++i) {
+      if (FMT == W4_KV_Q4 || i == 0) {
+        float ps[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ps[k] = FMT == W4_KV_BF16 ? p[k] : p[k] * scale_of(vsr[k >> 2], i, k & 3);
-      split_bf16(ps, hi[i], lo[i]);
+        for (int k = 0; k < 8; ++k) ps[k] = FMT == W4_KV_BF16 ? p[k] : p[k] * scale_of(vsr[k >> 2], i, k & 3);
+        split_bf16(ps, ph, pl);
+      }
       if constexpr (FMT == W4_KV_Q4) {
         const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
-        vbias[i] = mfma(bias, hi[i], vbias[i]);
-        vbias[i] = mfma(bias, lo[i], vbias[i]);
+        vbias[i] = mfma(bias, ph, vbias[i]);
+        vbias[i] = mfma(bias, pl, vbias[i]);
       }
-    }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int u = g / L::U, part = g % L::U;
-      if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
-      const u32x4 ph = hi[g % NP], pl = lo[g % NP];
-      if constexpr (FMT == W4_KV_BF16) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const u32x4 av = {vr[0][u][2 * b], vr[0][u][2 * b + 1], vr[1][u][2 * b], vr[1][u][2 * b + 1]};
-          acc[g][b] = mfma(av, ph, acc[g][b]);
-          acc[g][b] = mfma(av, pl, acc[g][b]);
-        }
-      } else if constexpr (FMT == W4_KV_E4M3) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const u32x2 a0 = e4m3_to_bf16(vr[0][u][2 * part + b]), a1 = e4m3_to_bf16(vr[1][u][2 * part + b]);
-          const u32x4 av = {a0[0], a0[1], a1[0], a1[1]};
-          acc[g][b] = mfma(av, ph, acc[g][b]);
-          acc[g][b] = mfma(av, pl, acc[g][b]);
-        }
-      } else {
+      for (int r = 0; r < R; ++r) {
+        const int g = r * GR + i, u = g / L::U, part = g % L::U;
+        if constexpr (NG == 8) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           u32x4 av;
+          if constexpr (FMT == W4_KV_BF16) {
+            av = u32x4{vr[0][u][2 * b], vr[0][u][2 * b + 1], vr[1][u][2 * b], vr[1][u][2 * b + 1]};
+          } else if constexpr (FMT == W4_KV_E4M3) {
+            const u32x2 a0 = e4m3_to_bf16(vr[0][u][2 * part + b]), a1 = e4m3_to_bf16(vr[1][u][2 * part + b]);
+            av = u32x4{a0[0], a0[1], a1[0], a1[1]};
+          } else {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            // byte j: token j's code of dimension 2m (low nibble), 2m + 1 (high)
-            const uint32_t w = (b ? vr[t][u][part] >> 4 : vr[t][u][part]) & 0x0F0F0F0Fu;
-            av[2 * t] = __builtin_amdgcn_perm(0x43434343u, w, 0x04010400u);
-            av[2 * t + 1] = __builtin_amdgcn_perm(0x43434343u, w, 0x04030402u);
+            for (int t = 0; t < 2; ++t) {
+              // byte j: token j's code of dimension 2m (low nibble), 2m + 1 (high)
+              const uint32_t w = (b ? vr[t][u][part] >> 4 : vr[t][u][part]) & 0x0F0F0F0Fu;
+              av[2 * t] = __builtin_amdgcn_perm(0x43434343u, w, 0x04010400u);
+              av[2 * t + 1] = __builtin_amdgcn_perm(0x43434343u, w, 0x04030402u);
+            }
           }
           acc[g][b] = mfma(av, ph, acc[g][b]);
           acc[g][b] = mfma(av, pl, acc[g][b]);
         }
-      }
-      if constexpr (SHARED)
-        if (part == L::U - 1) {
+        if (SHARED && unit_done(g)) {
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int t = 0; t < 2; ++t) load_unit(false, t, u, kr[t][u]);
         }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (SHARED) load_scales(false, ksr);
@@ -707,7 +710,7 @@ int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_head
 // 32768 of 4 x 256: 153, 106, 122, 111.
 int64_t target_of(int32_t format, int32_t head_dim) {
   if (format == W4_KV_BF16) return 256;
-  if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 512;
+  if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 768;
   return head_dim == 64 ? 1024 : head_dim == 128 ? 768 : 512;
 }
 constexpr int64_t kMostTarget = 1024;
@@ -724,7 +727,7 @@ constexpr int64_t kUnsplit = 4096, kMostCounted = 256;
 Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int64_t tokens) {
   const int64_t hrows = kv_heads * head_tiles_of(heads, kv_heads);
   const int64_t most = (tokens + kWaves * kChunk - 1) / (kWaves * kChunk);   // items a sequence can have
-  const bool enough = seqs * hrows >= target;
+  const bool enough = seqs * hrows * 3 >= target * 2;
   if (most <= 1 || (enough && (tokens <= kUnsplit || seqs > kMostCounted))) return {0, seqs};
   int64_t shares = (target + hrows - 1) / hrows;
   if (shares < seqs) shares = seqs;

@@ -11,6 +11,7 @@ tensors with torch and then make the same calls.
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -418,43 +419,68 @@ def w8a8_moe_layer(x, logits, k, I, w1q, w1_scale, w2q, w2_scale, activation, y,
 def _call(name, device, stream, *args):
     """One library call on `device` (the launch needs it current) and on
     `stream` (default: that device's current stream)."""
-    fn = getattr(lib(), name)
-    with contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        st = fn(*args, _stream(stream))
-    check(st, name)
+    index = device.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    st = getattr(_lib._lib or lib(), name)(*args, s)
+    if st != _lib.W4_OK:
+        check(st, name)
 
 
-def _check_norm(x, residual, weight, sum_out, d):
+def _arg(t, name, dtypes, nbytes, device):
+    """Pointer of a contiguous tensor of at least nbytes on `device` (None
+    passes as a null pointer); the checks' own errors where one fails."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.nbytes >= nbytes \
+            and t.device == device and t.is_cuda:
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        _need(t, name, nbytes, device)
+    return _ptr(t, name, dtypes)
+
+
+def _given(t, name):
+    if t is None:
+        raise ValueError("%s must not be None" % name)
+    return t
+
+
+_F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
+_BF16_OR_F32 = _F32 + _BF16_LIKE
+
+
+def _norm(name, x, residual, weight, eps, sum_out, weight_offset, outs, stream):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d], got %s" % (tuple(x.shape),))
-    n = x.shape[0] * d * 2
-    _need(residual, "residual", n, x.device)
-    _need(weight, "weight", d * 2, x.device)
-    _need(sum_out, "sum_out", n, x.device)
-    return (_ptr(x, "x", _BF16_LIKE), _ptr(residual, "residual", _BF16_LIKE, True), _ptr(weight, "weight", _BF16_LIKE))
+    rows, d = x.shape
+    dv = x.device
+    n = rows * d * 2
+    if not x.is_cuda:   # sizes first, as in the other calls
+        for t, k, b in ((residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n)):
+            _need(t, k, b, dv)
+        for t, k, dt, per in outs:
+            _need(t, k, rows * per, dv)
+    _call(name, dv, stream,
+          _arg(x, "x", _BF16_LIKE, n, dv), _arg(residual, "residual", _BF16_LIKE, n, dv),
+          _arg(_given(weight, "weight"), "weight", _BF16_LIKE, d * 2, dv), rows, d, eps, weight_offset,
+          _arg(sum_out, "sum_out", _BF16_LIKE, n, dv),
+          *[_arg(_given(t, k), k, dt, rows * per, dv) for t, k, dt, per in outs])
 
 
 def w4a16_add_rmsnorm(x, residual, weight, eps, sum_out, y, weight_offset=0.0, stream=None):
     """y = bf16(RMS norm of r = bf16(x + residual)); residual and sum_out (r)
     may be None."""
-    d = x.shape[-1]
-    ptrs = _check_norm(x, residual, weight, sum_out, d)
-    _need(y, "y", x.shape[0] * d * 2, x.device)
-    _call("w4a16_add_rmsnorm", x.device, stream, *ptrs, x.shape[0], d, eps, weight_offset,
-          _ptr(sum_out, "sum_out", _BF16_LIKE, True), _ptr(y, "y", _BF16_LIKE))
+    _norm("w4a16_add_rmsnorm", x, residual, weight, eps, sum_out, weight_offset,
+          ((y, "y", _BF16_LIKE, x.shape[-1] * 2),), stream)
 
 
 def w8a8_add_rmsnorm_quantize(x, residual, weight, eps, sum_out, q, scale, weight_offset=0.0, stream=None):
     """The norm's rows as E4M3 codes q [rows, d] and fp32 row scales."""
-    d = x.shape[-1]
-    ptrs = _check_norm(x, residual, weight, sum_out, d)
-    _need(q, "q", x.shape[0] * d, x.device)
-    _need(scale, "scale", x.shape[0] * 4, x.device)
-    _call("w8a8_add_rmsnorm_quantize", x.device, stream, *ptrs, x.shape[0], d, eps, weight_offset,
-          _ptr(sum_out, "sum_out", _BF16_LIKE, True), _ptr(q, "q", (torch.uint8,)),
-          _ptr(scale, "scale", (torch.float32,)))
+    _norm("w8a8_add_rmsnorm_quantize", x, residual, weight, eps, sum_out, weight_offset,
+          ((q, "q", _U8, x.shape[-1]), (scale, "scale", _F32, 4)), stream)
 
 
 def _rows(t, name, dtypes, like=None):
@@ -470,11 +496,14 @@ def _rows(t, name, dtypes, like=None):
     if t.dtype not in dtypes:
         raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
     rows, heads, dim = t.shape
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    step, head, one = t.stride()
+    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
         raise ValueError("%s: the heads of a row must be contiguous" % name)
-    if rows > 1 and t.stride(0) < heads * dim:
+    if rows <= 1:
+        return t.data_ptr(), heads * dim
+    if step < heads * dim:
         raise ValueError("%s: rows must not overlap" % name)
-    return t.data_ptr(), t.stride(0) if rows > 1 else heads * dim
+    return t.data_ptr(), step
 
 
 def _on_device(t, name):
@@ -482,6 +511,7 @@ def _on_device(t, name):
         raise ValueError("%s must be a device tensor" % name)
 
 
+@functools.lru_cache(maxsize=None)
 def kv_cache_page_bytes(format, page_size, kv_heads, head_dim):
     """Bytes of one page; ValueError for sizes outside the limits."""
     n = int(lib().kv_cache_page_bytes(format, page_size, kv_heads, head_dim))
@@ -494,41 +524,35 @@ def kv_cache_page_bytes(format, page_size, kv_heads, head_dim):
 def _pages(cache, format, page_size, kv_heads, head_dim, device):
     """Pointer and page count of a cache buffer."""
     page = kv_cache_page_bytes(format, page_size, kv_heads, head_dim)
-    p = _ptr(cache, "cache", (torch.uint8,))
-    if cache.numel() % page:
+    n, rest = divmod(_given(cache, "cache").numel(), page)
+    if rest:
         raise ValueError("cache holds %d bytes, not a multiple of a page's %d" % (cache.numel(), page))
-    if cache.device != device:
-        raise ValueError("cache is on %s, expected %s" % (cache.device, device))
-    return p, cache.numel() // page
+    return _arg(cache, "cache", _U8, 0, device), n
 
 
 def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=None):
     """Quantize the rows k, v [tokens, kv_heads, head_dim] into their slots."""
-    tokens, heads, dim = k.shape
     kp, ks = _rows(k, "k", _BF16_LIKE)
     vp, vs = _rows(v, "v", _BF16_LIKE, k)
     _on_device(k, "k")
+    tokens, heads, dim = k.shape
     d = k.device
-    _need(slots, "slots", tokens * 8, d)
-    _need(counters, "counters", 16, d)
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
-    _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs, _ptr(slots, "slots", (torch.int64,)), format, cp, pages,
-          page_size, heads, dim, _ptr(counters, "counters", (torch.int64,), True))
+    _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs, _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d),
+          format, cp, pages, page_size, heads, dim, _arg(counters, "counters", _I64, 16, d))
 
 
 def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=None):
     """The rows of `slots` into k, v [tokens, kv_heads, head_dim] (bf16 or fp32)."""
-    tokens, heads, dim = k.shape
-    kp, ks = _rows(k, "k", (torch.float32,) + _BF16_LIKE)
-    vp, vs = _rows(v, "v", (torch.float32,) + _BF16_LIKE, k)
+    kp, ks = _rows(k, "k", _BF16_OR_F32)
+    vp, vs = _rows(v, "v", _BF16_OR_F32, k)
     _on_device(k, "k")
+    tokens, heads, dim = k.shape
     d = k.device
-    _need(slots, "slots", tokens * 8, d)
-    _need(counters, "counters", 16, d)
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
-    _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim, _ptr(slots, "slots", (torch.int64,)),
-          tokens, kp, vp, ks, vs, W4_OUT_F32 if k.dtype == torch.float32 else W4_OUT_BF16,
-          _ptr(counters, "counters", (torch.int64,), True))
+    _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim,
+          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), tokens, kp, vp, ks, vs,
+          W4_OUT_F32 if k.dtype == torch.float32 else W4_OUT_BF16, _arg(counters, "counters", _I64, 16, d))
 
 
 def kv_cache_attention_workspace(seqs, heads, kv_heads, head_dim, table_width, page_size):
@@ -539,24 +563,19 @@ def kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_l
                        ws=None, counters=None, stream=None):
     """One new token's attention per sequence: q [seqs, heads, head_dim] over
     the cache rows that block_table [seqs, width] and seq_lens [seqs] name."""
-    seqs, heads, dim = q.shape
     qp, qs = _rows(q, "q", _BF16_LIKE)
     _on_device(q, "q")
+    seqs, heads, dim = q.shape
     d = q.device
     if block_table.dim() != 2 or block_table.shape[0] != seqs:
         raise ValueError("block_table must be [seqs=%d, width], got %s" % (seqs, tuple(block_table.shape)))
-    _need(block_table, "block_table", 0, d)
-    _need(seq_lens, "seq_lens", seqs * 4, d)
-    _need(out, "out", seqs * heads * dim * 2, d)
-    _need(lse, "lse", seqs * heads * 4, d)
-    _need(counters, "counters", 16, d)
-    _need(ws, "ws", 0, d)
+    n = seqs * heads
     cp, pages = _pages(cache, format, page_size, kv_heads, dim, d)
-    wp, wn = _ws(ws)
     _call("kv_cache_attention", d, stream, qp, seqs, qs, heads, cp, format, pages, page_size, kv_heads, dim,
-          _ptr(block_table, "block_table", (torch.int32,)), block_table.shape[1],
-          _ptr(seq_lens, "seq_lens", (torch.int32,)), scale, window, _ptr(out, "out", _BF16_LIKE),
-          _ptr(lse, "lse", (torch.float32,), True), _ptr(counters, "counters", (torch.int64,), True), wp, wn)
+          _arg(block_table, "block_table", _I32, 0, d), block_table.shape[1],
+          _arg(_given(seq_lens, "seq_lens"), "seq_lens", _I32, seqs * 4, d), scale, window,
+          _arg(_given(out, "out"), "out", _BF16_LIKE, n * dim * 2, d), _arg(lse, "lse", _F32, n * 4, d),
+          _arg(counters, "counters", _I64, 16, d), _arg(ws, "ws", _U8, 0, d), 0 if ws is None else ws.numel())
 
 
 # -------------------------------------------------------- allocating helpers
