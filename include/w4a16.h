@@ -617,8 +617,9 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  *   ws           kv_cache_attention_workspace(...) bytes, 16-byte aligned (it may
  *                be null where that is 0); its contents do not matter.  Calls
  *                that overlap in time need one each.
- * The results do not depend on what else runs (no atomics in the sums); they
- * depend on table_width through the split of the length.
+ * The results do not depend on what else runs (no atomics in the sums).  Their
+ * last bits depend on the batch: its lengths and table_width decide how the
+ * positions are split.
  * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, seqs * heads <
  * 2^24, table_width * page_size < 2^31, n_pages >= 1, window >= 0, finite scale.
  */

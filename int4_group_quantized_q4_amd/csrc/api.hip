@@ -825,7 +825,8 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
   const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
                                head_dim, counters);
   if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
-  w4::KvArgs a = kv_args(format, const_cast<void*>(cache), n_pages, page_size, kv_heads, head_dim, slots, tokens, counters);
+  w4::KvArgs a = kv_args(format, const_cast<void*>(cache), n_pages, page_size, kv_heads, head_dim, slots, tokens,
+                         counters);
   a.k_out = k;
   a.v_out = v;
   a.k_stride = k_stride;

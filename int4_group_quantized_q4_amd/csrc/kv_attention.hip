@@ -102,6 +102,12 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
+// 1 / l and the log of the sum of a row: l is 0 for an empty one; NaN passes on.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.f ? -INFINITY : l;
+}
+
 // The positions a sequence attends to, and their 32-token chunks.
 struct Span {
   int n, lo;          // positions [lo, n); all positions fit 31 bits
@@ -193,7 +199,8 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int want) {
 }
 
 template <int FMT, int NG, int R>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_per_simd(FMT, NG, R)))) kv_attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_per_simd(FMT, NG, R))))
+kv_attention_kernel(AttnArgs a) {
   typedef KvLayout<FMT, NG> L;
   constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
   constexpr int HPR = 16 / R;                         // heads per replica
@@ -238,8 +245,10 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     q[g] = u32x4{0u, 0u, 0u, 0u};
-    if (hl < live_heads && rep == g / GR)
-      q[g] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D + 32 * g + 8 * c);
+    if (hl < live_heads && rep == g / GR) {
+      const uint16_t* row = a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D;
+      q[g] = *reinterpret_cast<const u32x4*>(row + 32 * g + 8 * c);
+    }
   }
   // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
   float kbias[GR];
@@ -250,7 +259,10 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 #pragma unroll
       for (int r = 0; r < R; ++r)     // all but the replica's own are zero
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t += bf16_to_f32(q[r * GR + i][k] & 0xFFFFu) + __uint_as_float(q[r * GR + i][k] & 0xFFFF0000u);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = q[r * GR + i][k];
+          t += bf16_to_f32(w & 0xFFFFu) + __uint_as_float(w & 0xFFFF0000u);
+        }
       kbias[i] = -136.0f * column_sum(t);
     }
   }
@@ -316,7 +328,8 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
   auto load_scales = [&](bool v, u32x4 (&r)[2][NS1]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + scale_off + (uint32_t)next_tip[t] * (uint32_t)L::kScaleTileBytes;
+      const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + scale_off +
+                         (uint32_t)next_tip[t] * (uint32_t)L::kScaleTileBytes;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         if constexpr (FMT == W4_KV_Q4 && GR == 1) {
@@ -610,10 +623,10 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
       const int64_t row = (int64_t)seq * a.heads + h0 + h;
       const int dim = rd * BD + d;
       if (live == 1) {
-        const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // l: 0 for an empty row, NaN passes on
+        const float inv = inverse_sum(l);
         u32x2 w2 = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
         *reinterpret_cast<u32x2*>(a.out + row * L::D + dim) = w2;
-        if (a.lse && dim == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+        if (a.lse && dim == 0) a.lse[row] = log_sum(mx, l);
       } else {
         const int64_t pr = (int64_t)blockIdx.y * a.heads + h0 + h;
         *reinterpret_cast<f32x4*>(a.part_o + pr * L::D + dim) = o;
@@ -677,16 +690,20 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
   if (grp != 0) return;
 #pragma unroll
   for (int i = 1; i < GROUPS; ++i) o += s_o[i][d];
-  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-  *reinterpret_cast<u32x2*>(a.out + row * D + 4 * d) = u32x2{pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
-  if (a.lse && d == 0) a.lse[row] = l > 0.f ? (mx + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  const float inv = inverse_sum(l);
+  *reinterpret_cast<u32x2*>(a.out + row * D + 4 * d) =
+      u32x2{pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
+  if (a.lse && d == 0) a.lse[row] = log_sum(mx, l);
 }
 
+// Replicas of the heads, Q4 only (16 sequences of 32768 tokens, 8 heads a kv
+// head: 146 us with R = 1, 118 with 2).
 template <int FMT, int NG>
 void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
+  constexpr int MOST = FMT != W4_KV_Q4 ? 1 : NG < 4 ? 2 : 4, HALF = MOST < 2 ? 1 : 2;
   const int G = a.heads / a.kv_heads;
-  if (FMT == W4_KV_Q4 && NG >= 4 && G <= 4) kv_attention_kernel<FMT, NG, FMT == W4_KV_Q4 && NG >= 4 ? 4 : 1><<<grid, 64 * kWaves, 0, stream>>>(a);
-  else if (FMT == W4_KV_Q4 && G <= 8) kv_attention_kernel<FMT, NG, FMT == W4_KV_Q4 ? 2 : 1><<<grid, 64 * kWaves, 0, stream>>>(a);
+  if (G <= 16 / MOST) kv_attention_kernel<FMT, NG, MOST><<<grid, 64 * kWaves, 0, stream>>>(a);
+  else if (G <= 16 / HALF) kv_attention_kernel<FMT, NG, HALF><<<grid, 64 * kWaves, 0, stream>>>(a);
   else kv_attention_kernel<FMT, NG, 1><<<grid, 64 * kWaves, 0, stream>>>(a);
 }
 
@@ -741,7 +758,8 @@ Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int6
 // more items.
 size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
   const Plan p = plan_of(kMostTarget, seqs, heads, kv_heads, tokens);
-  return p.shares == 0 ? 0 : (size_t)(p.items * heads) * (size_t)(head_dim + 2) * sizeof(float) + (size_t)seqs * sizeof(int2);
+  if (p.shares == 0) return 0;
+  return (size_t)(p.items * heads) * (size_t)(head_dim + 2) * sizeof(float) + (size_t)seqs * sizeof(int2);
 }
 
 void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {

@@ -68,12 +68,14 @@ __device__ __forceinline__ u32x4 quad_transpose(u32x4 x, int q) {
   }
   return x;
 }
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 // Bytes: lane q's byte i <-> lane i's byte q.
 __device__ __forceinline__ uint32_t quad_transpose_bytes(uint32_t x, int q) {
   const uint32_t sel = (uint32_t)q | ((uint32_t)(q + 4) << 8);
   const uint32_t p01 = __builtin_amdgcn_perm(quad_lane<1>(x), quad_lane<0>(x), sel);
   const uint32_t p23 = __builtin_amdgcn_perm(quad_lane<3>(x), quad_lane<2>(x), sel);
-  return __builtin_amdgcn_perm(p23, p01, 0x05040100u);
+  return low_halves(p01, p23);
 }
 // Byte pairs: lane q's 8 bytes are pairs i (bytes 2i, 2i + 1); afterwards lane
 // q holds pair q of lanes 0..3, first bytes in word 0, second in word 1.
@@ -86,7 +88,7 @@ __device__ __forceinline__ u32x2 quad_pairs_to_planes(u32x2 x, int q) {
   const uint32_t b = 2u * (q & 1);   // [w0.b, w1.b, w0.b+1, w1.b+1]
   const uint32_t sel = b | ((b + 4) << 8) | ((b + 1) << 16) | ((b + 5) << 24);
   const uint32_t p01 = __builtin_amdgcn_perm(w1, w0, sel), p23 = __builtin_amdgcn_perm(w3, w2, sel);
-  return u32x2{__builtin_amdgcn_perm(p23, p01, 0x05040100u), __builtin_amdgcn_perm(p23, p01, 0x07060302u)};
+  return u32x2{low_halves(p01, p23), high_halves(p01, p23)};
 }
 // The reverse.
 __device__ __forceinline__ u32x2 quad_planes_to_pairs(u32x2 x, int q) {
@@ -95,7 +97,7 @@ __device__ __forceinline__ u32x2 quad_planes_to_pairs(u32x2 x, int q) {
   const uint32_t p1 = __builtin_amdgcn_perm(quad_lane<1>(x[1]), quad_lane<1>(x[0]), sel);
   const uint32_t p2 = __builtin_amdgcn_perm(quad_lane<2>(x[1]), quad_lane<2>(x[0]), sel);
   const uint32_t p3 = __builtin_amdgcn_perm(quad_lane<3>(x[1]), quad_lane<3>(x[0]), sel);
-  return u32x2{__builtin_amdgcn_perm(p1, p0, 0x05040100u), __builtin_amdgcn_perm(p3, p2, 0x05040100u)};
+  return u32x2{low_halves(p0, p1), low_halves(p2, p3)};
 }
 
 __device__ __forceinline__ uint32_t max_magnitude(u32x4 v) {
@@ -182,7 +184,8 @@ __device__ __forceinline__ uint32_t v_offset(int ch, int r, int t) {
 
 // One head's K or V row piece(s) of this lane into the cache.
 template <int FMT, int NG, bool V>
-__device__ __forceinline__ void write_row(const KvArgs& a, const Place& pl, const u32x4 (&x)[RowSplit<NG>::CPT], int head) {
+__device__ __forceinline__ void write_row(const KvArgs& a, const Place& pl, const u32x4 (&x)[RowSplit<NG>::CPT],
+                                          int head) {
   typedef KvLayout<FMT, NG> L;
   typedef RowSplit<NG> S;
   uint8_t* block = const_cast<uint8_t*>(pl.page) + (int64_t)head * 2 * a.block_bytes + (V ? a.block_bytes : 0);
@@ -204,8 +207,8 @@ __device__ __forceinline__ void write_row(const KvArgs& a, const Place& pl, cons
       } else if (pl.quads) {
         // lane q: pairs q of the 4 tokens, as [b][j]
         const u32x4 y = quad_transpose(x[i], pl.q);
-        const u32x4 w = {__builtin_amdgcn_perm(y[1], y[0], 0x05040100u), __builtin_amdgcn_perm(y[3], y[2], 0x05040100u),
-                         __builtin_amdgcn_perm(y[1], y[0], 0x07060302u), __builtin_amdgcn_perm(y[3], y[2], 0x07060302u)};
+        const u32x4 w = {low_halves(y[0], y[1]), low_halves(y[2], y[3]), high_halves(y[0], y[1]),
+                         high_halves(y[2], y[3])};
         *reinterpret_cast<u32x4*>(codes + v_offset<FMT, NG>(ch, pl.r, pl.q)) = w;
       } else if (pl.live) {
 #pragma unroll
@@ -379,14 +382,15 @@ __device__ __forceinline__ void load_row(const KvArgs& a, const Place& pl, int h
 template <int FMT, int NG, bool V, typename OUT>
 __device__ __forceinline__ void store_row(const KvArgs& a, const Place& pl, int head, const RowPiece<FMT, NG>& x) {
   typedef RowSplit<NG> S;
-  OUT* dst = reinterpret_cast<OUT*>(V ? a.v_out : a.k_out) + pl.tok * (V ? a.v_stride : a.k_stride) + (int64_t)head * (32 * NG);
+  OUT* dst = reinterpret_cast<OUT*>(V ? a.v_out : a.k_out) + pl.tok * (V ? a.v_stride : a.k_stride) +
+             (int64_t)head * (32 * NG);
 #pragma unroll
   for (int i = 0; i < S::CPT; ++i) {
     u32x4 w = x.w[i];
     if (V && pl.quads) {
       if constexpr (FMT == W4_KV_BF16) {   // [b][j] -> pairs of the 4 tokens, exchanged
-        w = quad_transpose(u32x4{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
-                                 __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)}, pl.q);
+        w = quad_transpose(u32x4{low_halves(w[0], w[2]), high_halves(w[0], w[2]), low_halves(w[1], w[3]),
+                                 high_halves(w[1], w[3])}, pl.q);
       } else if constexpr (FMT == W4_KV_E4M3) {
         const u32x2 y = quad_planes_to_pairs(u32x2{w[0], w[1]}, pl.q);
         w[0] = y[0];
@@ -459,7 +463,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvArgs a) {
 template <int FMT, int NG, int HB>
 void launch_heads(const KvArgs& a, bool write, int out_dtype, hipStream_t stream) {
   constexpr int H = HB > 0 ? HB : 1;
-  const dim3 grid((unsigned)((a.tokens + RowSplit<NG>::ROWS - 1) / RowSplit<NG>::ROWS), (a.kv_heads + H - 1) / H, HB > 0 ? 1 : 2);
+  const dim3 grid((unsigned)((a.tokens + RowSplit<NG>::ROWS - 1) / RowSplit<NG>::ROWS), (a.kv_heads + H - 1) / H,
+                  HB > 0 ? 1 : 2);
   if (write) kv_write_kernel<FMT, NG, HB><<<grid, kThreads, 0, stream>>>(a);
   else if (out_dtype == W4_OUT_F32) kv_read_kernel<FMT, NG, HB, float><<<grid, kThreads, 0, stream>>>(a);
   else kv_read_kernel<FMT, NG, HB, uint16_t><<<grid, kThreads, 0, stream>>>(a);

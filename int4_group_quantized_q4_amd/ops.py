@@ -538,8 +538,8 @@ def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=
     tokens, heads, dim = k.shape
     d = k.device
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
-    _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs, _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d),
-          format, cp, pages, page_size, heads, dim, _arg(counters, "counters", _I64, 16, d))
+    _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs,
+          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), format, cp, pages, page_size, heads, dim, _arg(counters, "counters", _I64, 16, d))
 
 
 def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=None):

@@ -95,12 +95,13 @@ def test_attention_refusals():
     need = lib.kv_cache_attention_workspace(4, 8, 2, 128, 8, 16)
     long = lib.kv_cache_attention_workspace(4, 8, 2, 128, 1024, 16)
     assert long > need >= 0
-    for b in (dict(q=None), dict(q=FAKE + 8), dict(qs=1016), dict(qs=1028), dict(cache=None), dict(fmt=3), dict(pages=0),
-              dict(table=None), dict(lens=None), dict(lens=FAKE + 2), dict(out=None), dict(out=FAKE + 8),
+    for b in (dict(q=None), dict(q=FAKE + 8), dict(qs=1016), dict(qs=1028), dict(cache=None), dict(fmt=3),
+              dict(pages=0), dict(table=None), dict(lens=None), dict(lens=FAKE + 2), dict(out=None), dict(out=FAKE + 8),
               dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")), dict(heads=0), dict(lse=FAKE + 2),
               dict(counters=FAKE + 4), dict(seqs=-1)):
         assert f(*changed(a, **b)) == w4.W4_ERR_ARG, b
-    for b in (dict(heads=7), dict(seqs=65535, heads=512, kv=32, qs=65536), dict(D=80), dict(page=48), dict(seqs=65536), dict(width=1 << 27), dict(heads=32768)):
+    for b in (dict(heads=7), dict(seqs=65535, heads=512, kv=32, qs=65536), dict(D=80), dict(page=48), dict(seqs=65536),
+              dict(width=1 << 27), dict(heads=32768)):
         assert f(*changed(a, **b)) == w4.W4_ERR_SHAPE, b
     for b in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=long - 1)):
         assert f(*changed(a, width=1024, **b)) == w4.W4_ERR_WORKSPACE, b

@@ -140,6 +140,32 @@ def test_head_layouts(form, kv_heads, group):
     s.check(*s.run())
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("group", [1, 4, 5, 8, 9, 16])
+def test_q4_head_replicas(D, group):
+    """The heads a kv head has decide how many matrix columns hold copies of them."""
+    s = Setup("q4", [90, 33, 0, 400], 2, group, D, 16, seed=D + group)
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+@pytest.mark.parametrize("seqs,kv_heads,width", [(150, 1, 40), (150, 1, 400), (300, 2, 40), (300, 2, 400), (70, 4, 400)])
+def test_many_sequences(form, seqs, kv_heads, width):
+    """Batches counted in several rounds of 64 lengths, batches that are not split at all, short and long tables."""
+    rng = np.random.default_rng(seqs)
+    lens = np.minimum((rng.random(seqs) ** 4 * 700).astype(int), 640)
+    lens[[0, 63, 64, seqs - 1]] = [640, 0, 1, 333]
+    s = Setup(form, lens, kv_heads, 1, 64, 16, seed=seqs + width, width=width, share=True, junk=False)
+    s.check(*s.run())
+
+
+def test_largest_pages():
+    """Pages of 65536 tokens and a table of 2^30 positions (the lengths' sum no longer counted in 32 bits)."""
+    s = Setup("e4m3", [70, 66000, 0, 65537], 1, 2, 64, 65536, seed=14, width=16384, share=True, junk=False)
+    s.check(*s.run())
+    s.check(*s.run(1000), 1000)
+
+
 @pytest.mark.parametrize("form", kv_layout.FORMATS)
 @pytest.mark.parametrize("window", [1, 15, 16, 33, 100, 4096])
 def test_windows(form, window):
@@ -290,15 +316,17 @@ def test_strided_queries_streams_and_graphs():
     for s in (a, b):
         qkv = torch.zeros(len(s.lens), (s.heads + 2) * s.D, dtype=torch.bfloat16, device=dev())
         qkv[:, s.D:(s.heads + 1) * s.D] = bf16_dev(s.q).flatten(1)
+        n = len(s.lens)
+        need = w4.kv_cache_attention_workspace(n, s.heads, s.kv_heads, s.D, s.width, s.page)
+        assert need > 0
         job = dict(q=qkv[:, s.D:(s.heads + 1) * s.D].unflatten(1, (s.heads, s.D)), lens=to_dev(s.lens),
-                   table=to_dev(s.table), out=torch.zeros(len(s.lens), s.heads, s.D, dtype=torch.bfloat16, device=dev()),
-                   lse=torch.zeros(len(s.lens), s.heads, device=dev()), stream=torch.cuda.Stream(), graph=torch.cuda.CUDAGraph(),
-                   ws=torch.empty(max(16, w4.kv_cache_attention_workspace(len(s.lens), s.heads, s.kv_heads, s.D, s.width,
-                                                                          s.page)), dtype=torch.uint8, device=dev()))
+                   table=to_dev(s.table), out=torch.zeros(n, s.heads, s.D, dtype=torch.bfloat16, device=dev()),
+                   lse=torch.zeros(n, s.heads, device=dev()), ws=torch.empty(need, dtype=torch.uint8, device=dev()),
+                   stream=torch.cuda.Stream(), graph=torch.cuda.CUDAGraph())
         torch.cuda.synchronize()
         with torch.cuda.graph(job["graph"], stream=job["stream"]):
-            w4.kv_cache_attention(job["q"], s.cache, FMT[s.form], s.page, s.kv_heads, job["table"], job["lens"], s.scale,
-                                  job["out"], 0, job["lse"], job["ws"])
+            w4.kv_cache_attention(job["q"], s.cache, FMT[s.form], s.page, s.kv_heads, job["table"], job["lens"],
+                                  s.scale, job["out"], 0, job["lse"], job["ws"])
         jobs.append(job)
     for step in range(3):
         for s, job in zip((a, b), jobs):
