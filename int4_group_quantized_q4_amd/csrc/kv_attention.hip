@@ -102,6 +102,12 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
+// The value N columns on (of 16).
+template <int N>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xF, 0xF, true));
+}
+
 // 1 / l and the log of the sum of a row: l is 0 for an empty one; NaN passes on.
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l; }
 __device__ __forceinline__ float log_sum(float m, float l) {
@@ -226,6 +232,11 @@ kv_attention_kernel(AttnArgs a) {
   } else {
     len = a.lens[seq];
   }
+  // the same in every lane: kept in scalar registers
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  index = __builtin_amdgcn_readfirstlane(index);
+  live = __builtin_amdgcn_readfirstlane(live);
+  len = __builtin_amdgcn_readfirstlane(len);
   const int G = (int)((unsigned)a.heads / (unsigned)a.kv_heads);
   const int live_heads = G - 16 * ht < 16 ? G - 16 * ht : 16;
   const int h0 = head * G + 16 * ht;     // first query head
@@ -313,10 +324,17 @@ kv_attention_kernel(AttnArgs a) {
   const uint8_t* next_p[2];   // page and head block of the tiles that are loaded
   int next_tip[2];            // their place in the page
   bool good[2], next_good[2];
-  // a uniform base and a 32-bit lane offset
+  // Loads take a uniform base and a 32-bit lane offset; hidden from the
+  // optimizer here, which would widen it outside the loop and add in vector
+  // registers.
+  auto lane_offset = [](uint32_t off) {
+    asm volatile("" : "+v"(off));
+    return off;
+  };
   auto load_unit = [&](bool v, int t, int u, u32x4& r) {
     const uint8_t* p = next_p[t] + (v ? a.block_bytes : 0) + (uint32_t)next_tip[t] * (uint32_t)L::kTileBytes;
-    const uint32_t off = (uint32_t)(u * 64 + lane) * L::kUnitBytes;
+    p += u * 64 * L::kUnitBytes;
+    const uint32_t off = lane_offset((uint32_t)lane * L::kUnitBytes);
     if constexpr (L::kUnitBytes == 16) {
       r = load16(p + off);
     } else {
@@ -333,11 +351,11 @@ kv_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         if constexpr (FMT == W4_KV_Q4 && GR == 1) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(p + (uint32_t)(8 * (c * NG + rep)));
+          const u32x2 w = *reinterpret_cast<const u32x2*>(p + lane_offset((uint32_t)(8 * (c * NG + rep))));
           r[t][0] = u32x4{w[0], w[1], 0u, 0u};
         } else {
           const uint32_t at = FMT == W4_KV_Q4 ? 8 * (c * NG + rep * GR) : 16 * c;
-          r[t][i] = *reinterpret_cast<const u32x4*>(p + at + 16u * i);
+          r[t][i] = *reinterpret_cast<const u32x4*>(p + 16 * i + lane_offset(at));
         }
       }
     }
@@ -375,6 +393,18 @@ kv_attention_kernel(AttnArgs a) {
     if constexpr (FMT == W4_KV_E4M3) return __uint_as_float(sr[0][j]);
     const uint32_t w = sr[NS > 0 ? i >> 1 : 0][2 * (i & 1) + (j >> 1)];
     return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
+  };
+
+  // Q4: takes the codes' +136 off the outputs.  Every 8 chunks: left to the
+  // end, the sums would grow to 136 times the values' own, and lose that much
+  // of their 24 bits where long flat attention averages the values out.
+  auto take_bias = [&]() {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[g][b] += vbias[g % GR];
+#pragma unroll
+    for (int i = 0; i < GR; ++i) vbias[i] = zero4;
   };
 
   // whether group g is the last of its unit in the order (i, r), g = r GR + i
@@ -425,8 +455,8 @@ kv_attention_kernel(AttnArgs a) {
       // Q4: over the replicas; in this order every replica gets the same bits
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (R >= 2) s4[j] += dpp_row_f32<0x128>(s4[j]);   // rotate by 8 columns
-        if constexpr (R >= 4) s4[j] += dpp_row_f32<0x124>(s4[j]);   // by 4
+        if constexpr (R >= 2) s4[j] += rotated<8>(s4[j]);
+        if constexpr (R >= 4) s4[j] += rotated<4>(s4[j]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -570,16 +600,17 @@ kv_attention_kernel(AttnArgs a) {
   if (ch < end) {
     fill_ids((2 * ch) >> tile_shift);
     load_k(ch);
+    // in this order, as in the loop: loads complete in order, and waiting for K
+    // must not mean waiting for V
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (!SHARED) load_v();
-    for (; ch < end; ch += kWaves) step(ch);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 1; ch < end; ch += kWaves, ++i) {
+      step(ch);
+      if (FMT == W4_KV_Q4 && (i & 7) == 0) take_bias();
+    }
   }
-
-  if constexpr (FMT == W4_KV_Q4) {
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) acc[g][b] += vbias[g % GR];
-  }
+  if constexpr (FMT == W4_KV_Q4) take_bias();
 
   // Join the waves: lane (c, n) holds, for group g, dimensions 32g + 8c + 2i + b.
   const float l_col = column_sum(l_run);
