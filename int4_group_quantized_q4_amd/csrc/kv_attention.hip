@@ -45,17 +45,11 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// Least waves per SIMD that the register allocator keeps: measured against one
-// more and one fewer, E4M3 48 ragged sequences of 8 x 128 55.6 (3) and 57 us
-// (2), Q4 16 x 32768 of 4 x 256 with 16 heads a kv head 192 (1) and 315 us (2,
-// spilling); the others within 3%.
-constexpr int waves_per_simd(int fmt, int ng, int r) {
-  if (ng == 2) return 4;
-  if (ng == 4) return fmt == W4_KV_E4M3 ? 3 : 2;
-  return fmt == W4_KV_Q4 && r == 1 ? 1 : 2;
-}
+// Least waves per SIMD that the register allocator keeps (none spills at these).
+constexpr int waves_per_simd(int fmt, int ng) { return ng == 2 ? 4 : ng == 4 && fmt == W4_KV_E4M3 ? 3 : 2; }
 
 constexpr int kWaves = 4;
+constexpr int kWideWaves = 8;       // of a workgroup that takes a short row alone
 constexpr int kChunk = 32;          // tokens per wave step
 constexpr float kSlack = 8.0f;       // of the softmax's running reference, in powers of two
 constexpr float kLog2e = 1.4426950408889634f;
@@ -204,15 +198,15 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int want) {
   return it;
 }
 
-template <int FMT, int NG, int R>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_per_simd(FMT, NG, R))))
+template <int FMT, int NG, int R, int W>
+__global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(waves_per_simd(FMT, NG))))
 kv_attention_kernel(AttnArgs a) {
   typedef KvLayout<FMT, NG> L;
   constexpr int BD = NG < 4 ? 32 * NG : 128;          // dimensions joined at a time
   constexpr int HPR = 16 / R;                         // heads per replica
   constexpr int GR = NG / R;                          // groups per replica
-  __shared__ float s_o[kWaves][16][BD + 4];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  __shared__ float s_o[W][16][BD + 4];
+  __shared__ float s_m[W][16], s_l[W][16];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, c = lane >> 4;
@@ -245,7 +239,7 @@ kv_attention_kernel(AttnArgs a) {
   const Span sp = span_of(a, len);
   if (a.counters && index == 0 && hrow == 0) {  // table entries outside the cache, once per entry
     const int p1 = (int)(((unsigned)sp.n + (1u << a.page_shift) - 1) >> a.page_shift);
-    for (int p = (sp.lo >> a.page_shift) + (int)threadIdx.x; p < p1; p += 64 * kWaves) {
+    for (int p = (sp.lo >> a.page_shift) + (int)threadIdx.x; p < p1; p += 64 * W) {
       const int id = table[p];
       if (id < 0 || id >= a.n_pages) atomicAdd(a.counters, 1ull);
     }
@@ -259,6 +253,7 @@ kv_attention_kernel(AttnArgs a) {
     if (hl < live_heads && rep == g / GR) {
       const uint16_t* row = a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D;
       q[g] = *reinterpret_cast<const u32x4*>(row + 32 * g + 8 * c);
+      if (a.scale < 0.f) q[g] ^= 0x80008000u;
     }
   }
   // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
@@ -286,7 +281,9 @@ kv_attention_kernel(AttnArgs a) {
 #pragma unroll
   for (int i = 0; i < (FMT == W4_KV_Q4 ? GR : 1); ++i) vbias[i] = zero4;
   float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's tokens only
-  const float scale2 = a.scale * kLog2e;
+  // The scores' scale enters with the exponent, where it has to be positive for
+  // the maximum: a negative one turned q round above, 0 is applied at once.
+  const float scale2 = a.scale == 0.f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
 
   const int size = (int)((unsigned)sp.chunks / (unsigned)live), rest = sp.chunks - size * live;
   const int begin = sp.first + index * size + (index < rest ? index : rest);
@@ -427,7 +424,8 @@ kv_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         float kb = kbias[i];
-        asm volatile("" : "+v"(kb));   // spread here, not kept in four registers each over the loop
+        // four registers each over the loop are too many for more than two of them
+        if constexpr (GR > 2) asm volatile("" : "+v"(kb));
         f32x4 d = {kb, kb, kb, kb};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -459,11 +457,14 @@ kv_attention_kernel(AttnArgs a) {
         if constexpr (R >= 4) s4[j] += rotated<4>(s4[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        p[4 * t + j] = s4[j] * (FMT == W4_KV_E4M3 ? scale2 * scale_of(ksr[t], 0, j) : scale2);
+      for (int j = 0; j < 4; ++j) p[4 * t + j] = FMT == W4_KV_E4M3 ? s4[j] * scale_of(ksr[t], 0, j) : s4[j];
+    }
+    if (a.scale == 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] *= 0.f;
     }
     __builtin_amdgcn_sched_barrier(0);   // not before the scores: K's registers are reused
-    const int next = ch + kWaves < end ? ch + kWaves : ch;   // the last chunk again, unused
+    const int next = ch + W < end ? ch + W : ch;   // the last chunk again, unused
     if constexpr (SHARED) {
       load_scales(true, vsr);
       find_tiles(next);
@@ -521,7 +522,7 @@ kv_attention_kernel(AttnArgs a) {
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
-    top = column_max(top);
+    top = column_max(top) * scale2;
     if (__any(top > m_run + kSlack)) {
       const float m_new = fmaxf(m_run, top);
       const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_run - m_new);
@@ -540,7 +541,7 @@ kv_attention_kernel(AttnArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(p[i] - m_use);
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], scale2, -m_use));
       sum += p[i];
     }
     l_run += sum;
@@ -605,7 +606,7 @@ kv_attention_kernel(AttnArgs a) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!SHARED) load_v();
     __builtin_amdgcn_sched_barrier(0);
-    for (int i = 1; ch < end; ch += kWaves, ++i) {
+    for (int i = 1; ch < end; ch += W, ++i) {
       step(ch);
       if (FMT == W4_KV_Q4 && (i & 7) == 0) take_bias();
     }
@@ -621,7 +622,7 @@ kv_attention_kernel(AttnArgs a) {
   __syncthreads();
   float m_all = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) m_all = fmaxf(m_all, s_m[w][n16]);
+  for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, s_m[w][n16]);
   const float mine = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_all);
   constexpr int ROUNDS = 32 * NG / BD;
 #pragma unroll
@@ -639,14 +640,14 @@ kv_attention_kernel(AttnArgs a) {
     }
     __syncthreads();
     // thread -> 4 dimensions of one head
-    for (int e = threadIdx.x; e < live_heads * (BD / 4); e += 64 * kWaves) {
+    for (int e = threadIdx.x; e < live_heads * (BD / 4); e += 64 * W) {
       const int h = e / (BD / 4), d = 4 * (e % (BD / 4));
       float mx = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w][h]);
       f32x4 o = zero4;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < W; ++w) {
         // a wave without a score has l = 0 (or NaN, which passes on)
         l += s_m[w][h] == -INFINITY ? s_l[w][h] : s_l[w][h] * __builtin_amdgcn_exp2f(s_m[w][h] - mx);
         o += *reinterpret_cast<const f32x4*>(&s_o[w][h][d]);
@@ -729,20 +730,26 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
 
 // Replicas of the heads, Q4 only (16 sequences of 32768 tokens, 8 heads a kv
 // head: 146 us with R = 1, 118 with 2).
-template <int FMT, int NG>
+template <int FMT, int NG, int W>
 void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MOST = FMT != W4_KV_Q4 ? 1 : NG < 4 ? 2 : 4, HALF = MOST < 2 ? 1 : 2;
   const int G = a.heads / a.kv_heads;
-  if (G <= 16 / MOST) kv_attention_kernel<FMT, NG, MOST><<<grid, 64 * kWaves, 0, stream>>>(a);
-  else if (G <= 16 / HALF) kv_attention_kernel<FMT, NG, HALF><<<grid, 64 * kWaves, 0, stream>>>(a);
-  else kv_attention_kernel<FMT, NG, 1><<<grid, 64 * kWaves, 0, stream>>>(a);
+  if (G <= 16 / MOST) kv_attention_kernel<FMT, NG, MOST, W><<<grid, 64 * W, 0, stream>>>(a);
+  else if (G <= 16 / HALF) kv_attention_kernel<FMT, NG, HALF, W><<<grid, 64 * W, 0, stream>>>(a);
+  else kv_attention_kernel<FMT, NG, 1, W><<<grid, 64 * W, 0, stream>>>(a);
+}
+
+template <int FMT, int W>
+void launch_dim(const AttnArgs& a, dim3 grid, hipStream_t stream) {
+  if (a.head_dim == 64) launch_fmt<FMT, 2, W>(a, grid, stream);
+  else if (a.head_dim == 128) launch_fmt<FMT, 4, W>(a, grid, stream);
+  else launch_fmt<FMT, 8, W>(a, grid, stream);
 }
 
 template <int FMT>
-void launch_dim(const AttnArgs& a, dim3 grid, hipStream_t stream) {
-  if (a.head_dim == 64) launch_fmt<FMT, 2>(a, grid, stream);
-  else if (a.head_dim == 128) launch_fmt<FMT, 4>(a, grid, stream);
-  else launch_fmt<FMT, 8>(a, grid, stream);
+void launch_waves(const AttnArgs& a, bool wide, dim3 grid, hipStream_t stream) {
+  if (wide) launch_dim<FMT, kWideWaves>(a, grid, stream);
+  else launch_dim<FMT, kWaves>(a, grid, stream);
 }
 
 int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_heads + 15) / 16; }
@@ -750,12 +757,12 @@ int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_head
 // How a call's positions are split.  The workgroups aimed at are those that
 // keep the memory busy: fewer and longer ones lose less in starts, ends and
 // partial results.  Measured (us; 256, 512, 768, 1024 workgroups): bf16 8 x
-// 32768 tokens of 8 x 128: 163, 166, 169, 170; bf16 32 x 8192 of 8 x 64: 83,
-// 90, 93, 92; bf16 16 x 8192 of 4 x 256: 92, 103, 113, 109; E4M3 32 x 32768
-// ragged of 8 x 128: 238, 141, 135, 130; E4M3 16 x 16384 of 8 x 128: 90, 92,
-// 95, 94; E4M3 16 x 16384 of 4 x 256: 91, 94, 103, 96; Q4 16 x 32768 of 8 x
-// 128: 149, 118, 114, 116; Q4 32 x 16384 of 8 x 64: 156, 100, 83, 77; Q4 16 x
-// 32768 of 4 x 256: 153, 106, 122, 111.
+// 32768 tokens of 8 x 128: 161, 173, 173, 179; bf16 32 x 8192 of 8 x 64: 85,
+// 90, 92, 92; bf16 16 x 8192 of 4 x 256: 92, 95, 97, 102; E4M3 32 x 32768
+// ragged of 8 x 128: 152, 141, 133, 132; E4M3 16 x 16384 of 8 x 128: 89, 92,
+// 96, 94; E4M3 16 x 16384 of 4 x 256: 91, 93, 101, 99; Q4 16 x 32768 of 8 x
+// 128: 153, 116, 112, 114; Q4 32 x 16384 of 8 x 64: 112, 82, 69, 68; Q4 16 x
+// 32768 of 4 x 256: 160, 108, 126, 111.
 int64_t target_of(int32_t format, int32_t head_dim) {
   if (format == W4_KV_BF16) return 256;
   if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 768;
@@ -765,6 +772,7 @@ constexpr int64_t kMostTarget = 1024;
 
 struct Plan {
   int shares;     // 0: one workgroup per sequence and head row
+  bool wide;      // of 8 waves
   int64_t items;  // at most
 };
 
@@ -772,15 +780,26 @@ struct Plan {
 // head rows is split too where a long sequence among short ones would outlast
 // the others (over kUnsplit tokens), unless counting the items takes too long.
 constexpr int64_t kUnsplit = 4096, kMostCounted = 256;
-Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int64_t tokens) {
+
+// With too few rows to fill the card, splitting a short row costs more (a
+// second launch and its start) than one workgroup of 8 waves takes for it.  In
+// tokens x dimensions (us in a graph, split against wide): Q4 1 x 500 tokens of
+// 8 x 128: 9.0, 7.9; 1 x 1000: 9.3, 10.8; 1 x 250 of 4 x 256: 11.0, 10.1; 1 x
+// 500: 11.1, 12.6; with more rows up to twice as far (12 x 1000 of 8 x 128:
+// 13.7, 11.7; bf16 19.3, 17.0; Q4 12 x 2000: 16.0, 17.9).
+constexpr int64_t kWide = 512 * 128, kWideManyRows = 2 * kWide, kManyRows = 64;
+
+Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
   const int64_t hrows = kv_heads * head_tiles_of(heads, kv_heads);
   const int64_t most = (tokens + kWaves * kChunk - 1) / (kWaves * kChunk);   // items a sequence can have
   const bool enough = seqs * hrows * 3 >= target * 2;
-  if (most <= 1 || (enough && (tokens <= kUnsplit || seqs > kMostCounted))) return {0, seqs};
+  if (most <= 1 || (enough && (tokens <= kUnsplit || seqs > kMostCounted))) return {0, false, seqs};
+  const int64_t wide = seqs * hrows >= kManyRows ? kWideManyRows : kWide;
+  if (!enough && tokens * head_dim <= wide) return {0, true, seqs};
   int64_t shares = (target + hrows - 1) / hrows;
   if (shares < seqs) shares = seqs;
   const int64_t items = shares + seqs;
-  return {(int)shares, items < seqs * most ? items : seqs * most};
+  return {(int)shares, false, items < seqs * most ? items : seqs * most};
 }
 
 }  // namespace
@@ -788,7 +807,7 @@ Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int6
 // For any format and window: a smaller target or fewer attended tokens give no
 // more items.
 size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
-  const Plan p = plan_of(kMostTarget, seqs, heads, kv_heads, tokens);
+  const Plan p = plan_of(kMostTarget, seqs, heads, kv_heads, head_dim, tokens);
   if (p.shares == 0) return 0;
   return (size_t)(p.items * heads) * (size_t)(head_dim + 2) * sizeof(float) + (size_t)seqs * sizeof(int2);
 }
@@ -797,15 +816,15 @@ void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {
   a.head_tiles = (int32_t)head_tiles_of(a.heads, a.kv_heads);
   int64_t tokens = a.table_width << a.page_shift;
   if (a.window > 0 && tokens > a.window + kChunk) tokens = a.window + kChunk;
-  const Plan p = plan_of(target_of(a.format, a.head_dim), a.seqs, a.heads, a.kv_heads, tokens);
+  const Plan p = plan_of(target_of(a.format, a.head_dim), a.seqs, a.heads, a.kv_heads, a.head_dim, tokens);
   a.shares = p.shares;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + p.items * a.heads * a.head_dim;
   a.part_plan = reinterpret_cast<int2*>(a.part_ml + p.items * a.heads * 2);
   const dim3 grid(a.kv_heads * a.head_tiles, (unsigned)p.items);
-  if (a.format == W4_KV_BF16) launch_dim<W4_KV_BF16>(a, grid, stream);
-  else if (a.format == W4_KV_E4M3) launch_dim<W4_KV_E4M3>(a, grid, stream);
-  else launch_dim<W4_KV_Q4>(a, grid, stream);
+  if (a.format == W4_KV_BF16) launch_waves<W4_KV_BF16>(a, p.wide, grid, stream);
+  else if (a.format == W4_KV_E4M3) launch_waves<W4_KV_E4M3>(a, p.wide, grid, stream);
+  else launch_waves<W4_KV_Q4>(a, p.wide, grid, stream);
   if (a.shares > 0) {
     const dim3 rows(a.heads, (unsigned)a.seqs);
     if (a.head_dim == 64) kv_join_kernel<2><<<rows, 256, 0, stream>>>(a);

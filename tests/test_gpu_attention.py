@@ -106,7 +106,7 @@ class Setup:
                 continue
             qa = np.abs(oracle.bf16_bits_to_f64(self.q[i]))
             for h in range(self.heads):
-                S = self.scale * (km[:, h // self.group] @ qa[h])
+                S = abs(self.scale) * (km[:, h // self.group] @ qa[h])
                 ep = np.max((self.D + 8) * 2.0 ** -23 * S + 2.0 ** -22 * np.abs(s[h])) + 2.0 ** -22
                 el = ep + (n + 40) * 2.0 ** -23
                 A = p[h] @ vm[:, h // self.group]
@@ -285,6 +285,15 @@ def test_large_scores():
     """Scores of several hundred: only the largest position counts, and nothing overflows."""
     s = Setup("bf16", [200], 1, 4, 64, 16, seed=8)
     s.scale = 40.0
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
+def test_scales(form, scale):
+    """Any finite scale: zero averages the values, a negative one turns the order round."""
+    s = Setup(form, [45, 170, 1], 2, 3, 64, 16, seed=15)
+    s.scale = scale
     s.check(*s.run())
 
 
