@@ -555,7 +555,8 @@ int w8a8_add_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const
  *
  * A slot is page * page_size + position in the page.
  * Common limits: head_dim 64, 128 or 256; page_size a power of two from 16 to
- * 65536; kv_heads <= 1024; n_pages < 2^31 (W4_ERR_SHAPE).
+ * 65536; kv_heads <= 1024; n_pages < 2^31 and at most 2^48 bytes
+ * (W4_ERR_SHAPE).
  */
 enum { W4_KV_BF16 = 0, W4_KV_E4M3 = 1, W4_KV_Q4 = 2 };
 
@@ -576,7 +577,8 @@ size_t kv_cache_page_bytes(int32_t format, int32_t page_size, int32_t kv_heads, 
  *              them): counters[0] += tokens whose slot lies past the cache
  *              (skipped too), counters[1] += rows (E4M3) or groups (Q4) with a
  *              NaN or an infinity
- * Requires tokens < 2^28.
+ * The cache may not overlap k, v or slots (W4_ERR_ARG).
+ * Requires tokens < 2^27, tokens * stride <= 2^48.
  */
 int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
                    const int64_t* slots, int32_t format, void* cache, int64_t n_pages, int32_t page_size,
@@ -588,7 +590,9 @@ int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t
  * negative slots and of slots past the cache (counted as above) are left as
  * they were; a slot may be named any number of times.
  *   k, v  out [tokens] rows of kv_heads*head_dim of out_dtype, strides in
- *         elements (multiples of 8), 16-byte aligned, not overlapping
+ *         elements (multiples of 8), 16-byte aligned; they may be slices of one
+ *         buffer, but no row may overlap another, the cache or slots
+ *         (W4_ERR_ARG).  Limits as above.
  */
 int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads,
                   int32_t head_dim, const int64_t* slots, int64_t tokens, void* k, void* v, int64_t k_stride,
@@ -603,8 +607,11 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  *   s_t = scale * (q . k_t)
  *   out = sum_t softmax(s)_t v_t,   lse = log sum_t exp(s_t)
  * over the dequantized (unrounded) rows, in fp32; out is rounded once.  A
- * sequence without positions gives out = 0 and lse = -infinity.  Cache rows
- * outside the positions may hold anything.  Lengths are cut to [0,
+ * sequence without positions, and a head whose scores are all -infinity, give
+ * out = 0 and lse = -infinity; a NaN or +infinity among the scores gives NaN.
+ * An infinite value (W4_KV_BF16) makes its dimension infinite or NaN, as the
+ * probabilities enter as the sum of two terms.  Cache rows outside the
+ * positions may hold anything.  Lengths are cut to [0,
  * table_width * page_size]; positions in pages outside [0, n_pages) count as
  * absent.
  *   q            in  [seqs] rows of heads*head_dim bf16, q_stride elements apart
@@ -621,7 +628,8 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  * last bits depend on the batch: its lengths and table_width decide how the
  * positions are split.
  * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, seqs * heads <
- * 2^24, table_width * page_size < 2^31, n_pages >= 1, window >= 0, finite scale.
+ * 2^24, table_width * page_size < 2^31, n_pages >= 1, window >= 0, |scale| <=
+ * 2^64.  No output (ws included) may overlap another argument (W4_ERR_ARG).
  */
 size_t kv_cache_attention_workspace(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     int64_t table_width, int32_t page_size);

@@ -757,6 +757,7 @@ static int check_kv_shape(int32_t format, int64_t n_pages, int32_t page_size, in
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return W4_ERR_SHAPE;
   if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return W4_ERR_SHAPE;
   if (kv_heads > 1024 || n_pages > INT32_MAX) return W4_ERR_SHAPE;
+  if (n_pages > ((int64_t)1 << 48) / (w4::kv_block_bytes(format, page_size, head_dim) * 2 * kv_heads)) return W4_ERR_SHAPE;
   return W4_OK;
 }
 
@@ -783,31 +784,55 @@ static w4::KvArgs kv_args(int32_t format, void* cache, int64_t n_pages, int32_t 
 }
 
 // Rows of the caller's k / v / q: 16-byte aligned, `stride` elements apart.
-static int check_rows(const void* p, int64_t stride, int64_t width) {
+static int check_rows(const void* p, int64_t rows, int64_t stride, int64_t width) {
   if (!p || !aligned16(p)) return W4_ERR_ARG;
   if (stride < width || stride % 8 != 0) return W4_ERR_ARG;
-  return W4_OK;
+  return rows > 0 && stride > ((int64_t)1 << 48) / rows ? W4_ERR_SHAPE : W4_OK;
+}
+
+static size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int64_t element) {
+  return (size_t)(((rows - 1) * stride + width) * element);
+}
+
+// Two sets of rows that share memory; rows of one buffer side by side (one
+// stride, a row's width or more apart) do not.
+static bool rows_overlap(const void* p, int64_t ps, const void* q, int64_t qs, int64_t rows, int64_t width,
+                         int64_t element) {
+  if (!overlap(p, rows_bytes(rows, ps, width, element), q, rows_bytes(rows, qs, width, element))) return false;
+  if (ps != qs) return true;
+  const int64_t pitch = ps * element, bytes = width * element;
+  const int64_t apart = (int64_t)((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) % (uintptr_t)pitch);
+  const int64_t back = q < p ? (int64_t)((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) % (uintptr_t)pitch)
+                             : pitch - apart;
+  const int64_t ahead = q < p ? pitch - back : apart;
+  return ahead < bytes || back < bytes;
 }
 
 static int check_kv_rows(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
                          const int64_t* slots, int32_t format, const void* cache, int64_t n_pages, int32_t page_size,
-                         int32_t kv_heads, int32_t head_dim, const unsigned long long* counters) {
+                         int32_t kv_heads, int32_t head_dim, const unsigned long long* counters, int64_t element) {
   if (tokens < 0) return W4_ERR_ARG;
   int st = check_kv_shape(format, n_pages, page_size, kv_heads, head_dim);
   if (st != W4_OK) return st;
-  if (tokens >= ((int64_t)1 << 28)) return W4_ERR_SHAPE;
+  if (tokens >= ((int64_t)1 << 27)) return W4_ERR_SHAPE;   // fewer than 2^32 threads along the tokens
   if (tokens == 0) return kLayerEmpty;
   if (!slots || !aligned8(slots) || !cache || !aligned16(cache) || (counters && !aligned8(counters))) return W4_ERR_ARG;
-  st = check_rows(k, k_stride, (int64_t)kv_heads * head_dim);
+  const int64_t width = (int64_t)kv_heads * head_dim;
+  st = check_rows(k, tokens, k_stride, width);
+  if (st == W4_OK) st = check_rows(v, tokens, v_stride, width);
   if (st != W4_OK) return st;
-  return check_rows(v, v_stride, (int64_t)kv_heads * head_dim);
+  const size_t held = (size_t)n_pages * kv_cache_page_bytes(format, page_size, kv_heads, head_dim);
+  if (overlap(cache, held, k, rows_bytes(tokens, k_stride, width, element)) ||
+      overlap(cache, held, v, rows_bytes(tokens, v_stride, width, element)) || overlap(cache, held, slots, tokens * 8))
+    return W4_ERR_ARG;
+  return W4_OK;
 }
 
 int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
                    const int64_t* slots, int32_t format, void* cache, int64_t n_pages, int32_t page_size,
                    int32_t kv_heads, int32_t head_dim, unsigned long long* counters, hipStream_t stream) {
   const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
-                               head_dim, counters);
+                               head_dim, counters, 2);
   if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
   w4::KvArgs a = kv_args(format, cache, n_pages, page_size, kv_heads, head_dim, slots, tokens, counters);
   a.k = k;
@@ -822,9 +847,14 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
                   int32_t head_dim, const int64_t* slots, int64_t tokens, void* k, void* v, int64_t k_stride,
                   int64_t v_stride, int32_t out_dtype, unsigned long long* counters, hipStream_t stream) {
   if (out_dtype != W4_OUT_BF16 && out_dtype != W4_OUT_F32) return W4_ERR_ARG;
+  const int64_t element = out_dtype == W4_OUT_F32 ? 4 : 2, width = (int64_t)kv_heads * head_dim;
   const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
-                               head_dim, counters);
+                               head_dim, counters, element);
   if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
+  if (rows_overlap(k, k_stride, v, v_stride, tokens, width, element) ||
+      overlap(slots, tokens * 8, k, rows_bytes(tokens, k_stride, width, element)) ||
+      overlap(slots, tokens * 8, v, rows_bytes(tokens, v_stride, width, element)))
+    return W4_ERR_ARG;
   w4::KvArgs a = kv_args(format, const_cast<void*>(cache), n_pages, page_size, kv_heads, head_dim, slots, tokens,
                          counters);
   a.k_out = k;
@@ -861,17 +891,33 @@ int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_
   if (st != W4_OK) return st;
   st = check_attention(seqs, heads, kv_heads, head_dim, table_width, page_size);
   if (st != W4_OK) return st;
-  if (window < 0 || !(scale > -INFINITY && scale < INFINITY)) return W4_ERR_ARG;
+  if (window < 0 || !(scale >= -0x1p64f && scale <= 0x1p64f)) return W4_ERR_ARG;
   if (seqs == 0) return W4_OK;
   if (n_pages < 1 || !cache || !seq_lens || !out || (table_width > 0 && !block_table)) return W4_ERR_ARG;
   if (!aligned16(cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (counters && !aligned8(counters)))
     return W4_ERR_ARG;
-  st = check_rows(q, q_stride, (int64_t)heads * head_dim);
+  st = check_rows(q, seqs, q_stride, (int64_t)heads * head_dim);
   if (st != W4_OK) return st;
   const size_t need = kv_cache_attention_workspace(seqs, heads, kv_heads, head_dim, table_width, page_size);
   if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return W4_ERR_WORKSPACE;
+  // the workgroups of a call read and write in no order: no output may lie in another argument
+  struct Part {
+    const void* p;
+    size_t n;
+  };
+  const size_t rows = (size_t)seqs * (size_t)heads;
+  const Part parts[] = {{out, rows * head_dim * 2},
+                        {lse, rows * 4},
+                        {need ? ws : nullptr, need},
+                        {q, rows_bytes(seqs, q_stride, (int64_t)heads * head_dim, 2)},
+                        {cache, (size_t)n_pages * kv_cache_page_bytes(format, page_size, kv_heads, head_dim)},
+                        {block_table, (size_t)seqs * (size_t)table_width * 4},
+                        {seq_lens, (size_t)seqs * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(parts[i].p, parts[i].n, parts[j].p, parts[j].n)) return W4_ERR_ARG;
   w4::AttnArgs a{};
   a.q = q;
   a.seqs = seqs;

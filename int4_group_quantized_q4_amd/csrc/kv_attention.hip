@@ -815,7 +815,7 @@ size_t kv_attention_workspace_bytes(int64_t seqs, int32_t heads, int32_t kv_head
 void launch_kv_attention(AttnArgs a, void* ws, hipStream_t stream) {
   a.head_tiles = (int32_t)head_tiles_of(a.heads, a.kv_heads);
   int64_t tokens = a.table_width << a.page_shift;
-  if (a.window > 0 && tokens > a.window + kChunk) tokens = a.window + kChunk;
+  if (a.window > 0 && tokens > (int64_t)a.window + kChunk) tokens = (int64_t)a.window + kChunk;
   const Plan p = plan_of(target_of(a.format, a.head_dim), a.seqs, a.heads, a.kv_heads, a.head_dim, tokens);
   a.shares = p.shares;
   a.part_o = static_cast<float*>(ws);

@@ -539,7 +539,8 @@ def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=
     d = k.device
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs,
-          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), format, cp, pages, page_size, heads, dim, _arg(counters, "counters", _I64, 16, d))
+          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), format, cp, pages, page_size, heads, dim,
+          _arg(counters, "counters", _I64, 16, d))
 
 
 def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=None):
@@ -704,19 +705,32 @@ def fp8_moe_layer(x, logits, k, I, w1q, w1_scale, w2q, w2_scale, activation=W4_E
     return y, views
 
 
+def _allocating(device, stream):
+    """The context in which a call on `stream` gets its outputs and workspace:
+    with that stream current, so that their memory is free on it, and is given
+    to another stream's work only as torch's allocator allows."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def add_rmsnorm(x, residual, weight, eps, weight_offset=0.0, stream=None):
     """(y, r): the norm and, with a residual, the sum it was taken of (else x)."""
-    y = torch.empty_like(x)
-    r = torch.empty_like(x) if residual is not None else None
+    with _allocating(x.device, stream):
+        y = torch.empty_like(x)
+        r = torch.empty_like(x) if residual is not None else None
     w4a16_add_rmsnorm(x, residual, weight, eps, r, y, weight_offset, stream)
     return y, x if r is None else r
 
 
 def add_rmsnorm_quantize(x, residual, weight, eps, weight_offset=0.0, stream=None):
     """(q, scale, r): as add_rmsnorm, with E4M3 codes and row scales."""
-    q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    r = torch.empty_like(x) if residual is not None else None
+    with _allocating(x.device, stream):
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        r = torch.empty_like(x) if residual is not None else None
     w8a8_add_rmsnorm_quantize(x, residual, weight, eps, r, q, scale, weight_offset, stream)
     return q, scale, x if r is None else r
 
@@ -730,10 +744,11 @@ def kv_cache(n_pages, format, page_size, kv_heads, head_dim, device="cuda"):
 def kv_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, window=0, stream=None):
     """kv_cache_attention with freshly allocated outputs; returns (out, lse)."""
     seqs, heads, dim = q.shape
-    out = torch.empty(seqs, heads, dim, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(seqs, heads, dtype=torch.float32, device=q.device)
     need = kv_cache_attention_workspace(seqs, heads, kv_heads, dim, block_table.shape[1], page_size)
-    ws = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+    with _allocating(q.device, stream):
+        out = torch.empty(seqs, heads, dim, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(seqs, heads, dtype=torch.float32, device=q.device)
+        ws = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
     kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, out, window, lse, ws,
                        stream=stream)
     return out, lse

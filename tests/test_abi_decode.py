@@ -68,40 +68,54 @@ def test_page_bytes_refusals():
 
 def test_write_and_read_refusals():
     lib = _lib.lib()
-    a = dict(k=FAKE, v=FAKE + BIG, tokens=4, ks=256, vs=256, slots=FAKE, fmt=2, cache=FAKE, pages=4, page=16, heads=2,
+    a = dict(k=FAKE, v=FAKE + BIG, tokens=4, ks=256, vs=256, slots=FAKE + 2 * BIG, fmt=2, cache=FAKE + 3 * BIG, pages=4, page=16, heads=2,
              D=128, counters=None, st=None)
     w = lib.kv_cache_write
-    bad = [dict(tokens=-1), dict(ks=248), dict(ks=260), dict(vs=128), dict(slots=None), dict(slots=FAKE + 4),
-           dict(cache=None), dict(cache=FAKE + 8), dict(k=None), dict(v=FAKE + 8), dict(fmt=5), dict(pages=-1),
+    bad = [dict(tokens=-1), dict(ks=248), dict(ks=260), dict(vs=128), dict(slots=None), dict(slots=FAKE + 2 * BIG + 4),
+           dict(cache=None), dict(cache=FAKE + 3 * BIG + 8), dict(cache=FAKE), dict(cache=FAKE + BIG),
+           dict(cache=FAKE + 2 * BIG), dict(slots=FAKE + 3 * BIG + 1024), dict(k=None), dict(v=FAKE + 8), dict(fmt=5), dict(pages=-1),
            dict(counters=FAKE + 4)]
     for b in bad:
         assert w(*changed(a, **b)) == w4.W4_ERR_ARG, b
-    for b in (dict(tokens=1 << 28), dict(page=20), dict(D=96), dict(heads=2000), dict(pages=1 << 31)):
+    for b in (dict(tokens=1 << 28), dict(tokens=1 << 27), dict(page=20), dict(D=96), dict(heads=2000),
+              dict(pages=1 << 31), dict(pages=1 << 30, page=65536), dict(ks=1 << 47)):
         assert w(*changed(a, **b)) == w4.W4_ERR_SHAPE, b
     assert w(*changed(a, tokens=0, k=None, v=None, slots=None, cache=None)) == w4.W4_OK
-    r = dict(cache=FAKE, fmt=2, pages=4, page=16, heads=2, D=128, slots=FAKE, tokens=4, k=FAKE, v=FAKE + BIG, ks=256,
+    r = dict(cache=FAKE + 3 * BIG, fmt=2, pages=4, page=16, heads=2, D=128, slots=FAKE + 2 * BIG, tokens=4, k=FAKE, v=FAKE + BIG, ks=256,
              vs=256, out=0, counters=None, st=None)
     f = lib.kv_cache_read
-    for b in (dict(out=2), dict(cache=None), dict(slots=None), dict(k=FAKE + 8), dict(vs=0), dict(fmt=-1)):
+    # rows of k in rows of v: the same, shifted, between v's rows but too near, with another stride; k in the cache, slots
+    over = [dict(v=FAKE), dict(v=FAKE + 496), dict(v=FAKE - 16), dict(ks=512, vs=512, v=FAKE + 496),
+            dict(ks=512, vs=512, v=FAKE - 528 + 1024), dict(ks=512, vs=512, v=FAKE + 1024 + 512 + 16),
+            dict(ks=512, vs=1024, v=FAKE + 512), dict(k=FAKE + 3 * BIG + 64), dict(v=FAKE + 3 * BIG - 2048 + 16),
+            dict(k=FAKE + 2 * BIG), dict(out=1, v=FAKE + 512)]
+    for b in [dict(out=2), dict(cache=None), dict(slots=None), dict(k=FAKE + 8), dict(vs=0), dict(fmt=-1)] + over:
         assert f(*changed(r, **b)) == w4.W4_ERR_ARG, b
     assert f(*changed(r, tokens=0)) == w4.W4_OK
 
 
 def test_attention_refusals():
     lib = _lib.lib()
-    a = dict(q=FAKE, seqs=4, qs=1024, heads=8, cache=FAKE, fmt=1, pages=4, page=16, kv=2, D=128, table=FAKE, width=8,
-             lens=FAKE, scale=0.1, window=0, out=FAKE, lse=None, counters=None, ws=FAKE, ws_bytes=1 << 30, st=None)
+    at = lambda i: FAKE + i * BIG
+    a = dict(q=FAKE, seqs=4, qs=1024, heads=8, cache=at(1), fmt=1, pages=4, page=16, kv=2, D=128, table=at(2), width=8,
+             lens=at(3), scale=0.1, window=0, out=at(4), lse=None, counters=None, ws=at(5), ws_bytes=1 << 30, st=None)
     f = lib.kv_cache_attention
     need = lib.kv_cache_attention_workspace(4, 8, 2, 128, 8, 16)
     long = lib.kv_cache_attention_workspace(4, 8, 2, 128, 1024, 16)
     assert long > need >= 0
     for b in (dict(q=None), dict(q=FAKE + 8), dict(qs=1016), dict(qs=1028), dict(cache=None), dict(fmt=3),
-              dict(pages=0), dict(table=None), dict(lens=None), dict(lens=FAKE + 2), dict(out=None), dict(out=FAKE + 8),
-              dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")), dict(heads=0), dict(lse=FAKE + 2),
-              dict(counters=FAKE + 4), dict(seqs=-1)):
+              dict(pages=0), dict(table=None), dict(lens=None), dict(lens=at(3) + 2), dict(out=None),
+              dict(out=at(4) + 8), dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")),
+              dict(scale=2.0 ** 65), dict(scale=-2.0 ** 65), dict(heads=0), dict(lse=at(6) + 2),
+              dict(counters=FAKE + 4), dict(seqs=-1),
+              # outputs in other arguments
+              dict(out=FAKE), dict(out=FAKE + 4 * 2048 - 16), dict(out=at(1) + 128), dict(out=at(2)), dict(out=at(3)),
+              dict(lse=at(4) + 64), dict(lse=at(1)), dict(width=1024, ws=FAKE), dict(width=1024, ws=at(4)),
+              dict(width=1024, ws=at(2) + 4096), dict(width=1024, ws=at(1) - 4096)):
         assert f(*changed(a, **b)) == w4.W4_ERR_ARG, b
     for b in (dict(heads=7), dict(seqs=65535, heads=512, kv=32, qs=65536), dict(D=80), dict(page=48), dict(seqs=65536),
-              dict(width=1 << 27), dict(heads=32768)):
+              dict(width=1 << 27), dict(heads=32768), dict(pages=1 << 30, page=65536),
+              dict(qs=1 << 47)):
         assert f(*changed(a, **b)) == w4.W4_ERR_SHAPE, b
     for b in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=long - 1)):
         assert f(*changed(a, width=1024, **b)) == w4.W4_ERR_WORKSPACE, b

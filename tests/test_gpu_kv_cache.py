@@ -181,3 +181,25 @@ def test_graph_replay(form):
         for got, x in ((ko, kb), (vo, vb)):
             want = decode.row_values(*decode.cache_rows(x, form), form)
             assert np.array_equal(bits_host(got), oracle.bf16_from_f32(want.astype(np.float32)))
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+def test_rows_of_one_buffer(form):
+    """k and v as slices of one buffer, written from it and read back into it: the values between them stay."""
+    tokens, heads, D, page = 37, 2, 64, 16
+    rng = np.random.default_rng(77)
+    k, v = rnd(rng, tokens, heads, D), rnd(rng, tokens, heads, D)
+    qkv = torch.full((tokens, 5 * heads * D), 3.0, dtype=torch.bfloat16, device=dev())
+    view = lambda i: qkv[:, i * heads * D:(i + 1) * heads * D].unflatten(1, (heads, D))
+    view(1).copy_(bf16_dev(k))
+    view(3).copy_(bf16_dev(v))
+    cache = empty_cache(form, 4, page, heads, D)
+    slots = to_dev(rng.permutation(4 * page)[:tokens].astype(np.int64))
+    w4.kv_cache_write(view(1), view(3), slots, FMT[form], page, cache)
+    w4.kv_cache_read(cache, FMT[form], page, slots, view(4), view(2))
+    torch.cuda.synchronize()
+    want = [oracle.bf16_from_f32(decode.row_values(*decode.cache_rows(x, form), form).astype(np.float32)) for x in (k, v)]
+    assert np.array_equal(bits_host(view(4).contiguous()), want[0])
+    assert np.array_equal(bits_host(view(2).contiguous()), want[1])
+    assert np.array_equal(bits_host(view(1).contiguous()), k) and np.array_equal(bits_host(view(3).contiguous()), v)
+    assert (view(0) == 3).all()
