@@ -417,28 +417,28 @@ def w8a8_moe_layer(x, logits, k, I, w1q, w1_scale, w2q, w2_scale, activation, y,
 
 # ------------------------------------------------- around the matmuls
 def _call(name, device, stream, *args):
-    """One library call on `device` (the launch needs it current) and on
-    `stream` (default: that device's current stream)."""
-    index = device.index
-    if index != torch._C._cuda_getDevice():
+    """One library call on device number `device` (the launch needs it current)
+    and on `stream` (default: that device's current stream)."""
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _call(name, device, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
     st = getattr(_lib._lib or lib(), name)(*args, s)
     if st != _lib.W4_OK:
         check(st, name)
 
 
 def _arg(t, name, dtypes, nbytes, device):
-    """Pointer of a contiguous tensor of at least nbytes on `device` (None
-    passes as a null pointer); the checks' own errors where one fails."""
+    """Pointer of a contiguous tensor of at least nbytes on device number
+    `device` (-1: the CPU, which is refused; None passes as a null pointer);
+    the checks' own errors where one fails.  Small calls wait for these checks,
+    so each is one cheap query (0.4 us an argument with whole devices compared)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.nbytes >= nbytes \
-            and t.device == device and t.is_cuda:
-        return t.data_ptr()
     if isinstance(t, torch.Tensor):
-        _need(t, name, nbytes, device)
+        if t.get_device() == device >= 0 and t.dtype in dtypes and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+        _need(t, name, nbytes, torch.device("cuda", device) if device >= 0 else None)
     return _ptr(t, name, dtypes)
 
 
@@ -456,13 +456,13 @@ def _norm(name, x, residual, weight, eps, sum_out, weight_offset, outs, stream):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d], got %s" % (tuple(x.shape),))
     rows, d = x.shape
-    dv = x.device
+    dv = x.get_device()
     n = rows * d * 2
-    if not x.is_cuda:   # sizes first, as in the other calls
+    if dv < 0:   # sizes first, as in the other calls
         for t, k, b in ((residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n)):
-            _need(t, k, b, dv)
+            _need(t, k, b, x.device)
         for t, k, dt, per in outs:
-            _need(t, k, rows * per, dv)
+            _need(t, k, rows * per, x.device)
     _call(name, dv, stream,
           _arg(x, "x", _BF16_LIKE, n, dv), _arg(residual, "residual", _BF16_LIKE, n, dv),
           _arg(_given(weight, "weight"), "weight", _BF16_LIKE, d * 2, dv), rows, d, eps, weight_offset,
@@ -486,6 +486,12 @@ def w8a8_add_rmsnorm_quantize(x, residual, weight, eps, sum_out, q, scale, weigh
 def _rows(t, name, dtypes, like=None):
     """Pointer and row stride (elements) of t [rows, heads, dim] whose rows are
     contiguous; the rows themselves may be apart (slices of one projection)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 3 and (like is None or (
+            t.shape == like.shape and t.dtype == like.dtype and t.get_device() == like.get_device())):
+        step, head, one = t.stride()
+        if one == 1 and head == t.shape[2] and step >= head * t.shape[1]:
+            return t.data_ptr(), step
+    # the checks one by one, for their errors and the layouts of single rows and heads
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dim() != 3:
@@ -536,7 +542,7 @@ def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=
     vp, vs = _rows(v, "v", _BF16_LIKE, k)
     _on_device(k, "k")
     tokens, heads, dim = k.shape
-    d = k.device
+    d = k.get_device()
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs,
           _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), format, cp, pages, page_size, heads, dim,
@@ -549,7 +555,7 @@ def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=N
     vp, vs = _rows(v, "v", _BF16_OR_F32, k)
     _on_device(k, "k")
     tokens, heads, dim = k.shape
-    d = k.device
+    d = k.get_device()
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim,
           _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), tokens, kp, vp, ks, vs,
@@ -567,7 +573,7 @@ def kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_l
     qp, qs = _rows(q, "q", _BF16_LIKE)
     _on_device(q, "q")
     seqs, heads, dim = q.shape
-    d = q.device
+    d = q.get_device()
     if block_table.dim() != 2 or block_table.shape[0] != seqs:
         raise ValueError("block_table must be [seqs=%d, width], got %s" % (seqs, tuple(block_table.shape)))
     n = seqs * heads
