@@ -428,12 +428,12 @@ def _call(name, device, stream, *args):
         check(st, name)
 
 
-def _arg(t, name, dtypes, nbytes, device):
+def _arg(t, name, dtypes, nbytes, device, nullable=True):
     """Pointer of a contiguous tensor of at least nbytes on device number
-    `device` (-1: the CPU, which is refused; None passes as a null pointer);
-    the checks' own errors where one fails.  Small calls wait for these checks,
+    `device` (-1: the CPU, which is refused; None passes as a null pointer where
+    nullable); the checks' own errors where one fails.  Small calls wait for these checks,
     so each is one cheap query (0.4 us an argument with whole devices compared)."""
-    if t is None:
+    if t is None and nullable:
         return None
     if isinstance(t, torch.Tensor):
         if t.get_device() == device >= 0 and t.dtype in dtypes and t.nbytes >= nbytes and t.is_contiguous():
@@ -442,45 +442,44 @@ def _arg(t, name, dtypes, nbytes, device):
     return _ptr(t, name, dtypes)
 
 
-def _given(t, name):
-    if t is None:
-        raise ValueError("%s must not be None" % name)
-    return t
-
-
 _F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
 _BF16_OR_F32 = _F32 + _BF16_LIKE
 
 
-def _norm(name, x, residual, weight, eps, sum_out, weight_offset, outs, stream):
+def _norm_sizes(x, residual, weight, sum_out, *outs):
+    """(rows, d, device) of x; what is not on a device is refused here, sizes
+    first, as in the other calls."""
     if x.dim() != 2:
         raise ValueError("x must be [rows, d], got %s" % (tuple(x.shape),))
     rows, d = x.shape
-    dv = x.get_device()
-    n = rows * d * 2
-    if dv < 0:   # sizes first, as in the other calls
+    device = x.get_device()
+    if device < 0:
+        n = rows * d * 2
         for t, k, b in ((residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n)):
             _need(t, k, b, x.device)
-        for t, k, dt, per in outs:
+        for t, k, per in outs:
             _need(t, k, rows * per, x.device)
-    _call(name, dv, stream,
-          _arg(x, "x", _BF16_LIKE, n, dv), _arg(residual, "residual", _BF16_LIKE, n, dv),
-          _arg(_given(weight, "weight"), "weight", _BF16_LIKE, d * 2, dv), rows, d, eps, weight_offset,
-          _arg(sum_out, "sum_out", _BF16_LIKE, n, dv),
-          *[_arg(_given(t, k), k, dt, rows * per, dv) for t, k, dt, per in outs])
+    return rows, d, device
 
 
 def w4a16_add_rmsnorm(x, residual, weight, eps, sum_out, y, weight_offset=0.0, stream=None):
     """y = bf16(RMS norm of r = bf16(x + residual)); residual and sum_out (r)
     may be None."""
-    _norm("w4a16_add_rmsnorm", x, residual, weight, eps, sum_out, weight_offset,
-          ((y, "y", _BF16_LIKE, x.shape[-1] * 2),), stream)
+    rows, d, dv = _norm_sizes(x, residual, weight, sum_out, (y, "y", x.shape[-1] * 2))
+    n = rows * d * 2
+    _call("w4a16_add_rmsnorm", dv, stream, _arg(x, "x", _BF16_LIKE, n, dv),
+          _arg(residual, "residual", _BF16_LIKE, n, dv), _arg(weight, "weight", _BF16_LIKE, d * 2, dv, False), rows, d,
+          eps, weight_offset, _arg(sum_out, "sum_out", _BF16_LIKE, n, dv), _arg(y, "y", _BF16_LIKE, n, dv, False))
 
 
 def w8a8_add_rmsnorm_quantize(x, residual, weight, eps, sum_out, q, scale, weight_offset=0.0, stream=None):
     """The norm's rows as E4M3 codes q [rows, d] and fp32 row scales."""
-    _norm("w8a8_add_rmsnorm_quantize", x, residual, weight, eps, sum_out, weight_offset,
-          ((q, "q", _U8, x.shape[-1]), (scale, "scale", _F32, 4)), stream)
+    rows, d, dv = _norm_sizes(x, residual, weight, sum_out, (q, "q", x.shape[-1]), (scale, "scale", 4))
+    n = rows * d * 2
+    _call("w8a8_add_rmsnorm_quantize", dv, stream, _arg(x, "x", _BF16_LIKE, n, dv),
+          _arg(residual, "residual", _BF16_LIKE, n, dv), _arg(weight, "weight", _BF16_LIKE, d * 2, dv, False), rows, d,
+          eps, weight_offset, _arg(sum_out, "sum_out", _BF16_LIKE, n, dv), _arg(q, "q", _U8, rows * d, dv, False),
+          _arg(scale, "scale", _F32, rows * 4, dv, False))
 
 
 def _rows(t, name, dtypes, like=None):
@@ -530,7 +529,9 @@ def kv_cache_page_bytes(format, page_size, kv_heads, head_dim):
 def _pages(cache, format, page_size, kv_heads, head_dim, device):
     """Pointer and page count of a cache buffer."""
     page = kv_cache_page_bytes(format, page_size, kv_heads, head_dim)
-    n, rest = divmod(_given(cache, "cache").numel(), page)
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    n, rest = divmod(cache.numel(), page)
     if rest:
         raise ValueError("cache holds %d bytes, not a multiple of a page's %d" % (cache.numel(), page))
     return _arg(cache, "cache", _U8, 0, device), n
@@ -545,7 +546,7 @@ def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=
     d = k.get_device()
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs,
-          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), format, cp, pages, page_size, heads, dim,
+          _arg(slots, "slots", _I64, tokens * 8, d, False), format, cp, pages, page_size, heads, dim,
           _arg(counters, "counters", _I64, 16, d))
 
 
@@ -558,7 +559,7 @@ def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=N
     d = k.get_device()
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim,
-          _arg(_given(slots, "slots"), "slots", _I64, tokens * 8, d), tokens, kp, vp, ks, vs,
+          _arg(slots, "slots", _I64, tokens * 8, d, False), tokens, kp, vp, ks, vs,
           W4_OUT_F32 if k.dtype == torch.float32 else W4_OUT_BF16, _arg(counters, "counters", _I64, 16, d))
 
 
@@ -580,8 +581,8 @@ def kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_l
     cp, pages = _pages(cache, format, page_size, kv_heads, dim, d)
     _call("kv_cache_attention", d, stream, qp, seqs, qs, heads, cp, format, pages, page_size, kv_heads, dim,
           _arg(block_table, "block_table", _I32, 0, d), block_table.shape[1],
-          _arg(_given(seq_lens, "seq_lens"), "seq_lens", _I32, seqs * 4, d), scale, window,
-          _arg(_given(out, "out"), "out", _BF16_LIKE, n * dim * 2, d), _arg(lse, "lse", _F32, n * 4, d),
+          _arg(seq_lens, "seq_lens", _I32, seqs * 4, d, False), scale, window,
+          _arg(out, "out", _BF16_LIKE, n * dim * 2, d, False), _arg(lse, "lse", _F32, n * 4, d),
           _arg(counters, "counters", _I64, 16, d), _arg(ws, "ws", _U8, 0, d), 0 if ws is None else ws.numel())
 
 
