@@ -7,13 +7,17 @@
 // with the running maximum and sum of the softmax.
 //
 // Bound by the cache's bytes: a token's K and V row of a head are read once
-// for all G query heads.
+// for all G query heads.  bf16 8 x 32768 tokens of 8 x 128: 162 us, 6.6 TB/s;
+// E4M3 48 ragged sequences up to 8000 of 8 x 128: 55 us, 4.9 TB/s; Q4 16 x
+// 32768 of 8 x 128: 112 us, 5.4 TB/s (Q4 by the vector instructions that
+// unpack and scale: 104 us while the card holds its highest clock; of 8 x 64
+// 73 us, 4.1 TB/s).
 //
 // Work split: grid (kv head x tile of 16 query heads, items), an item being a
 // run of a sequence's positions; a workgroup of 4 waves takes one, and a wave
 // 32 tokens at a time (two tiles of the cache), with its own running maximum,
 // sum and output.  The waves are joined through LDS, the items of a sequence
-// by a second kernel.
+// by a second kernel.  Few short sequences go to workgroups of 8 waves, whole.
 //
 // Matrix layouts (16x16x32 bf16, lane = 16c + n): the scores are formed as
 // S^T = K . Q^T with a tile's 16 tokens as rows, so lane (c, n) holds the
@@ -728,8 +732,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
   if (a.lse && d == 0) a.lse[row] = log_sum(mx, l);
 }
 
-// Replicas of the heads, Q4 only (16 sequences of 32768 tokens, 8 heads a kv
-// head: 146 us with R = 1, 118 with 2).
+// Replicas of the heads, Q4 only: as many as fit.  16 x 32768 tokens of 8 x
+// 128, 8 heads a kv head: 136 us with R = 1, 112 with 2; 4 heads: 132, 109, and
+// 105 with 4; of 4 x 256, 4 heads: 140, 115, 108; 32 x 16384 of 8 x 64: 78, 72.
 template <int FMT, int NG, int W>
 void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MOST = FMT != W4_KV_Q4 ? 1 : NG < 4 ? 2 : 4, HALF = MOST < 2 ? 1 : 2;
