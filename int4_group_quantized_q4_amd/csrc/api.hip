@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "decode.h"
 #include "internal.h"
 #include "kv_layout.h"
 #include "w4a16.h"

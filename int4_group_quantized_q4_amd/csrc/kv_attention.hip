@@ -39,7 +39,7 @@
 // rounding is its last one.
 
 #include "common.h"
-#include "internal.h"
+#include "decode.h"
 #include "kv_layout.h"
 #include "w4a16.h"
 

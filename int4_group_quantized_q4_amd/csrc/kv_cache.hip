@@ -18,7 +18,7 @@
 // us (5.5 TB/s), 11.2 -> 9.8 us for the two.
 
 #include "common.h"
-#include "internal.h"
+#include "decode.h"
 #include "kv_layout.h"
 #include "w4a16.h"
 

@@ -23,7 +23,7 @@
 // 6 or 8 chunks a lane, was slower (22.4 us, and spilling).
 
 #include "common.h"
-#include "internal.h"
+#include "decode.h"
 #include "w4a16.h"
 
 namespace w4 {
