@@ -446,27 +446,28 @@ _F32, _I32, _I64, _U8 = (torch.float32,), (torch.int32,), (torch.int64,), (torch
 _BF16_OR_F32 = _F32 + _BF16_LIKE
 
 
-def _norm_sizes(x, residual, weight, sum_out, *outs):
-    """(rows, d, device) of x; what is not on a device is refused here, sizes
-    first, as in the other calls."""
-    if x.dim() != 2:
-        raise ValueError("x must be [rows, d], got %s" % (tuple(x.shape),))
-    rows, d = x.shape
-    device = x.get_device()
-    if device < 0:
-        n = rows * d * 2
-        for t, k, b in ((residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n)):
-            _need(t, k, b, x.device)
-        for t, k, per in outs:
-            _need(t, k, rows * per, x.device)
-    return rows, d, device
+def _matrix(x):
+    """(rows, d, device number) of x."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must be [rows, d], got %s" % (tuple(shape),))
+    return shape[0], shape[1], x.get_device()
+
+
+def _sizes_first(x, *others):
+    """For an x that is on no device: the other arguments' sizes before that, as
+    in the other calls."""
+    for t, name, nbytes in others:
+        _need(t, name, nbytes, x.device)
 
 
 def w4a16_add_rmsnorm(x, residual, weight, eps, sum_out, y, weight_offset=0.0, stream=None):
     """y = bf16(RMS norm of r = bf16(x + residual)); residual and sum_out (r)
     may be None."""
-    rows, d, dv = _norm_sizes(x, residual, weight, sum_out, (y, "y", x.shape[-1] * 2))
+    rows, d, dv = _matrix(x)
     n = rows * d * 2
+    if dv < 0:
+        _sizes_first(x, (residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n), (y, "y", n))
     _call("w4a16_add_rmsnorm", dv, stream, _arg(x, "x", _BF16_LIKE, n, dv),
           _arg(residual, "residual", _BF16_LIKE, n, dv), _arg(weight, "weight", _BF16_LIKE, d * 2, dv, False), rows, d,
           eps, weight_offset, _arg(sum_out, "sum_out", _BF16_LIKE, n, dv), _arg(y, "y", _BF16_LIKE, n, dv, False))
@@ -474,8 +475,11 @@ def w4a16_add_rmsnorm(x, residual, weight, eps, sum_out, y, weight_offset=0.0, s
 
 def w8a8_add_rmsnorm_quantize(x, residual, weight, eps, sum_out, q, scale, weight_offset=0.0, stream=None):
     """The norm's rows as E4M3 codes q [rows, d] and fp32 row scales."""
-    rows, d, dv = _norm_sizes(x, residual, weight, sum_out, (q, "q", x.shape[-1]), (scale, "scale", 4))
+    rows, d, dv = _matrix(x)
     n = rows * d * 2
+    if dv < 0:
+        _sizes_first(x, (residual, "residual", n), (weight, "weight", d * 2), (sum_out, "sum_out", n),
+                     (q, "q", rows * d), (scale, "scale", rows * 4))
     _call("w8a8_add_rmsnorm_quantize", dv, stream, _arg(x, "x", _BF16_LIKE, n, dv),
           _arg(residual, "residual", _BF16_LIKE, n, dv), _arg(weight, "weight", _BF16_LIKE, d * 2, dv, False), rows, d,
           eps, weight_offset, _arg(sum_out, "sum_out", _BF16_LIKE, n, dv), _arg(q, "q", _U8, rows * d, dv, False),
@@ -511,6 +515,22 @@ def _rows(t, name, dtypes, like=None):
     return t.data_ptr(), step
 
 
+def _row_pair(k, v, dtypes):
+    """Pointers and row strides of k and v (as _rows), their shape and device
+    number.  The usual layout is seen in one go; any other, and every error,
+    goes through the checks one by one."""
+    shape, device = k.shape, k.get_device()
+    if device >= 0 and shape == v.shape and v.get_device() == device and len(shape) == 3 and k.dtype in dtypes \
+            and v.dtype == k.dtype:
+        (ks, kh, k1), (vs, vh, v1) = k.stride(), v.stride()
+        if k1 == v1 == 1 and kh == vh == shape[2] and ks >= kh * shape[1] <= vs:
+            return k.data_ptr(), ks, v.data_ptr(), vs, shape, device
+    kp, ks = _rows(k, "k", dtypes)
+    vp, vs = _rows(v, "v", dtypes, k)
+    _on_device(k, "k")
+    return kp, ks, vp, vs, shape, device
+
+
 def _on_device(t, name):
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
@@ -529,21 +549,16 @@ def kv_cache_page_bytes(format, page_size, kv_heads, head_dim):
 def _pages(cache, format, page_size, kv_heads, head_dim, device):
     """Pointer and page count of a cache buffer."""
     page = kv_cache_page_bytes(format, page_size, kv_heads, head_dim)
-    if not isinstance(cache, torch.Tensor):
-        raise TypeError("cache must be a torch.Tensor")
+    p = _arg(cache, "cache", _U8, 0, device, False)
     n, rest = divmod(cache.numel(), page)
     if rest:
         raise ValueError("cache holds %d bytes, not a multiple of a page's %d" % (cache.numel(), page))
-    return _arg(cache, "cache", _U8, 0, device), n
+    return p, n
 
 
 def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=None):
     """Quantize the rows k, v [tokens, kv_heads, head_dim] into their slots."""
-    kp, ks = _rows(k, "k", _BF16_LIKE)
-    vp, vs = _rows(v, "v", _BF16_LIKE, k)
-    _on_device(k, "k")
-    tokens, heads, dim = k.shape
-    d = k.get_device()
+    kp, ks, vp, vs, (tokens, heads, dim), d = _row_pair(k, v, _BF16_LIKE)
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_write", d, stream, kp, vp, tokens, ks, vs,
           _arg(slots, "slots", _I64, tokens * 8, d, False), format, cp, pages, page_size, heads, dim,
@@ -552,11 +567,7 @@ def kv_cache_write(k, v, slots, format, page_size, cache, counters=None, stream=
 
 def kv_cache_read(cache, format, page_size, slots, k, v, counters=None, stream=None):
     """The rows of `slots` into k, v [tokens, kv_heads, head_dim] (bf16 or fp32)."""
-    kp, ks = _rows(k, "k", _BF16_OR_F32)
-    vp, vs = _rows(v, "v", _BF16_OR_F32, k)
-    _on_device(k, "k")
-    tokens, heads, dim = k.shape
-    d = k.get_device()
+    kp, ks, vp, vs, (tokens, heads, dim), d = _row_pair(k, v, _BF16_OR_F32)
     cp, pages = _pages(cache, format, page_size, heads, dim, d)
     _call("kv_cache_read", d, stream, cp, format, pages, page_size, heads, dim,
           _arg(slots, "slots", _I64, tokens * 8, d, False), tokens, kp, vp, ks, vs,
