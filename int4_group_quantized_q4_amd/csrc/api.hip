@@ -758,7 +758,8 @@ static int check_kv_shape(int32_t format, int64_t n_pages, int32_t page_size, in
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return W4_ERR_SHAPE;
   if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return W4_ERR_SHAPE;
   if (kv_heads > 1024 || n_pages > INT32_MAX) return W4_ERR_SHAPE;
-  if (n_pages > ((int64_t)1 << 48) / (w4::kv_block_bytes(format, page_size, head_dim) * 2 * kv_heads)) return W4_ERR_SHAPE;
+  const int64_t page_bytes = w4::kv_block_bytes(format, page_size, head_dim) * 2 * kv_heads;
+  if (n_pages > ((int64_t)1 << 48) / page_bytes) return W4_ERR_SHAPE;
   return W4_OK;
 }
 
@@ -801,12 +802,10 @@ static bool rows_overlap(const void* p, int64_t ps, const void* q, int64_t qs, i
                          int64_t element) {
   if (!overlap(p, rows_bytes(rows, ps, width, element), q, rows_bytes(rows, qs, width, element))) return false;
   if (ps != qs) return true;
-  const int64_t pitch = ps * element, bytes = width * element;
-  const int64_t apart = (int64_t)((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) % (uintptr_t)pitch);
-  const int64_t back = q < p ? (int64_t)((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) % (uintptr_t)pitch)
-                             : pitch - apart;
-  const int64_t ahead = q < p ? pitch - back : apart;
-  return ahead < bytes || back < bytes;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t pitch = (uintptr_t)(ps * element), bytes = (uintptr_t)(width * element);
+  const uintptr_t apart = (a < b ? b - a : a - b) % pitch;   // of a row and the nearest one before it
+  return apart < bytes || pitch - apart < bytes;
 }
 
 static int check_kv_rows(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,

@@ -68,8 +68,12 @@ __device__ __forceinline__ u32x4 quad_transpose(u32x4 x, int q) {
   }
   return x;
 }
-__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
 // Bytes: lane q's byte i <-> lane i's byte q.
 __device__ __forceinline__ uint32_t quad_transpose_bytes(uint32_t x, int q) {
   const uint32_t sel = (uint32_t)q | ((uint32_t)(q + 4) << 8);

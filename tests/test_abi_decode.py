@@ -68,12 +68,13 @@ def test_page_bytes_refusals():
 
 def test_write_and_read_refusals():
     lib = _lib.lib()
-    a = dict(k=FAKE, v=FAKE + BIG, tokens=4, ks=256, vs=256, slots=FAKE + 2 * BIG, fmt=2, cache=FAKE + 3 * BIG, pages=4, page=16, heads=2,
-             D=128, counters=None, st=None)
+    a = dict(k=FAKE, v=FAKE + BIG, tokens=4, ks=256, vs=256, slots=FAKE + 2 * BIG, fmt=2, cache=FAKE + 3 * BIG,
+             pages=4, page=16, heads=2, D=128, counters=None, st=None)
     w = lib.kv_cache_write
     bad = [dict(tokens=-1), dict(ks=248), dict(ks=260), dict(vs=128), dict(slots=None), dict(slots=FAKE + 2 * BIG + 4),
            dict(cache=None), dict(cache=FAKE + 3 * BIG + 8), dict(cache=FAKE), dict(cache=FAKE + BIG),
-           dict(cache=FAKE + 2 * BIG), dict(slots=FAKE + 3 * BIG + 1024), dict(k=None), dict(v=FAKE + 8), dict(fmt=5), dict(pages=-1),
+           dict(cache=FAKE + 2 * BIG), dict(slots=FAKE + 3 * BIG + 1024), dict(k=None), dict(v=FAKE + 8),
+           dict(fmt=5), dict(pages=-1),
            dict(counters=FAKE + 4)]
     for b in bad:
         assert w(*changed(a, **b)) == w4.W4_ERR_ARG, b
@@ -81,10 +82,11 @@ def test_write_and_read_refusals():
               dict(pages=1 << 31), dict(pages=1 << 30, page=65536), dict(ks=1 << 47)):
         assert w(*changed(a, **b)) == w4.W4_ERR_SHAPE, b
     assert w(*changed(a, tokens=0, k=None, v=None, slots=None, cache=None)) == w4.W4_OK
-    r = dict(cache=FAKE + 3 * BIG, fmt=2, pages=4, page=16, heads=2, D=128, slots=FAKE + 2 * BIG, tokens=4, k=FAKE, v=FAKE + BIG, ks=256,
-             vs=256, out=0, counters=None, st=None)
+    r = dict(cache=FAKE + 3 * BIG, fmt=2, pages=4, page=16, heads=2, D=128, slots=FAKE + 2 * BIG, tokens=4, k=FAKE,
+             v=FAKE + BIG, ks=256, vs=256, out=0, counters=None, st=None)
     f = lib.kv_cache_read
-    # rows of k in rows of v: the same, shifted, between v's rows but too near, with another stride; k in the cache, slots
+    # rows of k in rows of v: the same, shifted, between v's rows but too near, with another stride; k in the cache, in
+    # the slots
     over = [dict(v=FAKE), dict(v=FAKE + 496), dict(v=FAKE - 16), dict(ks=512, vs=512, v=FAKE + 496),
             dict(ks=512, vs=512, v=FAKE - 528 + 1024), dict(ks=512, vs=512, v=FAKE + 1024 + 512 + 16),
             dict(ks=512, vs=1024, v=FAKE + 512), dict(k=FAKE + 3 * BIG + 64), dict(v=FAKE + 3 * BIG - 2048 + 16),

@@ -142,7 +142,8 @@ def test_q4_head_replicas(D, group):
 
 
 @pytest.mark.parametrize("form", kv_layout.FORMATS)
-@pytest.mark.parametrize("seqs,kv_heads,width", [(150, 1, 40), (150, 1, 400), (300, 2, 40), (300, 2, 400), (70, 4, 400)])
+@pytest.mark.parametrize("seqs,kv_heads,width",
+                         [(150, 1, 40), (150, 1, 400), (300, 2, 40), (300, 2, 400), (70, 4, 400)])
 def test_many_sequences(form, seqs, kv_heads, width):
     """Batches counted in several rounds of 64 lengths, batches that are not split at all, short and long tables."""
     rng = np.random.default_rng(seqs)
@@ -412,9 +413,18 @@ def test_helpers_on_another_stream():
         y, r = w4.add_rmsnorm(x, x, w, 1e-6, stream=stream)
         q, sc, r2 = w4.add_rmsnorm_quantize(x, x, w, 1e-6, stream=stream)
         need = w4.kv_cache_attention_workspace(2, 8, 2, 128, s.width, 32)
-        other = [torch.full((n,), 0xA5, dtype=torch.uint8, device=dev()) for n in (need, out.nbytes, lse.nbytes, y.nbytes)]
+        other = [torch.full((n,), 0xA5, dtype=torch.uint8, device=dev())
+                 for n in (need, out.nbytes, lse.nbytes, y.nbytes)]
         torch.cuda.synchronize()
         assert all((o == 0xA5).all() for o in other)
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wl)
         assert torch.equal(y.view(torch.int16), wy.view(torch.int16)) and torch.equal(q, wq) and torch.equal(sc, ws)
         assert torch.equal(r.view(torch.int16), r2.view(torch.int16))
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+@pytest.mark.parametrize("kv_heads,group", [(1024, 1), (300, 3), (1024, 16)])
+def test_most_heads(form, kv_heads, group):
+    """Up to the 1024 kv heads and 16384 query heads of the limits."""
+    s = Setup(form, [33, 5], kv_heads, group, 64, 16, seed=33)
+    s.check(*s.run())

@@ -39,10 +39,13 @@ class Layer:
         self.past = [gen.bf16_normal(rng, (int(n), 2, kv_heads, D)) for n in self.start]
         b = {}
         b["cache"] = w4.kv_cache(self.pages, FMT[form], page, kv_heads, D)
-        for name, shape, dt in (("x", (T, d), torch.bfloat16), ("h", (T, d), torch.bfloat16), ("qkv", (T, N), torch.bfloat16),
+        for name, shape, dt in (("x", (T, d), torch.bfloat16), ("h", (T, d), torch.bfloat16),
+                                ("qkv", (T, N), torch.bfloat16),
                                 ("att", (T, heads, D), torch.bfloat16), ("proj", (T, d), torch.bfloat16),
-                                ("res", (T, d), torch.bfloat16), ("h2", (T, d), torch.bfloat16), ("y", (T, d), torch.bfloat16),
-                                ("q8", (T, d), torch.uint8), ("s8", (T,), torch.float32), ("gmm", (T, 2 * I), torch.float32),
+                                ("res", (T, d), torch.bfloat16), ("h2", (T, d), torch.bfloat16),
+                                ("y", (T, d), torch.bfloat16),
+                                ("q8", (T, d), torch.uint8), ("s8", (T,), torch.float32),
+                                ("gmm", (T, 2 * I), torch.float32),
                                 ("logits", (T, E), torch.float32), ("lse", (T, heads), torch.float32)):
             b[name] = torch.zeros(shape, dtype=dt, device=dev())
         b["lens"] = torch.zeros(T, dtype=torch.int32, device=dev())

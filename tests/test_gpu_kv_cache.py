@@ -198,8 +198,63 @@ def test_rows_of_one_buffer(form):
     w4.kv_cache_write(view(1), view(3), slots, FMT[form], page, cache)
     w4.kv_cache_read(cache, FMT[form], page, slots, view(4), view(2))
     torch.cuda.synchronize()
-    want = [oracle.bf16_from_f32(decode.row_values(*decode.cache_rows(x, form), form).astype(np.float32)) for x in (k, v)]
+    want = [oracle.bf16_from_f32(decode.row_values(*decode.cache_rows(x, form), form).astype(np.float32))
+            for x in (k, v)]
     assert np.array_equal(bits_host(view(4).contiguous()), want[0])
     assert np.array_equal(bits_host(view(2).contiguous()), want[1])
     assert np.array_equal(bits_host(view(1).contiguous()), k) and np.array_equal(bits_host(view(3).contiguous()), v)
     assert (view(0) == 3).all()
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+def test_most_heads(form):
+    """1024 heads: written, read back, and nothing else changed."""
+    tokens, heads, D, page, pages = 21, 1024, 64, 16, 3
+    rng = np.random.default_rng(78)
+    k, v = rnd(rng, tokens, heads, D), rnd(rng, tokens, heads, D)
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int64)
+    cache = empty_cache(form, pages, page, heads, D)
+    before = cache.cpu().numpy().copy()
+    w4.kv_cache_write(bf16_dev(k), bf16_dev(v), to_dev(slots), FMT[form], page, cache)
+    ko = torch.zeros(tokens, heads, D, device=dev())
+    vo = torch.zeros_like(ko)
+    w4.kv_cache_read(cache, FMT[form], page, to_dev(slots), ko, vo)
+    torch.cuda.synchronize()
+    check_written(cache, before, form, pages, page, heads, D, slots, k, v)
+    for got, x in ((ko, k), (vo, v)):
+        want = decode.row_values(*decode.cache_rows(x, form), form)
+        assert np.array_equal(got.cpu().numpy(), want.astype(np.float32))
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+@pytest.mark.parametrize("heads,D", [(1, 64), (3, 128), (2, 256)])
+def test_many_tokens_as_pieces(form, heads, D):
+    """A long list in one call, and in pieces of odd sizes on two streams at once (neighbouring tokens of a tile from
+    both): the same bytes in the cache, and the same rows read."""
+    page, tokens = 64, 50021
+    pages = -(-tokens // page)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k = torch.randn(tokens, heads, D, generator=g, device=dev(), dtype=torch.bfloat16)
+    v = torch.randn(tokens, heads, D, generator=g, device=dev(), dtype=torch.bfloat16)
+    slots = torch.arange(tokens, device=dev(), dtype=torch.int64)
+    mixed = slots.view(-1)[torch.randperm(tokens, generator=g, device=dev())].contiguous()
+    one, two = empty_cache(form, pages, page, heads, D), empty_cache(form, pages, page, heads, D)
+    w4.kv_cache_write(k, v, slots, FMT[form], page, one)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    at, i = 0, 0
+    while at < tokens:
+        n = min((1, 3, 61, 997, 12001)[i % 5], tokens - at)
+        part = slice(at, at + n)
+        w4.kv_cache_write(k[part], v[part], slots[part], FMT[form], page, two, stream=streams[i % 2])
+        at, i = at + n, i + 1
+    torch.cuda.synchronize()
+    assert torch.equal(one, two)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    w4.kv_cache_read(one, FMT[form], page, slots, ko, vo)
+    km, vm = torch.zeros_like(k), torch.zeros_like(v)
+    w4.kv_cache_read(one, FMT[form], page, mixed, km, vm)
+    torch.cuda.synchronize()
+    assert torch.equal(km, ko[mixed]) and torch.equal(vm, vo[mixed])
+    if form == "bf16":
+        assert torch.equal(ko, k) and torch.equal(vo, v)

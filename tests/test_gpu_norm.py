@@ -149,3 +149,29 @@ def test_norm_leaves_neighbours():
     w4.w4a16_add_rmsnorm(x, None, bf16_dev(rnd(rng, 96)), 1e-6, None, buf[1:6])
     torch.cuda.synchronize()
     assert (buf[0] == 7).all() and (buf[6:] == 7).all()
+
+
+def test_norm_largest():
+    """The longest row, and more rows than one launch takes (2^22): the rows around the border and at the end."""
+    rng = np.random.default_rng(41)
+    d = 1 << 20
+    x, w = rnd(rng, 1, d), rnd(rng, d, sigma=0.3)
+    _, y = decode.add_rmsnorm(x, None, w, 1e-5, 0.0)
+    got, _ = w4.add_rmsnorm(bf16_dev(x), None, bf16_dev(w), 1e-5)
+    q, s, _ = w4.add_rmsnorm_quantize(bf16_dev(x), None, bf16_dev(w), 1e-5)
+    check_bf16(got, y)
+    qr, sr = decode.quantize_f64_rows(y)
+    assert np.array_equal(s.cpu().numpy(), sr) and np.array_equal(q.cpu().numpy(), qr)
+    rows, d = (1 << 22) + 5, 32
+    block = rnd(rng, 4096, d)
+    xd = bf16_dev(block).repeat(-(-rows // 4096), 1)[:rows].contiguous()
+    w = rnd(rng, d, sigma=0.3)
+    _, y = decode.add_rmsnorm(block, None, w, 1e-5, 0.0)
+    got, _ = w4.add_rmsnorm(xd, None, bf16_dev(w), 1e-5)
+    q, s, _ = w4.add_rmsnorm_quantize(xd, None, bf16_dev(w), 1e-5)
+    qr, sr = decode.quantize_f64_rows(y)
+    for at in (0, (1 << 22) - 3, (1 << 22) + 1):
+        part = slice(at, min(at + 5, rows))
+        pick = np.arange(part.start, part.stop) % 4096
+        check_bf16(got[part], y[pick])
+        assert np.array_equal(s[part].cpu().numpy(), sr[pick]) and np.array_equal(q[part].cpu().numpy(), qr[pick])
