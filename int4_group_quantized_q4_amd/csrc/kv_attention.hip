@@ -38,6 +38,8 @@
 // terms, high and low, so they carry 16 bits and the output's only visible
 // rounding is its last one.
 
+#include <type_traits>
+
 #include "common.h"
 #include "decode.h"
 #include "kv_layout.h"
@@ -416,8 +418,11 @@ kv_attention_kernel(AttnArgs a) {
     return last;
   };
 
-  // One chunk, and the loads of the wave's next one.
-  auto step = [&](int ch) {
+  // One chunk, and the loads of the wave's next one (loading the last chunk
+  // again instead of a step of its own for it: E4M3 48 ragged sequences of 8 x
+  // 128 57 against 53 us, bf16 64 x 1024 46.6 against 43.0).
+  auto step = [&](int ch, auto last) {
+    constexpr bool LAST = decltype(last)::value;
     good[0] = next_good[0];
     good[1] = next_good[1];
     float p[8];
@@ -468,12 +473,11 @@ kv_attention_kernel(AttnArgs a) {
       for (int i = 0; i < 8; ++i) p[i] *= 0.f;
     }
     __builtin_amdgcn_sched_barrier(0);   // not before the scores: K's registers are reused
-    const int next = ch + W < end ? ch + W : ch;   // the last chunk again, unused
     if constexpr (SHARED) {
       load_scales(true, vsr);
-      find_tiles(next);
-    } else {
-      load_k(next);
+      if constexpr (!LAST) find_tiles(ch + W);
+    } else if constexpr (!LAST) {
+      load_k(ch + W);
     }
 
     // Positions outside the span or in pages outside the cache have no score,
@@ -589,16 +593,18 @@ kv_attention_kernel(AttnArgs a) {
           acc[g][b] = mfma(av, ph, acc[g][b]);
           acc[g][b] = mfma(av, pl, acc[g][b]);
         }
-        if (SHARED && unit_done(g)) {
+        if (SHARED && !LAST && unit_done(g)) {
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int t = 0; t < 2; ++t) load_unit(false, t, u, kr[t][u]);
         }
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (SHARED) load_scales(false, ksr);
-    else load_v();
+    if constexpr (!LAST) {
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (SHARED) load_scales(false, ksr);
+      else load_v();
+    }
   };
 
   int ch = begin + wv;
@@ -610,10 +616,11 @@ kv_attention_kernel(AttnArgs a) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!SHARED) load_v();
     __builtin_amdgcn_sched_barrier(0);
-    for (int i = 1; ch < end; ch += W, ++i) {
-      step(ch);
+    for (int i = 1; ch + W < end; ch += W, ++i) {
+      step(ch, std::false_type());
       if (FMT == W4_KV_Q4 && (i & 7) == 0) take_bias();
     }
+    step(ch, std::true_type());
   }
   if constexpr (FMT == W4_KV_Q4) take_bias();
 
