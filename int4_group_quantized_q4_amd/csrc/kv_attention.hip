@@ -52,7 +52,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Least waves per SIMD that the register allocator keeps (none spills at these).
-constexpr int waves_per_simd(int fmt, int ng) { return ng == 2 ? 4 : ng == 4 && fmt == W4_KV_E4M3 ? 3 : 2; }
+constexpr int waves_per_simd(int fmt, int ng) { return ng == 2 ? 4 : ng == 4 && fmt != W4_KV_BF16 ? 3 : 2; }
 
 constexpr int kWaves = 4;
 constexpr int kWideWaves = 8;       // of a workgroup that takes a short row alone
@@ -251,34 +251,6 @@ kv_attention_kernel(AttnArgs a) {
     }
   }
 
-  // q of the column's head: dimensions 32g + 8c .. of the replica's groups
-  u32x4 q[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    q[g] = u32x4{0u, 0u, 0u, 0u};
-    if (hl < live_heads && rep == g / GR) {
-      const uint16_t* row = a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D;
-      q[g] = *reinterpret_cast<const u32x4*>(row + 32 * g + 8 * c);
-      if (a.scale < 0.f) q[g] ^= 0x80008000u;
-    }
-  }
-  // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
-  float kbias[GR];
-  if constexpr (FMT == W4_KV_Q4) {
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      float t = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r)     // all but the replica's own are zero
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w = q[r * GR + i][k];
-          t += bf16_to_f32(w & 0xFFFFu) + __uint_as_float(w & 0xFFFF0000u);
-        }
-      kbias[i] = -136.0f * column_sum(t);
-    }
-  }
-
   f32x4 acc[NG][2];
   f32x4 vbias[FMT == W4_KV_Q4 ? GR : 1];   // Q4: -136 times the replica's sum of P . scale
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
@@ -309,6 +281,23 @@ kv_attention_kernel(AttnArgs a) {
       if (id >= 0 && id < a.n_pages) ids = id;
     }
   };
+  // The table first, then q, then K and V, and only then arithmetic on q (Q4 1 x
+  // 1000 tokens of 8 x 128 9.1 -> 8.7 us in a graph, bf16 24 x 1000 of 4 x 128
+  // 16.7 -> 15.1).
+  int ch = begin + wv;
+  if (ch < end) fill_ids((2 * ch) >> tile_shift);
+
+  // q of the column's head: dimensions 32g + 8c .. of the replica's groups
+  u32x4 q[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    q[g] = u32x4{0u, 0u, 0u, 0u};
+    if (hl < live_heads && rep == g / GR) {
+      const uint16_t* row = a.q + (int64_t)seq * a.q_stride + (int64_t)(h0 + hl) * L::D;
+      q[g] = *reinterpret_cast<const u32x4*>(row + 32 * g + 8 * c);
+    }
+  }
+  float kbias[GR];   // Q4, set once the first loads are on their way
 
   // One chunk's K and V (codes and scales of its two tiles), each unit loaded
   // again as soon as its registers are free.  Apart (head_dim 64 and 128): K
@@ -607,15 +596,32 @@ kv_attention_kernel(AttnArgs a) {
     }
   };
 
-  int ch = begin + wv;
   if (ch < end) {
-    fill_ids((2 * ch) >> tile_shift);
     load_k(ch);
     // in this order, as in the loop: loads complete in order, and waiting for K
     // must not mean waiting for V
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!SHARED) load_v();
     __builtin_amdgcn_sched_barrier(0);
+    if (a.scale < 0.f) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) q[g] ^= 0x80008000u;
+    }
+    // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
+    if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)     // all but the replica's own are zero
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = q[r * GR + i][k];
+            t += bf16_to_f32(w & 0xFFFFu) + __uint_as_float(w & 0xFFFF0000u);
+          }
+        kbias[i] = -136.0f * column_sum(t);
+      }
+    }
     for (int i = 1; ch + W < end; ch += W, ++i) {
       step(ch, std::false_type());
       if (FMT == W4_KV_Q4 && (i & 7) == 0) take_bias();
