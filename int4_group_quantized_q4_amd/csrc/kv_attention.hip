@@ -7,11 +7,11 @@
 // with the running maximum and sum of the softmax.
 //
 // Bound by the cache's bytes: a token's K and V row of a head are read once
-// for all G query heads.  bf16 8 x 32768 tokens of 8 x 128: 162 us, 6.6 TB/s;
-// E4M3 48 ragged sequences up to 8000 of 8 x 128: 55 us, 4.9 TB/s; Q4 16 x
-// 32768 of 8 x 128: 112 us, 5.4 TB/s (Q4 by the vector instructions that
-// unpack and scale: 104 us while the card holds its highest clock; of 8 x 64
-// 73 us, 4.1 TB/s).
+// for all G query heads.  bf16 8 x 32768 tokens of 8 x 128: 161 us, 6.7 TB/s;
+// E4M3 48 ragged sequences up to 8000 of 8 x 128: 53 us, 5.1 TB/s; Q4 16 x
+// 32768 of 8 x 128: 110 us, 5.5 TB/s (Q4 by the vector instructions that
+// unpack and scale, and the clock they leave; 32 x 16384 of 8 x 64: 69 us, 4.4
+// TB/s).
 //
 // Work split: grid (kv head x tile of 16 query heads, items), an item being a
 // run of a sequence's positions; a workgroup of 4 waves takes one, and a wave
@@ -746,8 +746,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
 }
 
 // Replicas of the heads, Q4 only: as many as fit.  16 x 32768 tokens of 8 x
-// 128, 8 heads a kv head: 136 us with R = 1, 112 with 2; 4 heads: 132, 109, and
-// 105 with 4; of 4 x 256, 4 heads: 140, 115, 108; 32 x 16384 of 8 x 64: 78, 72.
+// 128, 8 heads a kv head: 130 us with R = 1, 112 with 2; 4 heads: 127, 107, and
+// 102 with 4; of 4 x 256, 4 heads: 139, 112, 104; 32 x 16384 of 8 x 64: 74, 69.
 template <int FMT, int NG, int W>
 void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MOST = FMT != W4_KV_Q4 ? 1 : NG < 4 ? 2 : 4, HALF = MOST < 2 ? 1 : 2;
@@ -775,12 +775,12 @@ int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_head
 // How a call's positions are split.  The workgroups aimed at are those that
 // keep the memory busy: fewer and longer ones lose less in starts, ends and
 // partial results.  Measured (us; 256, 512, 768, 1024 workgroups): bf16 8 x
-// 32768 tokens of 8 x 128: 161, 173, 173, 179; bf16 32 x 8192 of 8 x 64: 85,
-// 90, 92, 92; bf16 16 x 8192 of 4 x 256: 92, 95, 97, 102; E4M3 32 x 32768
-// ragged of 8 x 128: 152, 141, 133, 132; E4M3 16 x 16384 of 8 x 128: 89, 92,
-// 96, 94; E4M3 16 x 16384 of 4 x 256: 91, 93, 101, 99; Q4 16 x 32768 of 8 x
-// 128: 153, 116, 112, 114; Q4 32 x 16384 of 8 x 64: 112, 82, 69, 68; Q4 16 x
-// 32768 of 4 x 256: 160, 108, 126, 111.
+// 32768 tokens of 8 x 128: 163, 167, 169, 169; bf16 32 x 8192 of 8 x 64: 85,
+// 89, 89, 88; bf16 16 x 8192 of 4 x 256: 89, 89, 93, 91; E4M3 32 x 32768
+// ragged of 8 x 128: 156, 141, 130, 129; E4M3 16 x 16384 of 8 x 128: 88, 90,
+// 90, 90; E4M3 16 x 16384 of 4 x 256: 89, 90, 100, 93; Q4 16 x 32768 of 8 x
+// 128: 145, 116, 111, 112; Q4 32 x 16384 of 8 x 64: 109, 80, 71, 67; Q4 16 x
+// 32768 of 4 x 256: 158, 103, 122, 108.
 int64_t target_of(int32_t format, int32_t head_dim) {
   if (format == W4_KV_BF16) return 256;
   if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 768;
@@ -802,9 +802,9 @@ constexpr int64_t kUnsplit = 4096, kMostCounted = 256;
 // With too few rows to fill the card, splitting a short row costs more (a
 // second launch and its start) than one workgroup of 8 waves takes for it.  In
 // tokens x dimensions (us in a graph, split against wide): Q4 1 x 500 tokens of
-// 8 x 128: 9.0, 7.9; 1 x 1000: 9.3, 10.8; 1 x 250 of 4 x 256: 11.0, 10.1; 1 x
-// 500: 11.1, 12.6; with more rows up to twice as far (12 x 1000 of 8 x 128:
-// 13.7, 11.7; bf16 19.3, 17.0; Q4 12 x 2000: 16.0, 17.9).
+// 8 x 128: 8.8, 7.6; 1 x 1000: 8.9, 10.3; 1 x 250 of 4 x 256: 10.2, 8.8; 1 x
+// 500: 10.2, 11.1; with more rows up to twice as far (12 x 1000 of 8 x 128:
+// 12.0, 10.7; bf16 16.8, 15.8; Q4 12 x 2000: 14.4, 16.3).
 constexpr int64_t kWide = 512 * 128, kWideManyRows = 2 * kWide, kManyRows = 64;
 
 Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {
