@@ -34,9 +34,8 @@
 // the second product a group's rows count in its own replica's columns only.
 //
 // Precision: q and the codes are exact in bf16 and all sums are fp32.  The
-// probabilities (times the V scales) enter the second product as two bf16
-// terms, high and low, so they carry 16 bits and the output's only visible
-// rounding is its last one.
+// probabilities (times the V scales) enter the second product as three bf16
+// terms that hold their 24 bits.
 
 #include <type_traits>
 
@@ -78,13 +77,23 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// 8 fp32 values -> bf16 high (truncated) and low parts
-__device__ __forceinline__ void split_bf16(const float p[8], u32x4& hi, u32x4& lo) {
+// 8 fp32 values -> three bf16 terms each, whose sum is the value: 8 of its 24
+// bits at a time, by truncation (the differences are exact).
+__device__ __forceinline__ void split_bf16(const float p[8], u32x4& hi, u32x4& mid, u32x4& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t a = __float_as_uint(p[2 * i]), b = __float_as_uint(p[2 * i + 1]);
-    hi[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // the upper halves
-    lo[i] = pk_bf16(p[2 * i] - __uint_as_float(a & 0xFFFF0000u), p[2 * i + 1] - __uint_as_float(b & 0xFFFF0000u));
+    uint32_t w[2][3];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v = p[2 * i + k];
+      const float r = v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+      w[k][0] = __float_as_uint(v);
+      w[k][1] = __float_as_uint(r);
+      w[k][2] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u));
+    }
+    hi[i] = __builtin_amdgcn_perm(w[1][0], w[0][0], 0x07060302u);   // the upper halves
+    mid[i] = __builtin_amdgcn_perm(w[1][1], w[0][1], 0x07060302u);
+    lo[i] = __builtin_amdgcn_perm(w[1][2], w[0][2], 0x07060302u);
   }
 }
 
@@ -544,18 +553,19 @@ kv_attention_kernel(AttnArgs a) {
     l_run += sum;
 
     // O^T += V^T . P^T (Q4: P times the scales of the replicas' i-th groups)
-    u32x4 ph, pl;
+    u32x4 ph, pm, pl;
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
       if (FMT == W4_KV_Q4 || i == 0) {
         float ps[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) ps[k] = FMT == W4_KV_BF16 ? p[k] : p[k] * scale_of(vsr[k >> 2], i, k & 3);
-        split_bf16(ps, ph, pl);
+        split_bf16(ps, ph, pm, pl);
       }
       if constexpr (FMT == W4_KV_Q4) {
         const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
         vbias[i] = mfma(bias, ph, vbias[i]);
+        vbias[i] = mfma(bias, pm, vbias[i]);
         vbias[i] = mfma(bias, pl, vbias[i]);
       }
 #pragma unroll
@@ -580,6 +590,7 @@ kv_attention_kernel(AttnArgs a) {
             }
           }
           acc[g][b] = mfma(av, ph, acc[g][b]);
+          acc[g][b] = mfma(av, pm, acc[g][b]);
           acc[g][b] = mfma(av, pl, acc[g][b]);
         }
         if (SHARED && !LAST && unit_done(g)) {
