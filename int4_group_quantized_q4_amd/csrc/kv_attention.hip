@@ -33,7 +33,9 @@
 // part of the scores is summed over the replicas by lane rotations, and of
 // the second product a group's rows count in its own replica's columns only.
 //
-// Precision: q and the codes are exact in bf16 and all sums are fp32.  The
+// Precision: q and the codes are exact in bf16 and all sums are fp32 (Q4: with
+// the codes as 8 + q, which an fp32 sum rounds about as much as the group's
+// largest values, whose codes are 7 and -7 or -8, make it round anyway).  The
 // probabilities (times the V scales) enter the second product as three bf16
 // terms that hold their 24 bits.
 
@@ -71,6 +73,27 @@ __device__ __forceinline__ u32x2 e4m3_to_bf16(uint32_t w) {
   o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
   return o;
 }
+
+// Q4: four codes u = q + 8, one in each byte -> bf16 u, exact: as an E4M3 code
+// a byte up to 15 stands for u 2^-9 (the subnormals and the first binade, which
+// have one step).
+__device__ __forceinline__ u32x2 q4_to_bf16(uint32_t w) {
+  u32x2 o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, false));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, true));
+  return o;
+}
+// A K word's 8 codes, in the order of its bytes: dimensions 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ u32x4 q4_word_to_bf16(uint32_t w) {
+  const u32x2 lo = q4_to_bf16(w & 0x0F0F0F0Fu), hi = q4_to_bf16((w >> 4) & 0x0F0F0F0Fu);
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+// q's 8 dimensions in that order.
+__device__ __forceinline__ u32x4 q4_word_order(u32x4 q) {
+  return u32x4{__builtin_amdgcn_perm(q[2], q[0], 0x05040100u), __builtin_amdgcn_perm(q[2], q[0], 0x07060302u),
+               __builtin_amdgcn_perm(q[3], q[1], 0x05040100u), __builtin_amdgcn_perm(q[3], q[1], 0x07060302u)};
+}
+constexpr uint32_t kNeg8Pair = 0xC100C100u;   // bf16 -8
 
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   const bf16x2 v = {(__bf16)a, (__bf16)b};
@@ -261,7 +284,7 @@ kv_attention_kernel(AttnArgs a) {
   }
 
   f32x4 acc[NG][2];
-  f32x4 vbias[FMT == W4_KV_Q4 ? GR : 1];   // Q4: -136 times the replica's sum of P . scale
+  f32x4 vbias[FMT == W4_KV_Q4 ? GR : 1];   // Q4: -8 times the replica's sum of P . scale
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < NG; ++g) acc[g][0] = acc[g][1] = zero4;
@@ -396,9 +419,9 @@ kv_attention_kernel(AttnArgs a) {
     return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
   };
 
-  // Q4: takes the codes' +136 off the outputs.  Every 8 chunks: left to the
-  // end, the sums would grow to 136 times the values' own, and lose that much
-  // of their 24 bits where long flat attention averages the values out.
+  // Q4: takes the codes' +8 off the outputs.  Every 8 chunks: left to the end,
+  // the sums would grow to 8 times those of the probabilities, and lose that
+  // much of their 24 bits where long flat attention averages the values out.
   auto take_bias = [&]() {
 #pragma unroll
     for (int g = 0; g < NG; ++g)
@@ -445,7 +468,7 @@ kv_attention_kernel(AttnArgs a) {
             s4 = mfma(u32x4{a0[0], a0[1], a1[0], a1[1]}, q[g], s4);
           } else {
             // a column gathers its replica's groups only (its q is zero in the others)
-            d = mfma(biased_pairs(kr[t][u][part]), q[g], d);
+            d = mfma(q4_word_to_bf16(kr[t][u][part]), q[g], d);
           }
           if (SHARED && unit_done(g)) {
             __builtin_amdgcn_sched_barrier(0);
@@ -563,7 +586,7 @@ kv_attention_kernel(AttnArgs a) {
         split_bf16(ps, ph, pm, pl);
       }
       if constexpr (FMT == W4_KV_Q4) {
-        const u32x4 bias = {kNeg136Pair, kNeg136Pair, kNeg136Pair, kNeg136Pair};
+        const u32x4 bias = {kNeg8Pair, kNeg8Pair, kNeg8Pair, kNeg8Pair};
         vbias[i] = mfma(bias, ph, vbias[i]);
         vbias[i] = mfma(bias, pm, vbias[i]);
         vbias[i] = mfma(bias, pl, vbias[i]);
@@ -584,9 +607,9 @@ kv_attention_kernel(AttnArgs a) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               // byte j: token j's code of dimension 2m (low nibble), 2m + 1 (high)
-              const uint32_t w = (b ? vr[t][u][part] >> 4 : vr[t][u][part]) & 0x0F0F0F0Fu;
-              av[2 * t] = __builtin_amdgcn_perm(0x43434343u, w, 0x04010400u);
-              av[2 * t + 1] = __builtin_amdgcn_perm(0x43434343u, w, 0x04030402u);
+              const u32x2 w = q4_to_bf16((b ? vr[t][u][part] >> 4 : vr[t][u][part]) & 0x0F0F0F0Fu);
+              av[2 * t] = w[0];
+              av[2 * t + 1] = w[1];
             }
           }
           acc[g][b] = mfma(av, ph, acc[g][b]);
@@ -618,8 +641,10 @@ kv_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) q[g] ^= 0x80008000u;
     }
-    // Q4 codes enter as 136 + q: -136 times q's sum over each group cancels that
+    // Q4 codes enter as 8 + q: -8 times q's sum over each group cancels that
     if constexpr (FMT == W4_KV_Q4) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) q[g] = q4_word_order(q[g]);
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         float t = 0.f;
@@ -630,7 +655,7 @@ kv_attention_kernel(AttnArgs a) {
             const uint32_t w = q[r * GR + i][k];
             t += bf16_to_f32(w & 0xFFFFu) + __uint_as_float(w & 0xFFFF0000u);
           }
-        kbias[i] = -136.0f * column_sum(t);
+        kbias[i] = -8.0f * column_sum(t);
       }
     }
     for (int i = 1; ch + W < end; ch += W, ++i) {

@@ -51,3 +51,66 @@ def test_cancelling_values(form, D, group):
             assert (err <= bound).all(), (i, h, np.max(err / bound), np.max(err / A))
             small += np.sum(np.abs(ref[h]) < 2.0 ** -11 * A)
     assert small >= 8       # outputs whose own rounding is below 2^-19 of A
+
+
+def _put(s, which, edit):
+    """Replace the codes and scales of the cache's K (0) or V (1)."""
+    codes, scales = (s.k, s.v)[which]
+    codes, scales = codes.copy(), scales.copy()
+    edit(codes, scales)
+    if which:
+        s.v = (codes, scales)
+    else:
+        s.k = (codes, scales)
+    s.cache = to_dev(kv_layout.encode_cache(s.k, s.v, "q4"))
+
+
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 16), (128, 4), (128, 8), (128, 16), (256, 4), (256, 5), (256, 9)])
+def test_q4_zeros_beside_a_large_scale(D, group):
+    """A group whose scale one large value set: its other codes are 0, and what the other position has in their places
+    comes out as it is.  Equal scores (scale 0) and scales 2^18 and 1: sums of codes -8 .. 7 times them, with the 8 that
+    is added to a code and taken off again, are integers below 2^23, so every step is exact."""
+    s = Setup("q4", [2] * 12, 2, group, D, 16, seed=D + group)
+    s.scale = 0.0
+    rng = np.random.default_rng(D)
+
+    def edit(codes, scales):
+        p = s.table[:, 0]
+        codes[p, :, 0] = 0
+        codes[p, :, 0, ::32] = 7
+        codes[p, :, 1] = rng.integers(-8, 8, codes[p, :, 1].shape)
+        scales[p, :, 0] = oracle.bf16_from_f64(np.float64(2.0 ** 18))
+        scales[p, :, 1] = oracle.bf16_from_f64(np.float64(1.0))
+
+    _put(s, 1, edit)
+    got = bits_host(s.run()[0])
+    for i in range(len(s.lens)):
+        v = s.rows(i, 0)[1][0]
+        want = oracle.bf16_from_f64((v[0] + v[1]) / 2.0)
+        assert np.array_equal(got[i], np.repeat(want, group, axis=0)), i
+
+
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 16), (128, 4), (128, 8), (128, 16), (256, 4), (256, 5), (256, 9)])
+def test_q4_zeros_beside_a_large_query(D, group):
+    """The same for the scores: large elements of q meet codes 0.  q is a multiple of 2^-7 (2^12 where the code is 0),
+    the scales are 1: the sums, with the codes' 8, are multiples of 2^-7 below 2^17, exact in fp32.  One position, so
+    lse is its score, up to the roundings of the score in base 2, of the reference 8 above it and of the way back."""
+    s = Setup("q4", [1] * 12, 2, group, D, 16, seed=D + group)
+    s.scale = 0.25
+    rng = np.random.default_rng(D)
+    q = rng.integers(-128, 129, s.q.shape) * 2.0 ** -7
+    q[..., ::32] = 2.0 ** 12
+    s.q = oracle.bf16_from_f64(q)
+
+    def edit(codes, scales):
+        p = s.table[:, 0]
+        codes[p, :, 0] = rng.integers(-8, 8, codes[p, :, 0].shape)
+        codes[p, :, 0, ::32] = 0
+        scales[p, :, 0] = oracle.bf16_from_f64(np.float64(1.0))
+
+    _put(s, 0, edit)
+    lse = s.run()[1].cpu().numpy().astype(np.float64)
+    for i in range(len(s.lens)):
+        (k, _), (v, _) = s.rows(i, 0)
+        _, want, _, _ = decode.attention(s.q[i], k, v, s.scale)
+        assert (np.abs(lse[i] - want) <= 2.0 ** -22 * (np.abs(want) + 8.0)).all(), (i, np.max(np.abs(lse[i] - want)))
