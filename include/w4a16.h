@@ -610,8 +610,11 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  * sequence without positions, and a head whose scores are all -infinity, give
  * out = 0 and lse = -infinity; a NaN or +infinity among the scores gives NaN.
  * An infinite value (W4_KV_BF16) makes its dimension infinite or NaN, as the
- * probabilities enter as the sum of three terms.  Cache rows outside the
- * positions may hold anything.  Lengths are cut to [0,
+ * probabilities enter as the sum of three terms; an infinite element of q
+ * counts as a NaN over W4_KV_Q4.  The sums are of the values themselves, not of
+ * their mean: n positions' values |v| have to stay below 2^126 / n, or a finite
+ * result may come out infinite or NaN; values below 2^-90 lose low bits.  Cache
+ * rows outside the positions may hold anything.  Lengths are cut to [0,
  * table_width * page_size]; positions in pages outside [0, n_pages) count as
  * absent.
  *   q            in  [seqs] rows of heads*head_dim bf16, q_stride elements apart

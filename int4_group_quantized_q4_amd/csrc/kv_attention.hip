@@ -58,7 +58,7 @@ constexpr int waves_per_simd(int fmt, int ng) { return ng == 2 ? 4 : ng == 4 && 
 constexpr int kWaves = 4;
 constexpr int kWideWaves = 8;       // of a workgroup that takes a short row alone
 constexpr int kChunk = 32;          // tokens per wave step
-constexpr float kSlack = 8.0f;       // of the softmax's running reference, in powers of two
+constexpr float kSlack = 8.0f;       // of the softmax's running reference above the maximum, in powers of two
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -546,14 +546,15 @@ kv_attention_kernel(AttnArgs a) {
     }
 
     // Softmax against a running reference: any reference gives the same
-    // result, so it follows the maximum only when that has grown by more than
-    // 2^kSlack, and the outputs are rarely rescaled.
+    // result, so it is set 2^kSlack above the maximum and follows only when the
+    // maximum has passed it: the outputs are rarely rescaled, and no p is over
+    // 1, so the sums hold no more than the values' own.
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
     top = column_max(top) * scale2;
-    if (__any(top > m_run + kSlack)) {
-      const float m_new = fmaxf(m_run, top);
+    if (__any(top > m_run)) {
+      const float m_new = fmaxf(m_run, top + kSlack);
       const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_run - m_new);
       m_run = m_new;
       l_run *= alpha;

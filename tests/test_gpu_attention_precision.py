@@ -114,3 +114,25 @@ def test_q4_zeros_beside_a_large_query(D, group):
         (k, _), (v, _) = s.rows(i, 0)
         _, want, _, _ = decode.attention(s.q[i], k, v, s.scale)
         assert (np.abs(lse[i] - want) <= 2.0 ** -22 * (np.abs(want) + 8.0)).all(), (i, np.max(np.abs(lse[i] - want)))
+
+
+@pytest.mark.parametrize("form", kv_layout.FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_values_after_a_growing_maximum(form, D):
+    """Values near the stated limit (n |v| < 2^126), met by a wave whose scores first grow by less than 2^8: the
+    probabilities enter relative to a reference that is never below the maximum, so the sums stay finite."""
+    n = 300     # 40 sequences: enough rows for workgroups of 8 waves, whose first wave takes chunks 0 and 8
+    s = Setup(form, [n] * 40, 2, 2, D, 16, seed=D, junk=False, share=True)
+    s.scale = 1.0
+    q = np.zeros(s.q.shape)
+    q[..., 0] = 1.0
+    s.q = oracle.bf16_from_f64(q)
+    pos = np.arange(n)
+    k = np.zeros((s.pages, 2, 16, D))
+    k[s.table[0, pos // 16], :, pos % 16, 0] = np.where(pos < 256, 0.0, 5.25)[:, None]     # 2^7.57
+    v = 2.0 ** 117 * (0.5 + 0.5 * s.rng.random((s.pages, 2, 16, D)))
+    s.k, s.v = (decode.cache_rows(oracle.bf16_from_f64(x), form) for x in (k, v))
+    s.cache = to_dev(kv_layout.encode_cache(s.k, s.v, form))
+    out, lse = s.run()
+    assert np.isfinite(oracle.bf16_bits_to_f64(bits_host(out))).all()
+    s.check(out, lse, only=[0, 39])
