@@ -506,10 +506,11 @@ int w8a8_moe_layer(const uint16_t* x, const float* logits, int64_t T, int32_t E,
  *   weight    in  [d] bf16; weight_offset 1 for weights stored around zero
  *   sum_out   out, nullable (needs residual)  [rows][d] bf16: r
  *   y         out [rows][d] bf16
- * Sums and products are 64-bit; y is rounded once.  A NaN or an infinity in a
- * row makes the row's y NaN where the formula does.  y may be x or residual,
- * sum_out may be x or residual (the same pointer); any other overlap of an
- * output with another argument is W4_ERR_ARG.
+ * The sum of squares is 64-bit; y is good to about 2^-46 before it is rounded to
+ * fp32 (a |y| under 2^-117: to about 2^-141), and from there to bf16.  NaN and
+ * infinities, of the weights too, come out where the formula has them.  y may be
+ * x or residual, sum_out may be x or residual (the same pointer); any other
+ * overlap of an output with another argument is W4_ERR_ARG.
  * Requires d % 32 == 0, d <= 2^20, rows*d <= 2^40, finite eps >= 0.
  */
 int w4a16_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t d,

@@ -12,9 +12,11 @@
 // of squares is 64-bit, max|n| is taken of exact products, 1 / rms and s
 // follow in 64 bits, and the per-element factor f (1 / rms, or 1 / (rms s))
 // enters as two fp32 terms: r f = a + b with a = fl(r fh), b = fl(r fh - a +
-// r fl), and y = fma(a, w', b w'), good to about 2^-46 before its rounding.
-// Rows whose statistics leave the range where that holds (below) take the same
-// steps in 64 bits throughout.
+// r fl), and y = fma(a, w', b w'), good to about 2^-46 before its rounding to
+// fp32 (the bf16 form then rounds that to bf16).  That holds where neither r f
+// nor its last bits leave fp32's range beside their w': rows whose statistics
+// do, and chunks with a |w'| over 2^8 (or one that is not finite), take the same
+// steps in 64 bits.
 //
 // Bound by memory for many rows (4096 x 2816 with residual, E4M3: 17.8 us, 4.5
 // TB/s; 8191 x 4096 bf16: 22.7 us, 5.9 TB/s), by latency for few (one row 2.6
@@ -106,6 +108,17 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
              max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
 }
 
+// Whether every |w'| of the chunk is at most 2^8: what r f loses below 2^-149 is
+// then at most 2^-141 in y, less than fp32's rounding of a y from 2^-117 up, and
+// 2^-8 of bf16's smallest step.
+__device__ __forceinline__ bool weights_near_one(u32x4 w, float offset) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+  return bf16_to_f32(max(m[0], m[1])) + __builtin_fabsf(offset) <= 256.0f;   // not for a NaN
+}
+
 // The output factor of a row: f = fh + fl, or (wide) in 64 bits.
 struct Factor {
   float fh, fl;
@@ -117,7 +130,7 @@ struct Factor {
 template <bool QUANT>
 __device__ __forceinline__ void store_chunk(const NormArgs& a, int64_t row, int ch, u32x4 r, u32x4 w, const Factor& k) {
   float y[8];
-  if (!k.wide) {
+  if (!k.wide && weights_near_one(w, a.offset)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float v = chunk_value(r, i), t = chunk_value(w, i) + a.offset;
