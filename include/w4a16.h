@@ -578,7 +578,8 @@ size_t kv_cache_page_bytes(int32_t format, int32_t page_size, int32_t kv_heads, 
  *              them): counters[0] += tokens whose slot lies past the cache
  *              (skipped too), counters[1] += rows (E4M3) or groups (Q4) with a
  *              NaN or an infinity
- * The cache may not overlap k, v or slots (W4_ERR_ARG).
+ * The cache may not overlap k, v or slots, nor the counters any of these
+ * (W4_ERR_ARG).
  * Requires tokens < 2^27, tokens * stride <= 2^48.
  */
 int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
@@ -592,8 +593,8 @@ int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t
  * they were; a slot may be named any number of times.
  *   k, v  out [tokens] rows of kv_heads*head_dim of out_dtype, strides in
  *         elements (multiples of 8), 16-byte aligned; they may be slices of one
- *         buffer, but no row may overlap another, the cache or slots
- *         (W4_ERR_ARG).  Limits as above.
+ *         buffer, but no row may overlap another, the cache or slots, nor
+ *         the counters any of these (W4_ERR_ARG).  Limits as above.
  */
 int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads,
                   int32_t head_dim, const int64_t* slots, int64_t tokens, void* k, void* v, int64_t k_stride,
@@ -633,7 +634,8 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
  * positions are split.
  * Requires heads % kv_heads == 0, heads <= 16384, seqs <= 65535, seqs * heads <
  * 2^24, table_width * page_size < 2^31, n_pages >= 1, window >= 0, |scale| <=
- * 2^64.  No output (ws included) may overlap another argument (W4_ERR_ARG).
+ * 2^64.  No output (ws and counters included) may overlap another argument
+ * (W4_ERR_ARG).
  */
 size_t kv_cache_attention_workspace(int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     int64_t table_width, int32_t page_size);

@@ -825,6 +825,11 @@ static int check_kv_rows(const void* k, const void* v, int64_t tokens, int64_t k
   if (overlap(cache, held, k, rows_bytes(tokens, k_stride, width, element)) ||
       overlap(cache, held, v, rows_bytes(tokens, v_stride, width, element)) || overlap(cache, held, slots, tokens * 8))
     return W4_ERR_ARG;
+  // the counters are written (two of them)
+  if (overlap(counters, 16, cache, held) || overlap(counters, 16, slots, tokens * 8) ||
+      overlap(counters, 16, k, rows_bytes(tokens, k_stride, width, element)) ||
+      overlap(counters, 16, v, rows_bytes(tokens, v_stride, width, element)))
+    return W4_ERR_ARG;
   return W4_OK;
 }
 
@@ -911,12 +916,13 @@ int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_
   const Part parts[] = {{out, rows * head_dim * 2},
                         {lse, rows * 4},
                         {need ? ws : nullptr, need},
+                        {counters, 8},
                         {q, rows_bytes(seqs, q_stride, (int64_t)heads * head_dim, 2)},
                         {cache, (size_t)n_pages * kv_cache_page_bytes(format, page_size, kv_heads, head_dim)},
                         {block_table, (size_t)seqs * (size_t)table_width * 4},
                         {seq_lens, (size_t)seqs * 4}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 7; ++j)
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 8; ++j)
       if (overlap(parts[i].p, parts[i].n, parts[j].p, parts[j].n)) return W4_ERR_ARG;
   w4::AttnArgs a{};
   a.q = q;
