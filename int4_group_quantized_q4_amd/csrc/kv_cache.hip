@@ -474,13 +474,22 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvArgs a) {
   }
 }
 
+template <int NG>
+unsigned row_blocks(const KvArgs& a) {
+  return (unsigned)((a.tokens + RowSplit<NG>::ROWS - 1) / RowSplit<NG>::ROWS);
+}
+
 template <int FMT, int NG, int HB>
-void launch_heads(const KvArgs& a, bool write, int out_dtype, hipStream_t stream) {
+void launch_write(const KvArgs& a, hipStream_t stream) {
+  const dim3 grid(row_blocks<NG>(a), a.kv_heads, HB > 0 ? 1 : 2);
+  kv_write_kernel<FMT, NG, HB><<<grid, kThreads, 0, stream>>>(a);
+}
+
+template <int FMT, int NG, int HB>
+void launch_read(const KvArgs& a, int out_dtype, hipStream_t stream) {
   constexpr int H = HB > 0 ? HB : 1;
-  const dim3 grid((unsigned)((a.tokens + RowSplit<NG>::ROWS - 1) / RowSplit<NG>::ROWS), (a.kv_heads + H - 1) / H,
-                  HB > 0 ? 1 : 2);
-  if (write) kv_write_kernel<FMT, NG, HB><<<grid, kThreads, 0, stream>>>(a);
-  else if (out_dtype == W4_OUT_F32) kv_read_kernel<FMT, NG, HB, float><<<grid, kThreads, 0, stream>>>(a);
+  const dim3 grid(row_blocks<NG>(a), (a.kv_heads + H - 1) / H, HB > 0 ? 1 : 2);
+  if (out_dtype == W4_OUT_F32) kv_read_kernel<FMT, NG, HB, float><<<grid, kThreads, 0, stream>>>(a);
   else kv_read_kernel<FMT, NG, HB, uint16_t><<<grid, kThreads, 0, stream>>>(a);
 }
 
@@ -494,10 +503,17 @@ constexpr int64_t kBoth = 1024, kTwoHeads = 2048;
 
 template <int FMT, int NG>
 void launch_fmt(const KvArgs& a, bool write, int out_dtype, hipStream_t stream) {
-  const int64_t wgs = (a.tokens + RowSplit<NG>::ROWS - 1) / RowSplit<NG>::ROWS * a.kv_heads;
-  if (wgs >= kTwoHeads && a.kv_heads > 1 && !write) launch_heads<FMT, NG, 2>(a, write, out_dtype, stream);
-  else if (wgs >= kBoth) launch_heads<FMT, NG, 1>(a, write, out_dtype, stream);
-  else launch_heads<FMT, NG, 0>(a, write, out_dtype, stream);
+  const int64_t wgs = (int64_t)row_blocks<NG>(a) * a.kv_heads;
+  if (write) {
+    if (wgs >= kBoth) launch_write<FMT, NG, 1>(a, stream);
+    else launch_write<FMT, NG, 0>(a, stream);
+  } else if (wgs >= kTwoHeads && a.kv_heads > 1) {
+    launch_read<FMT, NG, 2>(a, out_dtype, stream);
+  } else if (wgs >= kBoth) {
+    launch_read<FMT, NG, 1>(a, out_dtype, stream);
+  } else {
+    launch_read<FMT, NG, 0>(a, out_dtype, stream);
+  }
 }
 
 template <int FMT>
