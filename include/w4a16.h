@@ -587,8 +587,8 @@ int kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t
                    int32_t kv_heads, int32_t head_dim, unsigned long long* counters, hipStream_t stream);
 
 /*
- * kv_cache_read -- the rows of given slots as bf16 (code times scale rounded
- * once) or fp32 (W4_OUT_F32; exact for Q4, rounded once for E4M3).  Rows of
+ * kv_cache_read -- the rows of given slots as fp32 (W4_OUT_F32: code times
+ * scale, exact for Q4, rounded once for E4M3) or that rounded to bf16.  Rows of
  * negative slots and of slots past the cache (counted as above) are left as
  * they were; a slot may be named any number of times.
  *   k, v  out [tokens] rows of kv_heads*head_dim of out_dtype, strides in

@@ -7,11 +7,12 @@
 // with the running maximum and sum of the softmax.
 //
 // Bound by the cache's bytes: a token's K and V row of a head are read once
-// for all G query heads.  bf16 8 x 32768 tokens of 8 x 128: 161 us, 6.7 TB/s;
-// E4M3 48 ragged sequences up to 8000 of 8 x 128: 53 us, 5.1 TB/s; Q4 16 x
-// 32768 of 8 x 128: 110 us, 5.5 TB/s (Q4 by the vector instructions that
-// unpack and scale, and the clock they leave; 32 x 16384 of 8 x 64: 69 us, 4.4
-// TB/s).
+// for 16 query heads (more of them read it again: bf16 32 x 32768 of 2 x 128
+// 170 us with 16 heads a kv head, 330 with 32).  bf16 8 x 32768 tokens of 8 x
+// 128: 161 us, 6.7 TB/s; E4M3 48 ragged sequences up to 8000 of 8 x 128: 54 us,
+// 5.1 TB/s; Q4 16 x 32768 of 8 x 128, 8 heads a kv head: 129 us, 4.7 TB/s (Q4 by
+// the vector instructions that unpack, scale and split, and the clock they
+// leave; 32 x 16384 of 8 x 64: 76 us, 4.0 TB/s).
 //
 // Work split: grid (kv head x tile of 16 query heads, items), an item being a
 // run of a sequence's positions; a workgroup of 4 waves takes one, and a wave
@@ -76,7 +77,8 @@ __device__ __forceinline__ u32x2 e4m3_to_bf16(uint32_t w) {
 
 // Q4: four codes u = q + 8, one in each byte -> bf16 u, exact: as an E4M3 code
 // a byte up to 15 stands for u 2^-9 (the subnormals and the first binade, which
-// have one step).
+// have one step).  As 136 + q, by byte permutes, sums were rounded 17 times as
+// much, for 125 us instead of 129 (16 x 32768 tokens of 8 x 128).
 __device__ __forceinline__ u32x2 q4_to_bf16(uint32_t w) {
   u32x2 o;
   o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, false));
@@ -101,7 +103,9 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
 }
 
 // 8 fp32 values -> three bf16 terms each, whose sum is the value: 8 of its 24
-// bits at a time, by truncation (the differences are exact).
+// bits at a time, by truncation (the differences are exact).  Two terms (16
+// bits) took 112 us instead of 125 for Q4 16 x 32768 tokens of 8 x 128, and as
+// long as three where memory bounds the call (bf16, E4M3).
 __device__ __forceinline__ void split_bf16(const float p[8], u32x4& hi, u32x4& mid, u32x4& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -783,8 +787,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a) {
 }
 
 // Replicas of the heads, Q4 only: as many as fit.  16 x 32768 tokens of 8 x
-// 128, 8 heads a kv head: 130 us with R = 1, 112 with 2; 4 heads: 127, 107, and
-// 102 with 4; of 4 x 256, 4 heads: 139, 112, 104; 32 x 16384 of 8 x 64: 74, 69.
+// 128, 8 heads a kv head: 156 us with R = 1, 129 with 2; 4 heads: 152, 124, and
+// 113 with 4; of 4 x 256, 4 heads: 160, 133, 118; 32 x 16384 of 8 x 64: 88, 76.
 template <int FMT, int NG, int W>
 void launch_fmt(const AttnArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MOST = FMT != W4_KV_Q4 ? 1 : NG < 4 ? 2 : 4, HALF = MOST < 2 ? 1 : 2;
@@ -812,12 +816,12 @@ int64_t head_tiles_of(int32_t heads, int32_t kv_heads) { return (heads / kv_head
 // How a call's positions are split.  The workgroups aimed at are those that
 // keep the memory busy: fewer and longer ones lose less in starts, ends and
 // partial results.  Measured (us; 256, 512, 768, 1024 workgroups): bf16 8 x
-// 32768 tokens of 8 x 128: 163, 167, 169, 169; bf16 32 x 8192 of 8 x 64: 85,
-// 89, 89, 88; bf16 16 x 8192 of 4 x 256: 89, 89, 93, 91; E4M3 32 x 32768
-// ragged of 8 x 128: 156, 141, 130, 129; E4M3 16 x 16384 of 8 x 128: 88, 90,
-// 90, 90; E4M3 16 x 16384 of 4 x 256: 89, 90, 100, 93; Q4 16 x 32768 of 8 x
-// 128: 145, 116, 111, 112; Q4 32 x 16384 of 8 x 64: 109, 80, 71, 67; Q4 16 x
-// 32768 of 4 x 256: 158, 103, 122, 108.
+// 32768 tokens of 8 x 128: 163, 169, 171, 168; bf16 32 x 8192 of 8 x 64: 85,
+// 90, 89, 89; bf16 16 x 8192 of 4 x 256: 89, 90, 92, 92; E4M3 32 x 32768
+// ragged of 8 x 128: 154, 143, 133, 129; E4M3 16 x 16384 of 8 x 128: 88, 91,
+// 91, 91; E4M3 16 x 16384 of 4 x 256: 90, 91, 100, 93; Q4 16 x 32768 of 8 x
+// 128: 162, 135, 128, 128; Q4 32 x 16384 of 8 x 64: 117, 86, 80, 77; Q4 16 x
+// 32768 of 4 x 256: 165, 117, 128, 122.
 int64_t target_of(int32_t format, int32_t head_dim) {
   if (format == W4_KV_BF16) return 256;
   if (format == W4_KV_E4M3) return head_dim == 256 ? 256 : 768;
@@ -839,9 +843,9 @@ constexpr int64_t kUnsplit = 4096, kMostCounted = 256;
 // With too few rows to fill the card, splitting a short row costs more (a
 // second launch and its start) than one workgroup of 8 waves takes for it.  In
 // tokens x dimensions (us in a graph, split against wide): Q4 1 x 500 tokens of
-// 8 x 128: 8.8, 7.6; 1 x 1000: 8.9, 10.3; 1 x 250 of 4 x 256: 10.2, 8.8; 1 x
-// 500: 10.2, 11.1; with more rows up to twice as far (12 x 1000 of 8 x 128:
-// 12.0, 10.7; bf16 16.8, 15.8; Q4 12 x 2000: 14.4, 16.3).
+// 8 x 128: 8.9, 8.1; 1 x 1000: 8.9, 11.1; 1 x 250 of 4 x 256: 10.3, 9.2; 1 x
+// 500: 10.4, 11.8; with more rows up to twice as far (12 x 1000 of 8 x 128:
+// 12.1, 11.5; bf16 17.0, 15.1; Q4 12 x 2000: 14.7, 17.8).
 constexpr int64_t kWide = 512 * 128, kWideManyRows = 2 * kWide, kManyRows = 64;
 
 Plan plan_of(int64_t target, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t tokens) {

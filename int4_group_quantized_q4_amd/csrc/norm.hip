@@ -18,9 +18,9 @@
 // do, and chunks with a |w'| over 2^8 (or one that is not finite), take the same
 // steps in 64 bits.
 //
-// Bound by memory for many rows (4096 x 2816 with residual, E4M3: 17.8 us, 4.5
-// TB/s; 8191 x 4096 bf16: 22.7 us, 5.9 TB/s), by latency for few (one row 2.6
-// us, 64 rows 4.0).  With the per-element arithmetic in 64 bits too they took
+// Bound by memory for many rows (4096 x 2816 with residual, E4M3: 18.0 us, 4.5
+// TB/s; 8191 x 4096 bf16: 23.4 us, 5.7 TB/s), by latency for few (one row 2.8
+// us, 64 rows 4.2).  With the per-element arithmetic in 64 bits too they took
 // 22.2, 29.1, 2.9 and 4.5 us.  A workgroup takes a row; a wave alone, holding
 // 6 or 8 chunks a lane, was slower (22.4 us, and spilling).
 
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kNormThreads) add_rmsnorm_kernel(NormArgs a) {
 
 // Rows of up to 1024 values leave lanes of a workgroup idle: a wave takes one
 // (32768 x 1024 bf16: 51.7 against 60.7 us, 65536 x 512 E4M3: 50.5 against
-// 93.4; 8 rows of 1024: 3.6 against 3.0).
+// 93.4).  The rule does not look at the number of rows; few of them would be
+// faster by workgroups (8 rows of 1024: 3.0 against 3.6 us).
 constexpr int kWaveChunks = 128;
 
 template <bool QUANT, bool OFFSET>
