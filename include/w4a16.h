@@ -645,6 +645,153 @@ int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_
                        int32_t window, uint16_t* out, float* lse, unsigned long long* counters, void* ws,
                        size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------- around the matmuls (serving step)
+ * What a serving step runs beside the calls above: the plan of its rows over the
+ * paged cache (kv_cache_write's slots, kv_cache_attention's table and lengths),
+ * the adapters of its requests beside a projection, the rotary positions of q and
+ * k in front of the cache, and the draw of the next tokens from the logits.
+ */
+
+/*
+ * kv_cache_plan -- pages, slots and positions of a step, from the sequences'
+ * lengths alone.  Sequence i holds seq_lens[i] tokens in the pages
+ * block_table[i][0 .. ceil(seq_lens[i] / page_size)).
+ *   new_tokens[i] >= 0: it gets that many rows behind those, with the pages they
+ *     need from the stack free_pages[0 .. free_count);
+ *   new_tokens[i] < 0: it has ended: its pages go back onto the stack, and its
+ *     length becomes 0.
+ * Pages are first put onto the stack, in the order of the sequences and of their
+ * table rows, then taken off its end, in that order too.  The step's rows are
+ * numbered through the sequences: sequence i's are [row_offsets[i],
+ * row_offsets[i + 1]).  From the first sequence on whose rows pass max_rows, or
+ * whose pages are more than the stack holds (both counted through the sequences),
+ * no sequence gets rows or pages; ended ones give theirs back all the same.
+ *   seq_lens        in  [seqs] int32
+ *   new_tokens      in  [seqs] int32
+ *   block_table     in/out [seqs][table_width] int32: the new pages' columns are
+ *                   written, all others stay
+ *   free_pages      in/out [capacity] int32: entries above the stack's end are
+ *                   written as pages come back
+ *   free_count      in  [1] int32 (cut to [0, capacity])
+ *   seq_lens_out    out [seqs] int32: the lengths with the new rows
+ *   free_count_out  out [1] int32
+ *   row_offsets     out [seqs + 1] int32
+ *   slots           out [max_rows] int64: page * page_size + place in the page;
+ *                   -1 behind the last row (kv_cache_write skips those)
+ *   positions       out [max_rows] int32: place in the sequence; 0 behind the last row
+ *   row_seqs        out, nullable  [max_rows] int32: the row's sequence; -1 behind
+ *                   the last row
+ *   counters        in/out, nullable, 8-byte aligned, two values (the caller
+ *                   zeroes them): counters[0] += sequences with a length below 0
+ *                   or past table_width * page_size, before the step or after it
+ *                   (they get no rows and give nothing back, and their lengths
+ *                   stay), and pages that came back to a full stack (they are
+ *                   lost); counters[1] += sequences that got no rows for want of
+ *                   pages or rows
+ * seq_lens_out may be seq_lens and free_count_out may be free_count.  With other
+ * memory for both, a step can be planned again from the same state.  Page ids are
+ * passed on as they are.  Every other overlap of an output with another argument
+ * is W4_ERR_ARG.  int32 arrays 4-byte, slots 8-byte aligned.
+ * Requires seqs <= 65535, page_size a power of two from 16 to 65536, table_width
+ * * page_size < 2^31, capacity < 2^31, max_rows <= 2^26.
+ */
+int kv_cache_plan(const int32_t* seq_lens, const int32_t* new_tokens, int64_t seqs, int32_t* block_table,
+                  int64_t table_width, int32_t page_size, int32_t* free_pages, int64_t capacity,
+                  const int32_t* free_count, int32_t* seq_lens_out, int32_t* free_count_out, int32_t* row_offsets,
+                  int64_t* slots, int32_t* positions, int32_t* row_seqs, int64_t max_rows,
+                  unsigned long long* counters, hipStream_t stream);
+
+/*
+ * w4a16_rope -- rotary positions of the rows' queries and keys.
+ * Of every head the first rotary_dim dimensions are turned in pairs, pair j of a
+ * row at position p by the angle t = p * inv_freq[j]:
+ *   (a, b) -> scale * (a cos t - b sin t,  b cos t + a sin t)
+ * with the pair's dimensions (j, j + rotary_dim/2) (W4_ROPE_HALF) or (2j, 2j + 1)
+ * (W4_ROPE_INTERLEAVED); the dimensions behind rotary_dim stay as they are.
+ * Scalings for long contexts are a matter of inv_freq and scale.  Angles are
+ * reduced in 64 bits and more (an angle of 2^31 keeps 2^-22), cos and sin are
+ * fp32 and the sums fp32, rounded once.  A negative position turns back.
+ *   q, k       in  [rows] rows of heads*head_dim bf16, strides in elements
+ *              (multiples of 8, at least the row's width); k nullable (k_heads 0)
+ *   positions  in  [rows] int32
+ *   inv_freq   in  [rotary_dim/2] fp32
+ *   q_out, k_out  out, as q and k
+ * q_out may be q with q's stride, and k_out k with its; q and k may be slices of one
+ * buffer, and so may q_out and k_out.  Any other overlap of an output with another
+ * argument is W4_ERR_ARG.  positions and inv_freq 4-byte aligned.
+ * Requires head_dim % 16 == 0 and rotary_dim % 16 == 0, 16 <= rotary_dim <= head_dim
+ * <= 512, 1 <= q_heads, q_heads + k_heads <= 4096, rows < 2^27, rows * stride <=
+ * 2^48, finite scale.
+ */
+enum { W4_ROPE_HALF = 0, W4_ROPE_INTERLEAVED = 1 };
+int w4a16_rope(const uint16_t* q, int64_t q_stride, int32_t q_heads, const uint16_t* k, int64_t k_stride,
+               int32_t k_heads, int64_t rows, int32_t head_dim, int32_t rotary_dim, int32_t layout,
+               const int32_t* positions, const float* inv_freq, float scale, uint16_t* q_out, int64_t q_out_stride,
+               uint16_t* k_out, int64_t k_out_stride, hipStream_t stream);
+
+/*
+ * w4a16_lora_add -- low-rank adapters of many requests beside a projection
+ * (w4a16_linear or any other), each row its own:
+ *   out[t] = bf16( y[t] + scaling[i] * sum_r (sum_k x[t][k] a[i][r][k]) b[i][n][r] ),
+ * i = adapter_ids[t]; a row whose id lies outside [0, adapters) has no adapter: its
+ * out is y.  Sums are fp32, and the inner one enters the outer one with 24 bits.
+ *   x            in  [rows] rows of K bf16, x_stride elements apart
+ *   adapter_ids  in  [rows] int32
+ *   a, b         in  [adapters][rank][K], [adapters][N][rank] bf16; an adapter of a
+ *                smaller rank is filled up with zeros
+ *   scaling      in, nullable (1)  [adapters] fp32
+ *   y, out       in, out [rows] rows of N bf16; out may be y with its stride, any
+ *                other overlap of out or ws with another argument is W4_ERR_ARG
+ *   ws           w4a16_lora_workspace(...) bytes, 16-byte aligned; its contents do not
+ *                matter.  Calls that overlap in time need one each.
+ * Strides are multiples of 8 and at least the row's width.  Rows do not depend on
+ * one another: NaN and infinities of one leave the others as they are.
+ * Requires K % 32 == 0, K >= 32, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 256, K and N <=
+ * 2^20, adapters <= 65535, rows <= 2^24, rows * stride <= 2^48.
+ */
+size_t w4a16_lora_workspace(int64_t rows, int64_t K, int64_t N, int64_t adapters, int32_t rank);
+int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K, const int32_t* adapter_ids,
+                   const uint16_t* a, const uint16_t* b, const float* scaling, int64_t adapters, int32_t rank,
+                   int64_t N, const uint16_t* y, int64_t y_stride, uint16_t* out, int64_t out_stride, void* ws,
+                   size_t ws_bytes, hipStream_t stream);
+
+/*
+ * w4a16_sample -- one token a row, drawn from its logits z with a given number.
+ * With m = max z and weights w_i = exp((z_i - m) / temperature), the tokens in
+ * descending order of z (ties: the lower id first) are cut in turn
+ *   top_k   to the first top_k,
+ *   top_p   to the fewest first ones whose weights sum to at least top_p times the
+ *           sum of those that top_k left (at least one),
+ *   min_p   to those with w_i >= min_p,
+ * and the token is the lowest id whose sum of kept weights, over the ids up to it,
+ * exceeds uniform times the sum of all kept weights.
+ *   logits       in  [rows] rows of vocab values of logits_dtype (W4_OUT_BF16 or
+ *                W4_OUT_F32), stride elements apart (at least vocab), aligned to their
+ *                type
+ *   temperature  in, nullable (1)  [rows] fp32; not above 0 (or a NaN): the token of
+ *                the largest logit
+ *   top_k        in, nullable (off)  [rows] int32; off at 0 and below
+ *   top_p        in, nullable (off)  [rows] fp32; off at 1 and above and for a NaN
+ *   min_p        in, nullable (off)  [rows] fp32; off at 0 and below and for a NaN, above
+ *                1 as 1
+ *   uniforms     in  [rows] fp32 in [0, 1); others are cut to [0, 1], a NaN is 0
+ *   tokens       out [rows] int32
+ *   logprobs     out, nullable  [rows] fp32: log of the token's share of the kept weights
+ *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
+ *                matter.  Calls that overlap in time need one each.
+ * Weights and sums are 64-bit, so that a draw next to a border between two tokens falls
+ * on its side of it.  A logit of -infinity is never drawn; beside logits of +infinity no
+ * other is.  A row with a NaN, and one without a logit above -infinity: token -1, log
+ * probability NaN.
+ * int32 and fp32 arrays 4-byte aligned.  No output may overlap another argument
+ * (W4_ERR_ARG).  Requires 1 <= vocab <= 2^20, rows <= 65535.
+ */
+size_t w4a16_sample_workspace(int64_t rows, int64_t vocab);
+int w4a16_sample(const void* logits, int32_t logits_dtype, int64_t rows, int64_t vocab, int64_t stride,
+                 const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                 const float* uniforms, int32_t* tokens, float* logprobs, void* ws, size_t ws_bytes,
+                 hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,9 @@ W4_KV_BF16 = 0
 W4_KV_E4M3 = 1
 W4_KV_Q4 = 2
 
+W4_ROPE_HALF = 0
+W4_ROPE_INTERLEAVED = 1
+
 W4_KERNEL_AUTO = 0
 W4_KERNEL_STREAM = 1
 W4_KERNEL_TILED = 2
@@ -83,6 +86,15 @@ SIGNATURES = {
     "kv_cache_attention_workspace": (_sz, [_i64, _i32, _i32, _i32, _i64, _i32]),
     "kv_cache_attention": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _i32, _i64, _i32, _i32, _i32, _p, _i64, _p, _f32,
                                           _i32, _p, _p, _p, _p, _sz, _p]),
+    "kv_cache_plan": (ctypes.c_int, [_p, _p, _i64, _p, _i64, _i32, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p,
+                                     _p]),
+    "w4a16_rope": (ctypes.c_int, [_p, _i64, _i32, _p, _i64, _i32, _i64, _i32, _i32, _i32, _p, _p, _f32, _p, _i64, _p,
+                                  _i64, _p]),
+    "w4a16_lora_workspace": (_sz, [_i64, _i64, _i64, _i64, _i32]),
+    "w4a16_lora_add": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _i32, _i64, _p, _i64, _p, _i64, _p,
+                                      _sz, _p]),
+    "w4a16_sample_workspace": (_sz, [_i64, _i64]),
+    "w4a16_sample": (ctypes.c_int, [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
 

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "checks.h"
 #include "decode.h"
 #include "internal.h"
 #include "kv_layout.h"
@@ -14,14 +15,6 @@
 namespace {
 
 constexpr int kAbiVersion = 2;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
-int launch_status() {
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? W4_OK : W4_ERR_HIP;
-}
 
 int check_matrix(int64_t rows, int64_t K) {
   if (rows < 0 || K < 0) return W4_ERR_ARG;
@@ -389,7 +382,6 @@ int w4a16_moe_layer_sorted(int64_t T, int32_t E, int32_t k, int64_t d, int64_t I
 
 // Host checks of a layer call, everything but the workspace: W4_OK to run,
 // kLayerEmpty when there is nothing to enqueue, else the error.
-static constexpr int kLayerEmpty = 1;
 static int check_layer(const uint16_t* x, const float* logits, int64_t T, int32_t E, int32_t k, int64_t d, int64_t I,
                        const uint8_t* w1_q, const uint16_t* w1_s, const uint8_t* w2_q, const uint16_t* w2_s,
                        int32_t activation, const uint16_t* y) {
@@ -691,11 +683,6 @@ int w8a8_moe_layer(const uint16_t* x, const float* logits, int64_t T, int32_t E,
 // ---------------------------------------------------------------------------
 // Residual addition + RMS norm.
 
-static bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + qn && b < a + pn;
-}
-
 // Shared by both forms: W4_OK to run, kLayerEmpty for nothing to do, else the
 // error.  An output may be exactly one of the inputs (each element is read
 // before it is written, by the same thread), but no other overlap is allowed.
@@ -746,12 +733,6 @@ int w8a8_add_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const
 // ---------------------------------------------------------------------------
 // Key-value cache.
 
-static int log2_of(int64_t v) {
-  int s = 0;
-  while (((int64_t)1 << s) < v) ++s;
-  return s;
-}
-
 static int check_kv_shape(int32_t format, int64_t n_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
   if (format != W4_KV_BF16 && format != W4_KV_E4M3 && format != W4_KV_Q4) return W4_ERR_ARG;
   if (n_pages < 0 || page_size < 1 || kv_heads < 1 || head_dim < 1) return W4_ERR_ARG;
@@ -783,29 +764,6 @@ static w4::KvArgs kv_args(int32_t format, void* cache, int64_t n_pages, int32_t 
   a.tokens = tokens;
   a.counters = counters;
   return a;
-}
-
-// Rows of the caller's k / v / q: 16-byte aligned, `stride` elements apart.
-static int check_rows(const void* p, int64_t rows, int64_t stride, int64_t width) {
-  if (!p || !aligned16(p)) return W4_ERR_ARG;
-  if (stride < width || stride % 8 != 0) return W4_ERR_ARG;
-  return rows > 0 && stride > ((int64_t)1 << 48) / rows ? W4_ERR_SHAPE : W4_OK;
-}
-
-static size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int64_t element) {
-  return (size_t)(((rows - 1) * stride + width) * element);
-}
-
-// Two sets of rows that share memory; rows of one buffer side by side (one
-// stride, a row's width or more apart) do not.
-static bool rows_overlap(const void* p, int64_t ps, const void* q, int64_t qs, int64_t rows, int64_t width,
-                         int64_t element) {
-  if (!overlap(p, rows_bytes(rows, ps, width, element), q, rows_bytes(rows, qs, width, element))) return false;
-  if (ps != qs) return true;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  const uintptr_t pitch = (uintptr_t)(ps * element), bytes = (uintptr_t)(width * element);
-  const uintptr_t apart = (a < b ? b - a : a - b) % pitch;   // of a row and the nearest one before it
-  return apart < bytes || pitch - apart < bytes;
 }
 
 static int check_kv_rows(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
@@ -856,7 +814,7 @@ int kv_cache_read(const void* cache, int32_t format, int64_t n_pages, int32_t pa
   const int st = check_kv_rows(k, v, tokens, k_stride, v_stride, slots, format, cache, n_pages, page_size, kv_heads,
                                head_dim, counters, element);
   if (st != W4_OK) return st == kLayerEmpty ? W4_OK : st;
-  if (rows_overlap(k, k_stride, v, v_stride, tokens, width, element) ||
+  if (rows_overlap(k, k_stride, width, v, v_stride, width, tokens, element) ||
       overlap(slots, tokens * 8, k, rows_bytes(tokens, k_stride, width, element)) ||
       overlap(slots, tokens * 8, v, rows_bytes(tokens, v_stride, width, element)))
     return W4_ERR_ARG;

@@ -5,18 +5,21 @@ every computation runs in the library's HIP kernels on the given stream
 
 A few allocating helpers (``repack``, ``dequant``, ``pack_codes``,
 ``linear``, ``moe_route``, ``moe_layer``, ``add_rmsnorm``,
-``add_rmsnorm_quantize``, ``kv_cache``, ``kv_attention``) create the output
-tensors with torch and then make the same calls.
+``add_rmsnorm_quantize``, ``kv_cache``, ``kv_attention``, ``kv_plan``,
+``rope``, ``lora_add``, ``sample``) create the output tensors with torch and
+then make the same calls; ``rope_frequencies`` computes w4a16_rope's table on
+the host.
 """
 
 import contextlib
 import ctypes
 import functools
+import math
 
 import torch
 
 from . import _lib
-from ._lib import (W4_EPI_NONE, W4_EPI_GEGLU_TANH, W4_EPI_SWIGLU, W4_OUT_BF16, W4_OUT_F32,
+from ._lib import (W4_EPI_NONE, W4_EPI_GEGLU_TANH, W4_EPI_SWIGLU, W4_OUT_BF16, W4_OUT_F32, W4_ROPE_HALF,
                    check, lib)
 
 _BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
@@ -597,6 +600,107 @@ def kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_l
           _arg(counters, "counters", _I64, 16, d), _arg(ws, "ws", _U8, 0, d), 0 if ws is None else ws.numel())
 
 
+def kv_cache_plan(seq_lens, new_tokens, block_table, page_size, free_pages, free_count, seq_lens_out, free_count_out,
+                  row_offsets, slots, positions, row_seqs=None, counters=None, stream=None):
+    """Pages, slots and positions of a step: new_tokens[i] more rows for each
+    sequence (below 0: it has ended).  As many rows fit as slots holds."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs, width]")
+    seqs, width = block_table.shape
+    d = block_table.get_device()
+    n, rows = seqs * 4, slots.numel()
+    _call("kv_cache_plan", d, stream, _arg(seq_lens, "seq_lens", _I32, n, d, False),
+          _arg(new_tokens, "new_tokens", _I32, n, d, False), seqs, _arg(block_table, "block_table", _I32, 0, d, False),
+          width, page_size, _arg(free_pages, "free_pages", _I32, 0, d, False), free_pages.numel(),
+          _arg(free_count, "free_count", _I32, 4, d, False), _arg(seq_lens_out, "seq_lens_out", _I32, n, d, False),
+          _arg(free_count_out, "free_count_out", _I32, 4, d, False),
+          _arg(row_offsets, "row_offsets", _I32, n + 4, d, False), _arg(slots, "slots", _I64, 0, d, False),
+          _arg(positions, "positions", _I32, rows * 4, d, False), _arg(row_seqs, "row_seqs", _I32, rows * 4, d), rows,
+          _arg(counters, "counters", _I64, 16, d))
+
+
+def w4a16_rope(q, k, positions, inv_freq, q_out, k_out, layout=W4_ROPE_HALF, scale=1.0, stream=None):
+    """Turn the first 2 * len(inv_freq) dimensions of every head of q
+    [rows, heads, dim] and k (or None) by positions [rows]."""
+    qp, qs = _rows(q, "q", _BF16_LIKE)
+    op, os_ = _rows(q_out, "q_out", _BF16_LIKE, q)
+    _on_device(q, "q")
+    rows, heads, dim = q.shape
+    d = q.get_device()
+    kp = ko = None
+    ks = kos = kh = 0
+    if k is not None:
+        kp, ks = _rows(k, "k", _BF16_LIKE)
+        ko, kos = _rows(k_out, "k_out", _BF16_LIKE, k)
+        kh = k.shape[1]
+        if k.shape[0] != rows or k.shape[2] != dim or k.get_device() != d:
+            raise ValueError("k is %s on %s, expected [%d, heads, %d] on %s"
+                             % (tuple(k.shape), k.device, rows, dim, q.device))
+    _call("w4a16_rope", d, stream, qp, qs, heads, kp, ks, kh, rows, dim, 2 * inv_freq.numel(), layout,
+          _arg(positions, "positions", _I32, rows * 4, d, False), _arg(inv_freq, "inv_freq", _F32, 0, d, False), scale,
+          op, os_, ko, kos)
+
+
+def w4a16_lora_workspace(rows, K, N, adapters, rank):
+    return int(lib().w4a16_lora_workspace(rows, K, N, adapters, rank))
+
+
+def _row_matrix(t, name):
+    """Pointer and row stride of t [rows, width] bf16 whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be [rows, width], got %s" % (name, tuple(t.shape)))
+    return _rows(t.unsqueeze(1), name, _BF16_LIKE)
+
+
+def w4a16_lora_add(x, adapter_ids, a, b, scaling, y, out, ws=None, stream=None):
+    """out = bf16(y + scaling[i] (x a[i]^T) b[i]^T) for every row of x [rows, K],
+    y and out [rows, N], i its adapter: a [adapters, rank, K], b [adapters, N,
+    rank]."""
+    xp, xs = _row_matrix(x, "x")
+    yp, ys = _row_matrix(y, "y")
+    op, os_ = _row_matrix(out, "out")
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must be [adapters, rank, K] and [adapters, N, rank]")
+    (rows, K), (adapters, rank, ak), (bn, N, br), d = x.shape, a.shape, b.shape, x.get_device()
+    if ak != K or bn != adapters or br != rank or y.shape != (rows, N) or out.shape != (rows, N):
+        raise ValueError("x %s, a %s, b %s, y %s and out %s do not fit together" % tuple(
+            tuple(t.shape) for t in (x, a, b, y, out)))
+    if y.get_device() != d or out.get_device() != d:
+        raise ValueError("x, y and out must be on one device")
+    _on_device(x, "x")
+    _call("w4a16_lora_add", d, stream, xp, xs, rows, K, _arg(adapter_ids, "adapter_ids", _I32, rows * 4, d, False),
+          _arg(a, "a", _BF16_LIKE, 0, d, False), _arg(b, "b", _BF16_LIKE, 0, d, False),
+          _arg(scaling, "scaling", _F32, adapters * 4, d), adapters, rank, N, yp, ys, op, os_,
+          _arg(ws, "ws", _U8, 0, d), 0 if ws is None else ws.numel())
+
+
+def w4a16_sample_workspace(rows, vocab):
+    return int(lib().w4a16_sample_workspace(rows, vocab))
+
+
+def w4a16_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+                 ws=None, stream=None):
+    """tokens [rows]: one drawn from each row of logits [rows, vocab] with
+    uniforms [rows]; the filters are [rows] each, or None."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    if logits.dtype != torch.float32 and logits.dtype != torch.bfloat16:
+        raise TypeError("logits has dtype %s, expected bfloat16 or float32" % logits.dtype)
+    (rows, vocab), (step, one) = logits.shape, logits.stride()
+    if (vocab > 1 and one != 1) or (rows > 1 and step < vocab):
+        raise ValueError("logits: rows must be contiguous and not overlap")
+    _on_device(logits, "logits")
+    d, n = logits.get_device(), rows * 4
+    _call("w4a16_sample", d, stream, logits.data_ptr(),
+          W4_OUT_F32 if logits.dtype == torch.float32 else W4_OUT_BF16, rows, vocab, max(step, vocab),
+          _arg(temperature, "temperature", _F32, n, d), _arg(top_k, "top_k", _I32, n, d),
+          _arg(top_p, "top_p", _F32, n, d), _arg(min_p, "min_p", _F32, n, d),
+          _arg(uniforms, "uniforms", _F32, n, d, False), _arg(tokens, "tokens", _I32, n, d, False),
+          _arg(logprobs, "logprobs", _F32, n, d), _arg(ws, "ws", _U8, 0, d), 0 if ws is None else ws.numel())
+
+
 # -------------------------------------------------------- allocating helpers
 def repack(w, stream=None):
     """bf16 [rows, K] -> (qweight uint8 [rows*K/2], scales bf16 [rows*K/32]
@@ -770,3 +874,83 @@ def kv_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, s
     kv_cache_attention(q, cache, format, page_size, kv_heads, block_table, seq_lens, scale, out, window, lse, ws,
                        stream=stream)
     return out, lse
+
+
+def kv_plan(seq_lens, new_tokens, block_table, page_size, free_pages, free_count, max_rows, stream=None):
+    """kv_cache_plan in place (lengths, table and stack), with freshly allocated
+    (slots, positions, row_seqs, row_offsets)."""
+    dev = block_table.device
+    with _allocating(dev, stream):
+        slots = torch.empty(max_rows, dtype=torch.int64, device=dev)
+        positions = torch.empty(max_rows, dtype=torch.int32, device=dev)
+        row_seqs = torch.empty(max_rows, dtype=torch.int32, device=dev)
+        row_offsets = torch.empty(block_table.shape[0] + 1, dtype=torch.int32, device=dev)
+    kv_cache_plan(seq_lens, new_tokens, block_table, page_size, free_pages, free_count, seq_lens, free_count,
+                  row_offsets, slots, positions, row_seqs, stream=stream)
+    return slots, positions, row_seqs, row_offsets
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained=None, fast=32.0, slow=1.0):
+    """(inv_freq float32 CPU tensor [rotary_dim/2], scale) for w4a16_rope.  Pair j
+    turns by f_j = base^(-2j/rotary_dim) a position; for contexts `factor` times as
+    long as the `trained` ones (positions):
+      None      f_j
+      "linear"  f_j / factor
+      "base"    the base times factor^(rotary_dim / (rotary_dim - 2)): the slowest
+                pair's turns are divided by factor, the fastest pair's stay
+      "bands"   pairs with at least `fast` turns in the trained context stay, those
+                with at most `slow` are divided by factor, in between linearly in j;
+                scale is 1 + 0.1 ln(factor)"""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive, got %s" % rotary_dim)
+    if not factor >= 1.0:
+        raise ValueError("factor must be at least 1, got %s" % factor)
+    j = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    freq = lambda base: base ** (-2.0 * j / rotary_dim)
+    if scaling is None:
+        return freq(base).float(), 1.0
+    if scaling == "linear":
+        return (freq(base) / factor).float(), 1.0
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling the base needs a rotary_dim of at least 4")
+        return freq(base * factor ** (rotary_dim / (rotary_dim - 2))).float(), 1.0
+    if scaling != "bands":
+        raise ValueError("unknown scaling %r" % (scaling,))
+    if trained is None or not fast > slow > 0:
+        raise ValueError("bands need the trained length and fast > slow > 0")
+    # the pair that makes r turns in the trained context
+    at = lambda r: rotary_dim * math.log(trained / (2.0 * math.pi * r)) / (2.0 * math.log(base))
+    lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rotary_dim - 1)
+    part = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+    return (freq(base) * (1.0 - part + part / factor)).float(), 1.0 + 0.1 * math.log(factor)
+
+
+def rope(q, k, positions, inv_freq, layout=W4_ROPE_HALF, scale=1.0, stream=None):
+    """w4a16_rope into freshly allocated tensors; returns (q, k) turned."""
+    with _allocating(q.device, stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    w4a16_rope(q, k, positions, inv_freq, q_out, k_out, layout, scale, stream)
+    return q_out, k_out
+
+
+def lora_add(x, adapter_ids, a, b, scaling, y, stream=None):
+    """w4a16_lora_add into a freshly allocated tensor."""
+    need = w4a16_lora_workspace(x.shape[0], x.shape[1], y.shape[1], a.shape[0], a.shape[1])
+    with _allocating(x.device, stream):
+        out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        ws = torch.empty(max(16, need), dtype=torch.uint8, device=y.device)
+    w4a16_lora_add(x, adapter_ids, a, b, scaling, y, out, ws, stream)
+    return out
+
+
+def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """w4a16_sample into freshly allocated (tokens, logprobs)."""
+    rows, vocab = logits.shape
+    with _allocating(logits.device, stream):
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        ws = torch.empty(max(16, w4a16_sample_workspace(rows, vocab)), dtype=torch.uint8, device=logits.device)
+    w4a16_sample(logits, uniforms, tokens, temperature, top_k, top_p, min_p, logprobs, ws, stream)
+    return tokens, logprobs
