@@ -1,0 +1,195 @@
+"""GPU parity of w4a16_sample against oracle/serving.py: tokens exactly (both sides
+weigh and add in 64 bits), log probabilities to half an fp32 step and 2^-40 of
+their sums."""
+
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_q4_amd as w4
+import oracle
+from oracle import serving
+from gpu_util import bf16_dev, dev, say
+
+pytestmark = pytest.mark.gpu
+
+
+def run(z, temperature=None, top_k=None, top_p=None, min_p=None, uniform=None, dtype="f32", stride=0):
+    """z: float64 rows that dtype holds exactly; settings: a value or one a row."""
+    rows, V = z.shape
+    d = bf16_dev(oracle.bf16_from_f64(z)) if dtype == "bf16" else torch.tensor(z, dtype=torch.float32, device=dev())
+    if stride:
+        wide = torch.full((rows, V + stride), float("nan"), dtype=d.dtype, device=dev())
+        wide[:, 1:1 + V] = d
+        d = wide[:, 1:1 + V]
+    f = lambda v, t: None if v is None else torch.tensor(np.broadcast_to(v, rows).copy(), dtype=t, device=dev())
+    u = np.zeros(rows) if uniform is None else np.broadcast_to(uniform, rows)
+    tokens, lp = w4.sample(d, f(u, torch.float32), f(temperature, torch.float32), f(top_k, torch.int32),
+                           f(top_p, torch.float32), f(min_p, torch.float32))
+    torch.cuda.synchronize()
+    at = lambda v, i, default: default if v is None else np.broadcast_to(v, rows)[i]
+    for i in range(rows):
+        token, want, kept = serving.sample(z[i], at(temperature, i, 1.0), int(at(top_k, i, 0)), at(top_p, i, 1.0),
+                                           at(min_p, i, 0.0), u[i])
+        got = lp[i].item()
+        assert tokens[i].item() == token, (i, tokens[i].item(), token, len(kept))
+        close = abs(got - want) <= abs(want) * 2.0 ** -24 + 2.0 ** -40
+        assert close or (np.isnan(got) and np.isnan(want)), (i, got, want)
+    return tokens.cpu().numpy(), lp.cpu().numpy()
+
+
+def logits(rng, rows, V, dtype, sigma=2.0, peak=18.0):
+    z = sigma * rng.standard_normal((rows, V))
+    head = min(V, 500)
+    for i in range(rows):
+        ids = rng.permutation(V)[:head]
+        z[i, ids] = np.maximum(z[i, ids], peak - rng.uniform(1.2, 3) * np.log(np.arange(1, head + 1)))
+    if dtype == "bf16":
+        return oracle.bf16_bits_to_f64(oracle.bf16_from_f64(z))
+    return z.astype(np.float32).astype(np.float64)
+
+
+SIZES = [(1, 1), (3, 2), (5, 63), (2, 64), (4, 65), (7, 1000), (3, 2047), (2, 4097), (64, 8192), (5, 32771),
+         (2, 131072), (3, 200003), (1, 1 << 20)]
+
+
+@pytest.mark.parametrize("rows,V", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mixed_settings(rows, V, dtype):
+    say("[sample] rows=%d vocab=%d %s" % (rows, V, dtype))
+    rng = np.random.default_rng(V + rows)
+    z = logits(rng, rows, V, dtype)
+    pick = lambda *v: rng.choice(v, rows)
+    for trial in range(3):
+        run(z, pick(0.0, 0.7, 1.0, 1.3), pick(0, 1, 20, 50, 300, 5000), pick(1.0, 0.5, 0.9, 0.95, 0.999),
+            pick(0.0, 0.0, 0.01, 0.1), rng.random(rows).astype(np.float32), dtype, stride=trial * 3)
+    run(z, uniform=rng.random(rows).astype(np.float32), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_flat_distributions(dtype):
+    """Nuclei of thousands of tokens, and top_k past any candidate list."""
+    rng = np.random.default_rng(1)
+    z = logits(rng, 6, 50000, dtype, sigma=1.0, peak=3.0)
+    u = rng.random(6).astype(np.float32)
+    run(z, top_p=[0.1, 0.5, 0.9, 0.99, 0.9999, 0.999999], uniform=u, dtype=dtype)
+    run(z, top_k=[100, 1000, 3000, 10000, 49999, 50000], uniform=u, dtype=dtype)
+    run(z, min_p=[1e-6, 1e-4, 1e-3, 0.01, 0.1, 0.5], uniform=u, dtype=dtype)
+    run(z, temperature=[5.0, 50.0, 1e4, 3.0, 2.0, 1e30], top_k=20000, top_p=0.9, min_p=1e-5, uniform=u, dtype=dtype)
+
+
+@pytest.mark.parametrize("V", [1, 5, 64, 1000, 40000])
+def test_ties(V):
+    """All logits equal, and a few values only: order and draw go by the id alone, sums of equal weights are exact."""
+    n = 9
+    u = (np.arange(n) / n).astype(np.float32)
+    z = np.full((n, V), 3.25)
+    run(z, uniform=u)
+    run(z, top_k=max(1, V // 2), uniform=u)
+    run(z, top_p=0.5, uniform=u)
+    run(z, top_p=0.25, top_k=max(1, V // 4 * 2), uniform=u, dtype="bf16")
+    run(z, min_p=1.0, uniform=u)
+    rng = np.random.default_rng(V)
+    z = rng.choice([0.0, -1.0, -2.0, 1.0, -0.0], (n, V))
+    for kw in (dict(top_k=max(1, V // 3)), dict(top_p=0.3), dict(top_p=0.9, top_k=max(1, V // 2)), dict(min_p=0.2),
+               dict(temperature=0.0)):
+        run(z, uniform=u, **kw)
+
+
+def test_masks_and_special_values():
+    rng = np.random.default_rng(2)
+    V, inf = 3000, np.inf
+    z = logits(rng, 12, V, "f32")
+    z[0, :] = -inf
+    z[1, :] = -inf
+    z[1, 1234] = -5.0                       # one token allowed
+    z[2, 17] = np.nan
+    z[3, 17] = -np.nan
+    z[4, [5, 900, 2999]] = inf
+    z[5, :] = -3.0e38                       # the type's lowest values, and one above
+    z[5, 77] = -2.0e38
+    z[6] = np.where(rng.random(V) < 0.99, -inf, z[6])
+    z[7, :] = inf
+    z[8, :2990] = -np.finfo(np.float32).max
+    z[9] = 1e-42 * rng.integers(0, 5, V)    # subnormal logits
+    z[9] = z[9].astype(np.float32)
+    z[10, 100] = np.finfo(np.float32).max
+    z[11] = np.where(np.arange(V) == 2998, 0.0, -inf)
+    u = rng.random(12).astype(np.float32)
+    run(z, uniform=u)
+    run(z, 0.7, 50, 0.9, 0.05, u)
+    run(z, 0.0, uniform=u)
+    run(z, 1.0, 2000, uniform=u)
+    run(z, 3.0, top_p=0.99, uniform=u)
+    run(z, float("inf"), uniform=u)
+    run(z, float("inf"), top_p=0.5, uniform=u)
+
+
+def test_special_settings():
+    rng = np.random.default_rng(3)
+    z = logits(rng, 8, 5000, "f32")
+    nan, inf = float("nan"), float("inf")
+    u = rng.random(8).astype(np.float32)
+    run(z, temperature=[0.0, -1.0, nan, 1e-30, 1e-45, 1e30, inf, 0.01], uniform=u)
+    run(z, top_k=[0, -1, -2 ** 31, 2 ** 31 - 1, 5000, 4999, 1, 2], uniform=u)
+    run(z, top_p=[0.0, -1.0, nan, 2.0, inf, 1e-30, 1.0, -inf], uniform=u)
+    run(z, min_p=[0.0, -1.0, nan, 2.0, inf, 1e-30, 1.0, -inf], uniform=u)
+    below = np.nextafter(np.float32(1), np.float32(0))
+    for kw in (dict(), dict(top_k=7), dict(top_p=0.8)):
+        run(z, uniform=np.array([0.0, -1.0, nan, 1.0, 5.0, below, inf, -inf], dtype=np.float32), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=40), dict(top_p=0.9), dict(min_p=0.01), dict(temperature=1.5)])
+def test_draws_follow_the_distribution(kw):
+    """Evenly spaced numbers meet each token as often as its share says, up to one at each of its two borders."""
+    rng = np.random.default_rng(4)
+    n, V = 4096, 300
+    one = logits(rng, 1, V, "f32", peak=6.0)
+    z = np.broadcast_to(one, (n, V)).copy()
+    tokens, _ = run(z, uniform=((np.arange(n) + 0.5) / n).astype(np.float32), **kw)
+    t = kw.get("temperature", 1.0)
+    _, _, kept = serving.sample(one[0], t, kw.get("top_k", 0), kw.get("top_p", 1.0), kw.get("min_p", 0.0))
+    w = np.exp((one[0][kept] - one[0].max()) / t)
+    share = np.zeros(V)
+    share[kept] = w / w.sum()
+    assert (np.abs(np.bincount(tokens, minlength=V) - n * share) <= 1.0 + 1e-3).all()
+
+
+def test_rows_behind_and_strides():
+    rng = np.random.default_rng(5)
+    z = torch.tensor(logits(rng, 6, 999, "f32"), dtype=torch.float32, device=dev())
+    u = torch.rand(6, device=dev())
+    tokens = torch.full((6,), -9, dtype=torch.int32, device=dev())
+    lp = torch.full((6,), 9.0, device=dev())
+    ws = torch.full((max(16, w4.w4a16_sample_workspace(3, 999)),), 255, dtype=torch.uint8, device=dev())
+    w4.w4a16_sample(z[::2], u[:3], tokens, logprobs=lp, ws=ws)
+    want, wlp = w4.sample(z[::2].contiguous(), u[:3])
+    w4.w4a16_sample(z[:2], u, tokens[4:], ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(tokens[:3], want) and torch.equal(lp[:3], wlp)
+    assert tokens[3].item() == -9 and (lp[3:] == 9).all()
+
+
+@pytest.mark.parametrize("rows,V", [(1, 20000), (50, 3001)])
+def test_graph_replays(rows, V):
+    rng = np.random.default_rng(6)
+    z = torch.tensor(logits(rng, rows, V, "f32"), dtype=torch.float32, device=dev())
+    u = torch.rand(rows, device=dev())
+    k = torch.full((rows,), 30, dtype=torch.int32, device=dev())
+    p = torch.full((rows,), 0.9, device=dev())
+    tokens, lp = torch.empty(rows, dtype=torch.int32, device=dev()), torch.empty(rows, device=dev())
+    ws = torch.empty(max(16, w4.w4a16_sample_workspace(rows, V)), dtype=torch.uint8, device=dev())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w4.w4a16_sample(z, u, tokens, None, k, p, None, lp, ws)
+    for i in range(6):
+        u.uniform_()
+        k.fill_([30, 0, 2000, 1, 5, 100][i])
+        p.fill_([0.9, 1.0, 0.99, 0.5, 0.999, 0.7][i])
+        ws.fill_(255)
+        g.replay()
+        want, wlp = w4.sample(z, u, None, k, p)
+        torch.cuda.synchronize()
+        assert torch.equal(tokens, want) and torch.equal(lp, wlp)
