@@ -747,7 +747,7 @@ int w4a16_rope(const uint16_t* q, int64_t q_stride, int32_t q_heads, const uint1
  * Strides are multiples of 8 and at least the row's width.  Rows do not depend on
  * one another: NaN and infinities of one leave the others as they are.
  * Requires K % 32 == 0, K >= 32, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 256, K and N <=
- * 2^20, adapters <= 65535, rows <= 2^24, rows * stride <= 2^48.
+ * 2^20, adapters <= 4096, rows <= 2^20, rows * stride <= 2^48.
  */
 size_t w4a16_lora_workspace(int64_t rows, int64_t K, int64_t N, int64_t adapters, int32_t rank);
 int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K, const int32_t* adapter_ids,

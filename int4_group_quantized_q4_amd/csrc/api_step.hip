@@ -142,7 +142,7 @@ int w4a16_rope(const uint16_t* q, int64_t q_stride, int32_t q_heads, const uint1
 static int check_lora(int64_t rows, int64_t K, int64_t N, int64_t adapters, int32_t rank) {
   if (rows < 0 || K < 0 || N < 0 || adapters < 0 || rank < 0) return W4_ERR_ARG;
   if (K < 32 || K % 32 != 0 || N % 16 != 0 || rank % 8 != 0 || rank < 8 || rank > 256) return W4_ERR_SHAPE;
-  if (K > ((int64_t)1 << 20) || N > ((int64_t)1 << 20) || adapters > 65535 || rows > ((int64_t)1 << 24))
+  if (K > ((int64_t)1 << 20) || N > ((int64_t)1 << 20) || adapters > 4096 || rows > ((int64_t)1 << 20))
     return W4_ERR_SHAPE;
   return W4_OK;
 }

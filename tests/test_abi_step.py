@@ -83,8 +83,8 @@ def test_lora_refusals():
               dict(out=at(5) + 16), dict(out=at(5), os=520), dict(ws=at(0)), dict(ws=at(1)), dict(ws=at(2)),
               dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(ws=at(6))):
         assert f(*changed(a, **b)) == w4.W4_ERR_ARG, b
-    for b in (dict(K=0), dict(K=48), dict(N=24), dict(rank=0), dict(rank=12), dict(rank=264), dict(adapters=65536),
-              dict(K=(1 << 20) + 32, xs=1 << 21), dict(N=(1 << 20) + 16), dict(rows=(1 << 24) + 1), dict(xs=1 << 47)):
+    for b in (dict(K=0), dict(K=48), dict(N=24), dict(rank=0), dict(rank=12), dict(rank=264), dict(adapters=4097),
+              dict(K=(1 << 20) + 32, xs=1 << 21), dict(N=(1 << 20) + 16), dict(rows=(1 << 20) + 1), dict(xs=1 << 47)):
         assert f(*changed(a, **b)) == w4.W4_ERR_SHAPE, b
     need = lib.w4a16_lora_workspace(4, 256, 512, 3, 16)
     assert need > 0
