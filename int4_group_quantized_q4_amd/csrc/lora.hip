@@ -14,7 +14,7 @@
 //   expand  h enters as three bf16 terms that hold its 24 bits (their products
 //           with B are exact in the fp32 accumulators; one term would round h to
 //           8 bits).  The terms lie one after another along the product's inner
-//           dimension: 3 rank / 32 steps, B's row read again at each.
+//           dimension: 3 rank / 32 steps.
 
 #include "common.h"
 #include "serving.h"
@@ -28,6 +28,7 @@ constexpr int kWaves = kLoraThreads / 64;
 constexpr int kTile = 64;           // rows of one adapter in a tile
 constexpr int kDirectRows = 64;     // up to as many rows need no sort
 constexpr int kMaxSplits = 16;
+constexpr int kBatch = 4;           // steps of K whose loads a wave issues together
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;  // bins of the sort (and one for rows without)
 
@@ -186,11 +187,21 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(LoraArgs l, L
 #pragma unroll
       for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       const int b = s0 + min(steps, q * each), e = s0 + min(steps, (q + 1) * each);
-      for (int s = b; s < e; ++s) {
-        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xs + 32 * s);
+      for (int s = b; s < e; s += kBatch) {   // the loads of a batch together; past the end the last step again
+        bf16x8 xv[kBatch], av[kBatch][RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          acc[i] = mfma16x16x32(*reinterpret_cast<const bf16x8*>(as[i] + 32 * s), xv, acc[i]);
+        for (int j = 0; j < kBatch; ++j) {
+          const int at = 32 * min(s + j, e - 1);
+          xv[j] = *reinterpret_cast<const bf16x8*>(xs + at);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) av[j][i] = *reinterpret_cast<const bf16x8*>(as[i] + at);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s + j < e) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i] = mfma16x16x32(av[j][i], xv[j], acc[i]);
+          }
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -228,28 +239,44 @@ __device__ __forceinline__ uint16_t term_of(float v, int term) {
   return term == 1 ? (uint16_t)(__float_as_uint(rest) >> 16) : bf16_rne(rest - mid);
 }
 
-// A wave takes `pairs` times 32 columns; blockIdx.y: which.  G groups of 16
-// tokens at a time have their terms in LDS.
-template <int G>
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, LoraWork w, int pairs) {
+// Where the inner dimension's chunk of 8 (term, 8 ch ..) lies: step and lane
+// group.  Ranks of whole steps keep the terms of a chunk in successive steps, so
+// that B's chunk is loaded once for the three; below 32 the terms follow one
+// another, and B's chunk of a lane group is the same in all steps.
+__device__ __forceinline__ int2 place_of(int term, int ch, int chunks) {
+  if (chunks % 4 == 0) return {3 * (ch / 4) + term, ch % 4};
+  const int q = term * chunks + ch;
+  return {q / 4, q % 4};
+}
+
+// A wave takes `blocks` times 64 columns; blockIdx.y: which.  G groups of 16 tokens
+// at a time have their terms in LDS.  STEPS of the inner dimension and LOADS chunks
+// of B a lane: 1 and 1 (rank 8), 2 and 1 (16), 3 and 1 (32), 6 and 2 (64), 12 and 4
+// (128); STEPS 0: any rank, B's chunks loaded at every step.
+template <int G, int STEPS, int LOADS>
+__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, LoraWork w, int blocks) {
   extern __shared__ u32x4 s_terms[];   // [group][step][lane]: the operand's chunk of 8
   __shared__ int32_t s_rows[kTile];
   int id, count;
   if (!find_tile(l, w, s_rows, id, count)) return;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, c = lane >> 4;
-  const int groups = (count + 15) / 16, chunks = l.rank / 8, steps = (3 * chunks + 3) / 4;
-  const int n0 = (blockIdx.y * kWaves + wv) * pairs * 32;
+  const int groups = (count + 15) / 16, chunks = l.rank / 8;
+  const int steps = STEPS > 0 ? STEPS : (3 * chunks + 3) / 4;
+  const int n0 = (blockIdx.y * kWaves + wv) * blocks * 64;
   if (id < 0) {
     if (l.out == l.y) return;
-    for (int p = 0; p < pairs; ++p) {
-      const int n = n0 + 32 * p + 8 * c;
+    for (int p = 0; p < blocks; ++p) {
+      const int n = n0 + 64 * p + 16 * c;
       if (n >= l.N) break;
       for (int g = 0; g < groups; ++g)
         if (16 * g + m < count) {
           const int64_t row = s_rows[16 * g + m];
-          *reinterpret_cast<u32x4*>(l.out + row * l.out_stride + n) =
-              *reinterpret_cast<const u32x4*>(l.y + row * l.y_stride + n);
+          const u32x4* from = reinterpret_cast<const u32x4*>(l.y + row * l.y_stride + n);
+          const u32x4 v0 = from[0], v1 = from[1];
+          u32x4* to = reinterpret_cast<u32x4*>(l.out + row * l.out_stride + n);
+          to[0] = v0;
+          to[1] = v1;
         }
     }
     return;
@@ -259,72 +286,130 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
   for (int g0 = 0; g0 < groups; g0 += G) {
     const int here = min(G, groups - g0);
     if (g0 > 0) __syncthreads();   // the terms of the groups before are read
-    for (int i = threadIdx.x; i < here * steps * 64; i += kLoraThreads) {
-      const int q = 4 * (i / 64 % steps) + (i & 63) / 16, token = 16 * (g0 + i / 64 / steps) + (i & 15);
-      u32x4 o = {0u, 0u, 0u, 0u};
-      if (q < 3 * chunks && token < count) {
-        const int term = q / chunks;
-        const float* from = w.part + (int64_t)s_rows[token] * l.rank + 8 * (q - term * chunks);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = from[j];
-        for (int s = 1; s < w.splits; ++s) {
-          from += l.rows * l.rank;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += from[j];
+    for (int i = threadIdx.x; i < here * 16 * chunks; i += kLoraThreads) {
+      const int token = i / chunks, ch = i - token * chunks;
+      f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (16 * g0 + token < count) {
+        const f32x4* from = reinterpret_cast<const f32x4*>(w.part + (int64_t)s_rows[16 * g0 + token] * l.rank + 8 * ch);
+        const int64_t pitch = l.rows * l.rank / 4;
+#pragma unroll 4
+        for (int s = 0; s < w.splits; ++s) {
+          v[0] += from[s * pitch];
+          v[1] += from[s * pitch + 1];
         }
+      }
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        u32x4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          o[j] = term_of(v[2 * j] * scale, term) | ((uint32_t)term_of(v[2 * j + 1] * scale, term) << 16);
+          o[j] = term_of(v[j / 2][2 * (j & 1)] * scale, term) |
+                 ((uint32_t)term_of(v[j / 2][2 * (j & 1) + 1] * scale, term) << 16);
+        const int2 at = place_of(term, ch, chunks);
+        s_terms[((token / 16) * steps + at.x) * 64 + 16 * at.y + (token & 15)] = o;
       }
-      s_terms[i] = o;
+    }
+    // the last step's lane groups behind the terms
+    const int rest = 4 * steps - 3 * chunks;
+    for (int i = threadIdx.x; i < here * 16 * rest; i += kLoraThreads) {
+      const int g = i / (16 * rest), k = i - g * 16 * rest;
+      s_terms[(g * steps + steps - 1) * 64 + 16 * (4 - rest) + k] = u32x4{0u, 0u, 0u, 0u};
     }
     __syncthreads();
-    for (int p = 0; p < pairs; ++p) {
-      const int nb = n0 + 32 * p;
+    for (int p = 0; p < blocks; ++p) {
+      const int nb = n0 + 64 * p;
       if (nb >= l.N) break;
-      // rows n of the two left operands: the lane ends with 8 neighbouring columns
-      const int row0 = nb + 8 * (m / 4) + m % 4;
-      const uint16_t* b0 = bs + (int64_t)min(row0, l.N - 1) * l.rank;
-      const uint16_t* b1 = bs + (int64_t)min(row0 + 4, l.N - 1) * l.rank;
-      const int n = nb + 8 * c;
-      u32x4 old[G];
-      f32x4 acc[G][2];
+      // rows n of the four left operands: the lane ends with 16 neighbouring columns
+      const uint16_t* b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = bs + (int64_t)min(nb + 16 * (m / 4) + 4 * i + m % 4, l.N - 1) * l.rank;
+      const int n = nb + 16 * c;
+      u32x4 old[G][2];
+      f32x4 acc[G][4];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (n < l.N && 16 * (g0 + g) + m < count)
-          old[g] = *reinterpret_cast<const u32x4*>(l.y + s_rows[16 * (g0 + g) + m] * l.y_stride + n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (n < l.N && 16 * (g0 + g) + m < count) {
+          const u32x4* from = reinterpret_cast<const u32x4*>(l.y + s_rows[16 * (g0 + g) + m] * l.y_stride + n);
+          old[g][0] = from[0];
+          old[g][1] = from[1];
+        }
       }
-      for (int s = 0; s < steps; ++s) {
-        const int q = 4 * s + c;
-        const int at = q < 3 * chunks ? 8 * (q % chunks) : 0;   // (past the end: times the zeros of s_terms)
-        bf16x8 v0 = *reinterpret_cast<const bf16x8*>(b0 + at), v1 = *reinterpret_cast<const bf16x8*>(b1 + at);
-        if (q >= 3 * chunks) v0 = v1 = bf16x8{};   // a NaN there would not vanish
+      const auto step = [&](int s, const bf16x8 v[4]) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
           if (g < here) {
             const bf16x8 h = __builtin_bit_cast(bf16x8, s_terms[(g * steps + s) * 64 + lane]);
-            acc[g][0] = mfma16x16x32(v0, h, acc[g][0]);
-            acc[g][1] = mfma16x16x32(v1, h, acc[g][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[g][i] = mfma16x16x32(v[i], h, acc[g][i]);
           }
+      };
+      if constexpr (STEPS > 0) {
+        bf16x8 v[LOADS][4];
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[j][i] = *reinterpret_cast<const bf16x8*>(b[i] + 8 * ((4 * j + c) % (STEPS >= 3 ? 4 * LOADS : STEPS)));
+        // lane groups behind the terms: zeros, as a NaN of B would not vanish
+        constexpr int kRest = STEPS == 1 ? 1 : STEPS == 2 ? 2 : 0;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          if (kRest > 0 && s == STEPS - 1 && c >= 4 - kRest) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[0][i] = bf16x8{};
+          }
+          step(s, v[s * LOADS / STEPS]);
+        }
+      } else {
+        for (int s = 0; s < steps; ++s) {
+          // the chunk that place_of put at (s, c), or none
+          int ch = chunks % 4 == 0 ? 4 * (s / 3) + c : 4 * s + c;
+          const bool none = chunks % 4 != 0 && ch >= 3 * chunks;
+          ch = none ? 0 : ch % chunks;
+          bf16x8 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = *reinterpret_cast<const bf16x8*>(b[i] + 8 * ch);
+            if (none) v[i] = bf16x8{};
+          }
+          step(s, v);
+        }
       }
       if (n < l.N) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
           if (16 * (g0 + g) + m < count) {
-            u32x4 o;
+            u32x4 o[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const f32x4 d = acc[g][j / 2];
-              const float lo = bf16_to_f32(old[g][j] & 0xFFFFu) + d[2 * (j & 1)];
-              const float hi = __uint_as_float(old[g][j] & 0xFFFF0000u) + d[2 * (j & 1) + 1];
-              o[j] = bf16_rne(lo) | ((uint32_t)bf16_rne(hi) << 16);
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t was = old[g][j / 4][j % 4];
+              const float lo = bf16_to_f32(was & 0xFFFFu) + acc[g][j / 2][2 * (j & 1)];
+              const float hi = __uint_as_float(was & 0xFFFF0000u) + acc[g][j / 2][2 * (j & 1) + 1];
+              o[j / 4][j % 4] = bf16_rne(lo) | ((uint32_t)bf16_rne(hi) << 16);
             }
-            *reinterpret_cast<u32x4*>(l.out + s_rows[16 * (g0 + g) + m] * l.out_stride + n) = o;
+            u32x4* to = reinterpret_cast<u32x4*>(l.out + s_rows[16 * (g0 + g) + m] * l.out_stride + n);
+            to[0] = o[0];
+            to[1] = o[1];
           }
       }
     }
+  }
+}
+
+template <int G>
+void launch_expand(const LoraArgs& l, const LoraWork& w, int blocks, dim3 grid, hipStream_t stream) {
+  const int steps = (3 * (l.rank / 8) + 3) / 4;
+  const int groups = (int)((min(l.rows, (int64_t)kTile) + 15) / 16);
+  const size_t lds = (size_t)min(groups, G) * steps * 64 * sizeof(u32x4);
+  switch (l.rank) {
+    case 8: lora_expand_kernel<G, 1, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
+    case 16: lora_expand_kernel<G, 2, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
+    case 32: lora_expand_kernel<G, 3, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
+    case 64: lora_expand_kernel<G, 6, 2><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
+    case 128: lora_expand_kernel<G, 12, 4><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
+    default: lora_expand_kernel<G, 0, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks);
   }
 }
 
@@ -336,7 +421,7 @@ int64_t most_tiles(int64_t rows, int64_t adapters) {
 
 // Parts of K: enough workgroups for the chip where there are few tiles.
 int splits_of(int64_t rows, int64_t K, int64_t adapters) {
-  const int64_t want = 512 / most_tiles(rows, adapters), steps = K / 32;
+  const int64_t want = 256 / most_tiles(rows, adapters), steps = K / 32;
   int64_t s = want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want;
   if (s > (steps + 3) / 4) s = (steps + 3) / 4;   // a step for each of the four waves
   return (int)s;
@@ -374,17 +459,15 @@ void launch_lora(const LoraArgs& l, void* ws, hipStream_t stream) {
   if (rt == 1) lora_shrink_kernel<1><<<shrink, kLoraThreads, 0, stream>>>(l, w);
   else if (rt == 2) lora_shrink_kernel<2><<<shrink, kLoraThreads, 0, stream>>>(l, w);
   else lora_shrink_kernel<4><<<shrink, kLoraThreads, 0, stream>>>(l, w);
-  const int64_t all = (l.N + 31) / 32;
-  int64_t pairs = tiles * all / 4096;
-  pairs = pairs < 1 ? 1 : pairs > 8 ? 8 : pairs;
-  const int steps = (3 * (l.rank / 8) + 3) / 4;
-  const int64_t groups = ((l.rows < kTile ? l.rows : kTile) + 15) / 16;
-  const dim3 expand(groups_of_rows, (unsigned)((all + kWaves * pairs - 1) / (kWaves * pairs)));
-  // at most 64 KB of terms: four groups up to rank 168, else two
-  const size_t group_bytes = (size_t)steps * 64 * 16;
-  const size_t most = steps <= 16 ? 4 : 2, lds = (size_t)(groups < (int64_t)most ? (size_t)groups : most) * group_bytes;
-  if (steps <= 16) lora_expand_kernel<4><<<expand, kLoraThreads, lds, stream>>>(l, w, (int)pairs);
-  else lora_expand_kernel<2><<<expand, kLoraThreads, lds, stream>>>(l, w, (int)pairs);
+  const int64_t all = (l.N + 63) / 64;
+  int64_t blocks = tiles * all / 4096;
+  blocks = blocks < 1 ? 1 : blocks > 4 ? 4 : blocks;
+  const dim3 expand(groups_of_rows, (unsigned)((all + kWaves * blocks - 1) / (kWaves * blocks)));
+  // Few rows are mostly alone with their adapter: one group at a time leaves the
+  // registers to more waves.  At most 64 KB of terms: four groups up to rank 168.
+  if (l.rows <= kDirectRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
+  else if (l.rank <= 168) launch_expand<4>(l, w, (int)blocks, expand, stream);
+  else launch_expand<2>(l, w, (int)blocks, expand, stream);
 }
 
 }  // namespace w4
