@@ -39,9 +39,10 @@ COMMON_FLAGS = [
 ]
 
 
-# the attention kernel rescales its accumulators with vector instructions:
-# kept in VGPRs, they need no copies from and to accumulation registers
-FILE_FLAGS = {"kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# the attention and adapter kernels take their accumulators apart with vector
+# instructions: kept in VGPRs, they need no copies from and to accumulation registers
+FILE_FLAGS = {"kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "lora.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 PROBE = os.path.join(HERE, "probe")
 PROBE_LIB = os.path.join(HERE, "libw4probe.so")

@@ -8,9 +8,9 @@
 // 16x16x32 matrix cores with the factors' rows as the left and the tokens as the
 // right operand, so that a lane ends with neighbouring r, or neighbouring n, of
 // one token.
-//   shrink  h = x A^T, fp32; the tile's groups of 16 tokens go to the four waves,
-//           and what waves are left over, and other workgroups, take parts of K,
-//           whose sums the second kernel joins.
+//   shrink  h = x A^T, fp32; a workgroup's waves take pieces of K, and other
+//           workgroups parts of it where there are few tiles; the second kernel
+//           joins their sums.
 //   expand  h enters as three bf16 terms that hold its 24 bits (their products
 //           with B are exact in the fp32 accumulators; one term would round h to
 //           8 bits).  The terms lie one after another along the product's inner
@@ -24,11 +24,10 @@ namespace w4 {
 namespace {
 
 constexpr int kLoraThreads = 256;
-constexpr int kWaves = kLoraThreads / 64;
+constexpr int kWaves = kLoraThreads / 64;   // of the second product
 constexpr int kTile = 64;           // rows of one adapter in a tile
 constexpr int kDirectRows = 64;     // up to as many rows need no sort
 constexpr int kMaxSplits = 16;
-constexpr int kBatch = 4;           // steps of K whose loads a wave issues together
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;  // bins of the sort (and one for rows without)
 
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t* 
 // The workgroup's tile: rows (of the call) in s_rows, adapter id and count; false
 // where there is none.  Rows behind the count repeat the first one.
 __device__ __forceinline__ bool find_tile(const LoraArgs& l, const LoraWork& w, int32_t* s_rows, int& id, int& count) {
-  const int lane = threadIdx.x & 63, j = blockIdx.x;
+  const int lane = threadIdx.x & 63, j = blockIdx.y;
   if (w.tiles) {
     if (j >= *w.n_tiles) return false;
     const TileInfo t = w.tiles[j];
@@ -157,73 +156,73 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& l, const LoraWork& w, 
 }
 
 // ---------------------------------------------------------------- x A^T
-// RT tiles of 16 r; blockIdx.y: part of K + splits * (piece of the rank).
-template <int RT>
-__global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(LoraArgs l, LoraWork w) {
+// RT tiles of 16 r; blockIdx.x: part of K + splits * (piece of the rank).  Each of
+// the waves takes a piece of the part of K, for G groups of 16 tokens at once, so
+// that A is loaded once for them; the pieces are summed in the order of the waves.
+// A row's sums do not depend on the rows beside it.
+template <int WAVES, int G, int RT>
+__global__ void __launch_bounds__(64 * WAVES) lora_shrink_kernel(LoraArgs l, LoraWork w) {
+  constexpr int kBatch = G == 1 ? 4 : 2;   // steps of K whose loads a wave issues together
   __shared__ int32_t s_rows[kTile];
-  __shared__ f32x4 s_sum[kWaves][RT][64];
+  __shared__ f32x4 s_sum[WAVES][RT][64];
   int id, count;
   if (!find_tile(l, w, s_rows, id, count) || id < 0) return;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, c = lane >> 4;
-  const int split = blockIdx.y % w.splits, r0 = (blockIdx.y / w.splits) * 16 * RT;
-  const int groups = (count + 15) / 16;
-  const int per = groups == 1 ? 4 : groups == 2 ? 2 : 1;   // waves of a group of 16 tokens
-  const int g = wv / per, part = wv % per;
-  // The part of K is summed as (p0 + p1) + (p2 + p3) of its quarters, whichever
-  // waves take them: a row's sums do not depend on the rows beside it.
+  const int split = blockIdx.x % w.splits, r0 = (blockIdx.x / w.splits) * 16 * RT;
   const int s0 = split * w.k_steps, s1 = min(l.K / 32, s0 + w.k_steps);
-  const int steps = max(0, s1 - s0), each = (steps + 3) / 4;
-  f32x4 sum[RT];
-  if (g < groups) {
-    const uint16_t* xs = l.x + s_rows[16 * g + m] * l.x_stride + 8 * c;
-    const uint16_t* as[RT];
+  const int steps = max(0, s1 - s0), each = (steps + WAVES - 1) / WAVES;
+  const int b = s0 + min(steps, wv * each), e = s0 + min(steps, (wv + 1) * each);
+  const uint16_t* as[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)   // rows of r past the rank: the last one again, not stored
-      as[i] = l.a + ((int64_t)id * l.rank + min(l.rank - 1, r0 + 16 * i + m)) * l.K + 8 * c;
-    f32x4 half[RT];
-    for (int q = part * (4 / per); q < (part + 1) * (4 / per); ++q) {
-      f32x4 acc[RT];
+  for (int i = 0; i < RT; ++i)   // rows of r past the rank: the last one again, not stored
+    as[i] = l.a + ((int64_t)id * l.rank + min(l.rank - 1, r0 + 16 * i + m)) * l.K + 8 * c;
+  for (int g0 = 0; 16 * g0 < count; g0 += G) {
+    f32x4 acc[G][RT];
+    const uint16_t* xs[G];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int b = s0 + min(steps, q * each), e = s0 + min(steps, (q + 1) * each);
-      for (int s = b; s < e; s += kBatch) {   // the loads of a batch together; past the end the last step again
-        bf16x8 xv[kBatch], av[kBatch][RT];
+    for (int g = 0; g < G; ++g) {
+      xs[g] = l.x + s_rows[min(16 * (g0 + g) + m, kTile - 1)] * l.x_stride + 8 * c;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int at = 32 * min(s + j, e - 1);
-          xv[j] = *reinterpret_cast<const bf16x8*>(xs + at);
+      for (int i = 0; i < RT; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int s = b; s < e; s += kBatch) {   // past the end the last step again, not added
+      bf16x8 xv[kBatch][G], av[kBatch][RT];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) av[j][i] = *reinterpret_cast<const bf16x8*>(as[i] + at);
+      for (int j = 0; j < kBatch; ++j) {
+        const int at = 32 * min(s + j, e - 1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) av[j][i] = *reinterpret_cast<const bf16x8*>(as[i] + at);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (16 * (g0 + g) < count) xv[j][g] = *reinterpret_cast<const bf16x8*>(xs[g] + at);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (s + j < e) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            if (16 * (g0 + g) < count) {
+#pragma unroll
+              for (int i = 0; i < RT; ++i) acc[g][i] = mfma16x16x32(av[j][i], xv[j][g], acc[g][i]);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (s + j < e) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc[i] = mfma16x16x32(av[j][i], xv[j], acc[i]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if (per == 4) sum[i] = acc[i];
-        else if ((q & 1) == 0) half[i] = acc[i];
-        else if (per == 2 || q == 1) sum[i] = half[i] + acc[i];
-        else sum[i] += half[i] + acc[i];
-      }
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) s_sum[wv][i][lane] = sum[i];
-  }
-  __syncthreads();
-  // 4 r of one token each, by the first wave of its group
-  if (g < groups && part == 0 && 16 * g + m < count) {
-    float* to = w.part + ((int64_t)split * l.rows + s_rows[16 * g + m]) * l.rank;
+    for (int g = 0; g < G; ++g) {
+      if (16 * (g0 + g) >= count) break;
+      if (g0 + g > 0) __syncthreads();   // the sums of the group before are read
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (per == 4) sum[i] = (sum[i] + s_sum[wv + 1][i][lane]) + (s_sum[wv + 2][i][lane] + s_sum[wv + 3][i][lane]);
-      else if (per == 2) sum[i] += s_sum[wv + 1][i][lane];
-      const int r = r0 + 16 * i + 4 * c;
-      if (r < l.rank) *reinterpret_cast<f32x4*>(to + r) = sum[i];
+      for (int i = 0; i < RT; ++i) s_sum[wv][i][lane] = acc[g][i];
+      __syncthreads();
+      // 4 r of one token each
+      if (wv < RT && 16 * (g0 + g) + m < count) {
+        f32x4 sum = s_sum[0][wv][lane];
+        for (int v = 1; v < WAVES; ++v) sum += s_sum[v][wv][lane];
+        const int r = r0 + 16 * wv + 4 * c;
+        if (r < l.rank)
+          *reinterpret_cast<f32x4*>(w.part + ((int64_t)split * l.rows + s_rows[16 * (g0 + g) + m]) * l.rank + r) = sum;
+      }
     }
   }
 }
@@ -249,7 +248,22 @@ __device__ __forceinline__ int2 place_of(int term, int ch, int chunks) {
   return {q / 4, q % 4};
 }
 
-// A wave takes `blocks` times 64 columns; blockIdx.y: which.  G groups of 16 tokens
+// Between the products' layout, where a lane holds columns 8c.. and 32 + 8c.. of its
+// own token, and memory's, where it holds columns 32 (m % 2) + 8c.. of the tokens m
+// and m ^ 1 (the even one first), so that each load and store is of 128 bytes a row:
+// the lanes of a pair give each other one piece.
+__device__ __forceinline__ void swap_halves(u32x4 v[2]) {
+  const bool odd = threadIdx.x & 1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t v0 = v[0][j], v1 = v[1][j];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(odd ? v0 : v1), 0xB1, 0xF, 0xF, false);
+    v[0][j] = odd ? got : v0;
+    v[1][j] = odd ? v1 : got;
+  }
+}
+
+// A wave takes `blocks` times 64 columns; blockIdx.x: which.  G groups of 16 tokens
 // at a time have their terms in LDS.  STEPS of the inner dimension and LOADS chunks
 // of B a lane: 1 and 1 (rank 8), 2 and 1 (16), 3 and 1 (32), 6 and 2 (64), 12 and 4
 // (128); STEPS 0: any rank, B's chunks loaded at every step.
@@ -263,26 +277,49 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
   const int m = lane & 15, c = lane >> 4;
   const int groups = (count + 15) / 16, chunks = l.rank / 8;
   const int steps = STEPS > 0 ? STEPS : (3 * chunks + 3) / 4;
-  const int n0 = (blockIdx.y * kWaves + wv) * blocks * 64;
+  const int n0 = (blockIdx.x * kWaves + wv) * blocks * 64;
   if (id < 0) {
     if (l.out == l.y) return;
-    for (int p = 0; p < blocks; ++p) {
-      const int n = n0 + 64 * p + 16 * c;
-      if (n >= l.N) break;
+    for (int n = n0 + 8 * c; n < min(l.N, n0 + 64 * blocks); n += 32)
       for (int g = 0; g < groups; ++g)
         if (16 * g + m < count) {
           const int64_t row = s_rows[16 * g + m];
-          const u32x4* from = reinterpret_cast<const u32x4*>(l.y + row * l.y_stride + n);
-          const u32x4 v0 = from[0], v1 = from[1];
-          u32x4* to = reinterpret_cast<u32x4*>(l.out + row * l.out_stride + n);
-          to[0] = v0;
-          to[1] = v1;
+          *reinterpret_cast<u32x4*>(l.out + row * l.out_stride + n) =
+              *reinterpret_cast<const u32x4*>(l.y + row * l.y_stride + n);
         }
-    }
     return;
   }
   const float scale = l.scaling ? l.scaling[id] : 1.0f;
   const uint16_t* bs = l.b + (int64_t)id * l.N * l.rank;
+  // One block's chunks of B, and y of a round's tokens: asked for before the terms
+  // of the first round are made, and, where registers allow (G == 1), while the
+  // block before is computed.
+  struct Block {
+    bf16x8 v[LOADS][4];
+    u32x4 old[G][2];
+  };
+  const auto load = [&](Block& k, int g0, int nb) {
+    // rows n of the four left operands: the lane ends with twice 8 neighbouring columns
+    if constexpr (STEPS > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* b = bs + (int64_t)min(nb + 32 * (i / 2) + 8 * (m / 4) + 4 * (i % 2) + m % 4, l.N - 1) * l.rank;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+          k.v[j][i] = *reinterpret_cast<const bf16x8*>(b + 8 * ((4 * j + c) % (STEPS >= 3 ? 4 * LOADS : STEPS)));
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int token = 16 * (g0 + g) + (m & ~1) + h, n = nb + 32 * (m & 1) + 8 * c;
+        if (token < count && n < l.N)
+          k.old[g][h] = *reinterpret_cast<const u32x4*>(l.y + s_rows[token] * l.y_stride + n);
+      }
+  };
+  Block now, next;
+  if (n0 < l.N) load(now, 0, n0);
   for (int g0 = 0; g0 < groups; g0 += G) {
     const int here = min(G, groups - g0);
     if (g0 > 0) __syncthreads();   // the terms of the groups before are read
@@ -319,83 +356,69 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
     for (int p = 0; p < blocks; ++p) {
       const int nb = n0 + 64 * p;
       if (nb >= l.N) break;
-      // rows n of the four left operands: the lane ends with 16 neighbouring columns
-      const uint16_t* b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = bs + (int64_t)min(nb + 16 * (m / 4) + 4 * i + m % 4, l.N - 1) * l.rank;
-      const int n = nb + 16 * c;
-      u32x4 old[G][2];
-      f32x4 acc[G][4];
+      const bool more = p + 1 < blocks && nb + 64 < l.N;
+      if (G == 1 && more) load(next, g0, nb + 64);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        if (g >= here) continue;
+        f32x4 acc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (n < l.N && 16 * (g0 + g) + m < count) {
-          const u32x4* from = reinterpret_cast<const u32x4*>(l.y + s_rows[16 * (g0 + g) + m] * l.y_stride + n);
-          old[g][0] = from[0];
-          old[g][1] = from[1];
-        }
-      }
-      const auto step = [&](int s, const bf16x8 v[4]) {
+        for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (STEPS > 0) {
+          // lane groups behind the terms: zeros, as a NaN of B would not vanish
+          constexpr int kRest = STEPS == 1 ? 1 : STEPS == 2 ? 2 : 0;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-          if (g < here) {
+          for (int s = 0; s < STEPS; ++s) {
+            const bf16x8 h = __builtin_bit_cast(bf16x8, s_terms[(g * STEPS + s) * 64 + lane]);
+            const bool none = kRest > 0 && s == STEPS - 1 && c >= 4 - kRest;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[i] = mfma16x16x32(none ? bf16x8{} : now.v[s * LOADS / STEPS][i], h, acc[i]);
+          }
+        } else {
+          for (int s = 0; s < steps; ++s) {
+            // the chunk that place_of put at (s, c), or none
+            int ch = chunks % 4 == 0 ? 4 * (s / 3) + c : 4 * s + c;
+            const bool none = chunks % 4 != 0 && ch >= 3 * chunks;
+            ch = none ? 0 : ch % chunks;
             const bf16x8 h = __builtin_bit_cast(bf16x8, s_terms[(g * steps + s) * 64 + lane]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[g][i] = mfma16x16x32(v[i], h, acc[g][i]);
-          }
-      };
-      if constexpr (STEPS > 0) {
-        bf16x8 v[LOADS][4];
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[j][i] = *reinterpret_cast<const bf16x8*>(b[i] + 8 * ((4 * j + c) % (STEPS >= 3 ? 4 * LOADS : STEPS)));
-        // lane groups behind the terms: zeros, as a NaN of B would not vanish
-        constexpr int kRest = STEPS == 1 ? 1 : STEPS == 2 ? 2 : 0;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          if (kRest > 0 && s == STEPS - 1 && c >= 4 - kRest) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[0][i] = bf16x8{};
-          }
-          step(s, v[s * LOADS / STEPS]);
-        }
-      } else {
-        for (int s = 0; s < steps; ++s) {
-          // the chunk that place_of put at (s, c), or none
-          int ch = chunks % 4 == 0 ? 4 * (s / 3) + c : 4 * s + c;
-          const bool none = chunks % 4 != 0 && ch >= 3 * chunks;
-          ch = none ? 0 : ch % chunks;
-          bf16x8 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = *reinterpret_cast<const bf16x8*>(b[i] + 8 * ch);
-            if (none) v[i] = bf16x8{};
-          }
-          step(s, v);
-        }
-      }
-      if (n < l.N) {
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          if (16 * (g0 + g) + m < count) {
-            u32x4 o[2];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t was = old[g][j / 4][j % 4];
-              const float lo = bf16_to_f32(was & 0xFFFFu) + acc[g][j / 2][2 * (j & 1)];
-              const float hi = __uint_as_float(was & 0xFFFF0000u) + acc[g][j / 2][2 * (j & 1) + 1];
-              o[j / 4][j % 4] = bf16_rne(lo) | ((uint32_t)bf16_rne(hi) << 16);
+            for (int i = 0; i < 4; ++i) {
+              const uint16_t* b = bs + (int64_t)min(nb + 32 * (i / 2) + 8 * (m / 4) + 4 * (i % 2) + m % 4, l.N - 1) * l.rank;
+              const bf16x8 v = *reinterpret_cast<const bf16x8*>(b + 8 * ch);
+              acc[i] = mfma16x16x32(none ? bf16x8{} : v, h, acc[i]);
             }
-            u32x4* to = reinterpret_cast<u32x4*>(l.out + s_rows[16 * (g0 + g) + m] * l.out_stride + n);
-            to[0] = o[0];
-            to[1] = o[1];
           }
+        }
+        u32x4 o[2];
+        swap_halves(now.old[g]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t was = now.old[g][j / 4][j % 4];
+          const float lo = bf16_to_f32(was & 0xFFFFu) + acc[j / 2][2 * (j & 1)];
+          const float hi = __uint_as_float(was & 0xFFFF0000u) + acc[j / 2][2 * (j & 1) + 1];
+          o[j / 4][j % 4] = bf16_rne(lo) | ((uint32_t)bf16_rne(hi) << 16);
+        }
+        swap_halves(o);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int token = 16 * (g0 + g) + (m & ~1) + h, n = nb + 32 * (m & 1) + 8 * c;
+          if (token < count && n < l.N)
+            *reinterpret_cast<u32x4*>(l.out + s_rows[token] * l.out_stride + n) = o[h];
+        }
       }
+      if (G > 1 && more) load(now, g0, nb + 64);
+      else if (more) now = next;
     }
+    if (g0 + G < groups && n0 < l.N) load(now, g0 + G, n0);
   }
+}
+
+template <int WAVES, int G>
+void launch_shrink(const LoraArgs& l, const LoraWork& w, int rt, dim3 grid, hipStream_t stream) {
+  if (rt == 1) lora_shrink_kernel<WAVES, G, 1><<<grid, 64 * WAVES, 0, stream>>>(l, w);
+  else if (rt == 2) lora_shrink_kernel<WAVES, G, 2><<<grid, 64 * WAVES, 0, stream>>>(l, w);
+  else lora_shrink_kernel<WAVES, G, 4><<<grid, 64 * WAVES, 0, stream>>>(l, w);
 }
 
 template <int G>
@@ -455,14 +478,13 @@ void launch_lora(const LoraArgs& l, void* ws, hipStream_t stream) {
   const int r_tiles = (l.rank + 15) / 16;
   const int rt = r_tiles <= 1 ? 1 : r_tiles <= 2 ? 2 : 4;
   const unsigned groups_of_rows = (unsigned)(l.rows > kDirectRows ? tiles : l.rows);
-  const dim3 shrink(groups_of_rows, (unsigned)(w.splits * ((r_tiles + rt - 1) / rt)));
-  if (rt == 1) lora_shrink_kernel<1><<<shrink, kLoraThreads, 0, stream>>>(l, w);
-  else if (rt == 2) lora_shrink_kernel<2><<<shrink, kLoraThreads, 0, stream>>>(l, w);
-  else lora_shrink_kernel<4><<<shrink, kLoraThreads, 0, stream>>>(l, w);
+  const dim3 shrink((unsigned)(w.splits * ((r_tiles + rt - 1) / rt)), groups_of_rows);
+  if (l.rows <= kDirectRows) launch_shrink<4, 1>(l, w, rt, shrink, stream);
+  else launch_shrink<8, 4>(l, w, rt, shrink, stream);
   const int64_t all = (l.N + 63) / 64;
   int64_t blocks = tiles * all / 4096;
   blocks = blocks < 1 ? 1 : blocks > 4 ? 4 : blocks;
-  const dim3 expand(groups_of_rows, (unsigned)((all + kWaves * blocks - 1) / (kWaves * blocks)));
+  const dim3 expand((unsigned)((all + kWaves * blocks - 1) / (kWaves * blocks)), groups_of_rows);
   // Few rows are mostly alone with their adapter: one group at a time leaves the
   // registers to more waves.  At most 64 KB of terms: four groups up to rank 168.
   if (l.rows <= kDirectRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
