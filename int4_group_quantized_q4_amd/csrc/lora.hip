@@ -26,7 +26,8 @@ namespace {
 constexpr int kLoraThreads = 256;
 constexpr int kWaves = kLoraThreads / 64;   // of the second product
 constexpr int kTile = 64;           // rows of one adapter in a tile
-constexpr int kDirectRows = 64;     // up to as many rows need no sort
+constexpr int kFewRows = 64;        // up to as many rows are taken a group at a time
+constexpr int kDirectRows = 256;    // up to as many rows need no sort: 64-row pieces of the ids, one a lane
 constexpr int kMaxSplits = 16;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;  // bins of the sort (and one for rows without)
@@ -141,15 +142,34 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& l, const LoraWork& w, 
     __syncthreads();
     return true;
   }
-  int mine = lane < l.rows ? l.ids[lane] : -2;
-  if (lane < l.rows && (mine < 0 || mine >= l.adapters)) mine = -1;
-  id = __builtin_amdgcn_readlane(mine, j);
-  const uint64_t same = __ballot(mine == id);
-  if (__builtin_ctzll(same) != j) return false;   // an earlier row's tile
-  count = __builtin_popcountll(same);
+  // The j-th row leads a tile if the number of rows of its adapter before it is a
+  // multiple of 64; the tile is it and the next ones.
+  int mine[kDirectRows / 64];
+#pragma unroll
+  for (int q = 0; q < kDirectRows / 64; ++q) {
+    const int t = 64 * q + lane;
+    mine[q] = t < l.rows ? l.ids[t] : -2;
+    if (t < l.rows && (mine[q] < 0 || mine[q] >= l.adapters)) mine[q] = -1;
+  }
+  id = l.ids[j];
+  if (id < 0 || id >= l.adapters) id = -1;
+  int before = 0, all = 0, at[kDirectRows / 64];
+#pragma unroll
+  for (int q = 0; q < kDirectRows / 64; ++q) {
+    const uint64_t same = __ballot(mine[q] == id);
+    at[q] = mine[q] == id ? all + __builtin_popcountll(same & ((1ull << lane) - 1)) : -1;
+    before += j >= 64 * q + 64 ? __builtin_popcountll(same)
+              : j > 64 * q     ? __builtin_popcountll(same & ((1ull << (j & 63)) - 1))
+                               : 0;
+    all += __builtin_popcountll(same);
+  }
+  if (before % kTile != 0) return false;
+  count = min(kTile, all - before);
   if (threadIdx.x < 64) {
     if (lane >= count) s_rows[lane] = j;
-    if (mine == id) s_rows[__builtin_popcountll(same & ((1ull << lane) - 1))] = lane;
+#pragma unroll
+    for (int q = 0; q < kDirectRows / 64; ++q)
+      if (at[q] >= before && at[q] < before + kTile) s_rows[at[q] - before] = 64 * q + lane;
   }
   __syncthreads();
   return true;
@@ -403,8 +423,13 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int token = 16 * (g0 + g) + (m & ~1) + h, n = nb + 32 * (m & 1) + 8 * c;
-          if (token < count && n < l.N)
-            *reinterpret_cast<u32x4*>(l.out + s_rows[token] * l.out_stride + n) = o[h];
+          if (token < count && n < l.N) {
+            u32x4* to = reinterpret_cast<u32x4*>(l.out + s_rows[token] * l.out_stride + n);
+            // past the caches where there are many rows (the second product of 4090 rows of 14336 columns: 49
+            // against 62 us); few are what the next call reads
+            if constexpr (G > 1) __builtin_nontemporal_store(o[h], to);
+            else *to = o[h];
+          }
         }
       }
       if (G > 1 && more) load(now, g0, nb + 64);
@@ -479,15 +504,15 @@ void launch_lora(const LoraArgs& l, void* ws, hipStream_t stream) {
   const int rt = r_tiles <= 1 ? 1 : r_tiles <= 2 ? 2 : 4;
   const unsigned groups_of_rows = (unsigned)(l.rows > kDirectRows ? tiles : l.rows);
   const dim3 shrink((unsigned)(w.splits * ((r_tiles + rt - 1) / rt)), groups_of_rows);
-  if (l.rows <= kDirectRows) launch_shrink<4, 1>(l, w, rt, shrink, stream);
+  if (l.rows <= kFewRows) launch_shrink<4, 1>(l, w, rt, shrink, stream);
   else launch_shrink<8, 4>(l, w, rt, shrink, stream);
   const int64_t all = (l.N + 63) / 64;
   int64_t blocks = tiles * all / 4096;
-  blocks = blocks < 1 ? 1 : blocks > 4 ? 4 : blocks;
+  blocks = blocks >= 2 ? 4 : blocks >= 1 ? 2 : 1;
   const dim3 expand((unsigned)((all + kWaves * blocks - 1) / (kWaves * blocks)), groups_of_rows);
   // Few rows are mostly alone with their adapter: one group at a time leaves the
   // registers to more waves.  At most 64 KB of terms: four groups up to rank 168.
-  if (l.rows <= kDirectRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
+  if (l.rows <= kFewRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
   else if (l.rank <= 168) launch_expand<4>(l, w, (int)blocks, expand, stream);
   else launch_expand<2>(l, w, (int)blocks, expand, stream);
 }
