@@ -1,27 +1,36 @@
 // One token a row, drawn from its logits with a given uniform number.
 //
 // The kept tokens are a first piece of the order (logit descending, id ascending),
-// so no sort of a row is needed.  Two kernels read the logits once:
+// so no sort of a row is needed.  Two kernels, that read the logits once:
 //   scan  a workgroup for 16384 logits: their largest one, the sum of their
 //         weights beside it (where the row needs the whole sum), and the
 //         candidates: all logits from a bound up that at least `rank` of them reach,
-//         the rank-th largest of the maxima of 256 groups;
+//         the rank-th largest of the maxima of 256 groups, cut to its leading bits;
 //   draw  a workgroup a row.  All of the row's logits from the largest of the chunks'
 //         bounds up are among the candidates: where that piece of the order decides
-//         the filters, it is sorted in LDS, cut, and the draw is made among what is
-//         left, in the order of the ids.  A row without filters needs no candidates:
-//         the chunk in which the sums pass the number is read again.
-// Rows for which that piece is too short (a nucleus of many thousand tokens) go
-// through the row again, in the draw kernel: a radix select over the logits' order
-// keys finds the last kept one by counts (top-k) and sums of weights (top-p).
+//         the filters, it is sorted, cut, and the draw is made among what is left,
+//         in the order of the ids.  A row without filters needs no candidates, only
+//         the 256 or 512 logits in which the sums pass the number.
+// Where that piece may be too short (a nucleus of thousands of tokens) the scan also
+// leaves a histogram of weights (and counts) over bins of a sixteenth of an octave,
+// and a third kernel (rest) takes the rows that the second left: the histogram tells
+// the bin of the last kept logit; the row is read again for the logits of that bin,
+// and they are sorted.  Where the bin holds too many (ties), a radix select over the
+// logits' order keys takes the histogram's place.
+//
+// The second kernel's time is that of fetching its code as much as of running it (a
+// workgroup passes through it once), so it is kept short: one loop for its two sorts.
+// With the third kernel's code called from it, it took 8 us more, for a stack that
+// no row used.
 //
 // Weights are 2^((z - m) log2 e / T) in 64 bits.  Where they are added by atomics
-// (the histogram of the top-p select) they are whole multiples of 2^-43, so that
-// the sums do not depend on the order; elsewhere sums have a fixed order.
+// (the histograms) they are whole multiples of 2^-43 of the largest one, so that the
+// sums do not depend on the order; elsewhere sums have a fixed order.
 
 #include "common.h"
 #include "serving.h"
 #include "w4a16.h"
+#include "wave.h"
 
 namespace w4 {
 
@@ -29,11 +38,20 @@ namespace {
 
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / 64;
-constexpr int kBins = 2048;
+constexpr int kPer = 16;                               // logits a thread
+constexpr int kChunk = kSampleThreads * kPer;
+constexpr int kMostChunks = ((1 << 20) + 7 + kChunk - 1) / kChunk;
+constexpr int kGroups = 256;                           // of 4 threads each
+constexpr int kListMost = 512;                         // candidates of a chunk
+constexpr int kSortMost = 2048;                        // logits that are sorted
+constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
+constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
+constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
 
-// 2^t for t <= 0 (2^-1100, that is 0, for a NaN): the series of 2^r to the 11th power,
-// |r| <= 1/2, whose rest is below 1e-14 of it.
+// 2^t for t <= 0; 0 below 2^-1074 and for a NaN.  The nearest whole number is what t
+// leaves in the low bits of a large sum; the series of 2^r to the 11th power, |r| <=
+// 1/2, leaves out less than 1e-14.
 struct Series {
   double c[12];
   constexpr Series() : c() {
@@ -44,20 +62,22 @@ struct Series {
     }
   }
 };
+constexpr double kLarge = 0x1.8p52;
 __device__ __forceinline__ double exp2_f64(double t) {
   constexpr Series kSeries;
-  t = __builtin_fmax(t, -1100.0);
-  const double n = __builtin_rint(t), r = t - n;
+  t = __builtin_fmax(t, -2000.0);
+  const double sum = t + kLarge, r = t - (sum - kLarge);
   double v = kSeries.c[11];
 #pragma unroll
   for (int k = 10; k >= 0; --k) v = __builtin_fma(v, r, kSeries.c[k]);
-  return __builtin_ldexp(v, (int)n);
+  return __builtin_ldexp(v, (int)(uint32_t)__builtin_bit_cast(uint64_t, sum));
 }
 
 // Order keys: as unsigned numbers they compare as the logits do; zeros of both
 // signs are one value; a NaN is the largest key.
 constexpr uint32_t kNanKey = 0xFFFFFFFFu;
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;   // (0 stands for no logit)
+constexpr uint32_t kLowestKey = 0x00800000u;   // of the type's lowest value
 constexpr uint32_t kPosInfKey = 0xFF800000u;
 
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -67,15 +87,24 @@ __device__ __forceinline__ uint32_t order_key(float z) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k); }
 
-// A row's weights: exp((z - m) / T), 1 / T as given.
+// A row's weights: 2^((z - m) log2 e / T).  (Beside an infinite m all but its equals
+// are infinitely far below it, and weigh 0.)
 struct Weight {
+  float m;
   double top, per;   // m; log2 e / T
-  bool infinite;     // m is +infinity: those weigh 1, all others 0
-  __device__ __forceinline__ double operator()(uint32_t key) const {
-    if (infinite) return key == kPosInfKey ? 1.0 : 0.0;
-    return exp2_f64(((double)key_value(key) - top) * per);
+  __device__ __forceinline__ double of(float z) const {
+    return exp2_f64(z == m ? 0.0 : ((double)z - top) * per);
+  }
+  __device__ __forceinline__ double operator()(uint32_t key) const { return of(key_value(key)); }
+  // sixteenths of an octave, whole ones
+  __device__ __forceinline__ double steps(double z) const {
+    return __builtin_fma(z, 16.0 * per, kLarge) - kLarge;
   }
 };
+// A weight in multiples of 2^-43 (the last bits of a number between 2^9 and 2^10).
+__device__ __forceinline__ unsigned long long fixed_of(double w) {
+  return __builtin_bit_cast(unsigned long long, w + 0x1p9) - __builtin_bit_cast(unsigned long long, 0x1p9);
+}
 
 // The settings of a row, those that are off replaced by what they do not change.
 struct Settings {
@@ -85,8 +114,13 @@ struct Settings {
   double u;
   __device__ __forceinline__ bool greedy() const { return temperature == 0.f; }
   __device__ __forceinline__ bool filters(int n) const { return k < n || p < 1.0 || few > 0.0; }
+  // rows that need the sum of all weights, candidates, a histogram
+  __device__ __forceinline__ bool sums(int n) const { return !greedy() && k >= n && (p < 1.0 || few == 0.0); }
+  __device__ __forceinline__ bool lists(int n) const { return !greedy() && filters(n); }
+  __device__ __forceinline__ bool bins(int n) const { return lists(n) && n > kSmallVocab && k > kGroups; }
   __device__ __forceinline__ Weight weight(uint32_t top) const {
-    return {(double)key_value(top), 0x1.71547652b82fep+0 / (double)temperature, top == kPosInfKey};
+    const float m = key_value(top);
+    return {m, (double)m, 0x1.71547652b82fep+0 / (double)temperature};
   }
 };
 
@@ -105,30 +139,551 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t r) 
   return s;
 }
 
-__device__ __forceinline__ double shfl_f64(double v, int lane) {
-  return __builtin_bit_cast(double, __shfl(__builtin_bit_cast(long long, v), lane, 64));
-}
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __builtin_bit_cast(double, __shfl_xor(__builtin_bit_cast(long long, v), o, 64));
-  return v;
-}
-
 template <typename T>
 struct Row {
   const T* z;
   int n;
-  __device__ __forceinline__ uint32_t key(int i) const {
-    if constexpr (sizeof(T) == 2) return order_key(bf16_to_f32(z[i]));
-    else return order_key(z[i]);
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 2) return bf16_to_f32(z[i]);
+    else return z[i];
+  }
+  __device__ __forceinline__ uint32_t key(int i) const { return order_key(value(i)); }
+  // Places of the row's first chunk in front of the row: chunks are cut at multiples of 16 bytes.
+  __device__ __forceinline__ int in_front() const { return (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T)); }
+};
+
+// The thread's logits of a chunk (-infinity where there is none), and their ids.
+template <typename T>
+struct Piece {
+  static constexpr int kVec = 16 / sizeof(T);
+  float z[kPer];
+  int first;   // id of the chunk's first place
+  __device__ __forceinline__ int id(int i) const {
+    return first + (i / kVec * kSampleThreads + (int)threadIdx.x) * kVec + i % kVec;
+  }
+  __device__ __forceinline__ Piece(const Row<T>& row, int chunk) {
+    first = chunk * kChunk - row.in_front();
+    if (first >= 0 && first + kChunk <= row.n) {
+      u32x4 v[kPer / kVec];
+#pragma unroll
+      for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const u32x4*>(row.z + id(j * kVec));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
+        z[i] = __uint_as_float(sizeof(T) == 4 ? word : i % 2 ? word & 0xFFFF0000u : word << 16);
+      }
+    } else {   // the row's first or last chunk: value by value
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = id(i);
+        z[i] = at >= 0 && at < row.n ? row.value(at) : -INFINITY;
+      }
+    }
   }
 };
 
-struct Shared {
+// f of every chunk: the next one's loads are issued first.
+template <typename T, typename F>
+__device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, const F& f) {
+  Piece<T> now(row, 0);
+  for (int c = 0; c < chunks; ++c) {
+    const Piece<T> next(row, min(c + 1, chunks - 1));
+    f(now);
+    now = next;
+  }
+}
+
+struct ChunkInfo {
+  double sum;        // of the weights beside top
+  double ref;        // top in sixteenths of an octave, whole ones: the first bin; NaN: no histogram
+  uint32_t top;      // largest key; 0: no logit above -infinity
+  int32_t arg;       // the lowest id that has it
+  uint32_t bound;    // every logit from this key up is in the list
+  int32_t n;         // candidates; more than the list holds: it is not whole
+};
+
+int chunks_of(int64_t vocab) { return (int)((vocab + 7 + kChunk - 1) / kChunk); }   // a row starts inside 16 bytes
+__host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSmallVocab ? kSmallVocab : kListMost; }
+
+// A chunk's weights are summed in segments, a vector of each thread of a wave, which
+// follow one another in the order of the ids.
+template <typename T>
+constexpr int kSegments = kSampleWaves * kPer * (int)sizeof(T) / 16;
+constexpr int kMostSegments = kSampleWaves * kPer / 4;
+
+struct SampleWork {
+  ChunkInfo* info;             // [rows][chunks]
+  double* segment;             // [rows][chunks][kMostSegments], beside the chunk's top
+  int32_t* todo;               // [rows]: left to the third kernel
+  uint64_t* list;              // [rows][chunks][list_most]: key << 32 | ~id
+  unsigned long long* mass;    // [rows][chunks][kFine]
+  uint16_t* count;             // [rows][chunks][kFine]
+  int chunks;
+};
+
+// ---------------------------------------------------------------------- scan
+template <typename T>
+__global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleArgs a, SampleWork w) {
+  __shared__ uint32_t s_top[kSampleWaves];
+  __shared__ int s_arg, s_n;
+  __shared__ double s_sum[kMostSegments];
+  __shared__ uint32_t s_group[kGroups];
+  __shared__ uint32_t s_bound;
+  __shared__ unsigned long long s_mass[kFine];
+  __shared__ uint32_t s_count[kFine];
+  const int64_t r = blockIdx.y, at = r * w.chunks + blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
+  const Piece<T> piece(row, blockIdx.x);
+  const Settings set = settings_of(a, r);
+  float m = piece.z[0];
+  bool nan = m != m;
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) {
+    nan |= piece.z[i] != piece.z[i];
+    m = fmaxf(m, piece.z[i]);
+  }
+  const uint32_t own = nan ? kNanKey : order_key(m), mine = own == kNegInfKey ? 0u : own;
+  uint32_t top = quad_max(mine);
+  if ((lane & 3) == 0) s_group[tid / 4] = top;
+  top = wave_max_of_quads(top);
+  if (lane == 0) s_top[wv] = top;
+  if (tid == 0) {
+    s_arg = INT32_MAX;
+    s_n = 0;
+    s_bound = kLowestKey;
+  }
+  s_mass[tid] = 0;
+  s_count[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kSampleWaves; ++v) top = max(top, s_top[v]);
+  if (mine == top) {
+    const float z = key_value(top);
+    int arg = INT32_MAX;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i)
+      if (piece.z[i] == z) arg = piece.id(i);
+    atomicMin(&s_arg, arg);
+  }
+  const bool sums = set.sums(a.vocab), lists = set.lists(a.vocab);
+  // the bound: the leading 18 bits of the rank-th largest of the groups' maxima, which
+  // one wave finds bit by bit
+  if (lists && a.vocab > kSmallVocab && wv == 0) {
+    uint32_t g[kGroups / 64];
+    int some = 0;   // groups with a logit
+#pragma unroll
+    for (int i = 0; i < kGroups / 64; ++i) {
+      g[i] = s_group[64 * i + lane];
+      some += __builtin_popcountll(__ballot(g[i] > 0));
+    }
+    const int rank = max(1, min(some, set.k < a.vocab ? min(max(set.k, 16), kGroups) : 128));
+    uint32_t bound = 0;
+    for (uint32_t bit = 1u << 31; bit >= 1u << 14; bit >>= 1) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kGroups / 64; ++i) n += __builtin_popcountll(__ballot(g[i] >= (bound | bit)));
+      if (n >= rank) bound |= bit;
+    }
+    if (lane == 0) s_bound = max(bound, kLowestKey);
+  }
+  const Weight weight = set.weight(top);
+  const double ref = weight.steps(weight.top);
+  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 && __builtin_fabs(ref) < 0x1p30;
+  constexpr int kVec = Piece<T>::kVec;
+  double part[kPer / kVec] = {};
+  if (top >= kPosInfKey) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) part[i / kVec] += piece.z[i] == INFINITY ? 1.0 : 0.0;
+  } else if (bins) {
+    const bool counts = set.k < a.vocab;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const double e = exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
+      part[i / kVec] += e;
+      const double d = ref - weight.steps((double)piece.z[i]);
+      const int b = d < kFine - 1 ? (int)d : kFine - 1;
+      const unsigned long long fixed = fixed_of(e);
+      if (fixed > 0) atomicAdd(&s_mass[b], fixed);
+      if (counts && piece.z[i] > -INFINITY) atomicAdd(&s_count[b], 1u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else if (sums && top > 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      part[i / kVec] += exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
+      // two at a time: with more of them under way registers run out for a CU's second workgroup
+      if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer / kVec; ++j) {
+    const double sum = wave_sum(part[j]);
+    if (lane == 0) s_sum[j * kSampleWaves + wv] = sum;
+  }
+  __syncthreads();
+  const uint32_t bound = s_bound;
+  if (lists && mine >= bound) {
+    uint64_t* list = w.list + at * list_most(a.vocab);
+    const float z = key_value(bound);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (piece.z[i] >= z) {
+        const int n = atomicAdd(&s_n, 1);
+        if (n < list_most(a.vocab)) list[n] = ((uint64_t)order_key(piece.z[i]) << 32) | (uint32_t)~piece.id(i);
+      }
+  }
+  if (bins) {
+    w.mass[at * kFine + tid] = s_mass[tid];
+    if (set.k < a.vocab) w.count[at * kFine + tid] = (uint16_t)s_count[tid];
+  }
+  __syncthreads();
+  if (wv == 0) {
+    const double seg = lane < kSegments<T> ? s_sum[lane] : 0.0, sum = wave_sum(seg);
+    if (sums) w.segment[at * kMostSegments + lane] = seg;
+    if (lane == 0) w.info[at] = {sum, bins ? ref : __builtin_nan(""), top, s_arg, bound, s_n};
+  }
+}
+
+// ---------------------------------------------------------------------- draw
+struct PickShared {
+  double seg[kSampleWaves * kPer / 4];
+  int found;
+};
+
+// The first of 64 values (one a lane) at which their running sum exceeds target, the
+// last positive one if none does; before: the sum of those in front of it.
+__device__ __forceinline__ int pick_lane(double v, double target, double& before) {
+  const double c = wave_scan(v);
+  const uint64_t past = __ballot(v > 0.0 && c > target), some = __ballot(v > 0.0);
+  const int pick = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0;
+  before = pick > 0 ? lane_value(c, pick - 1) : 0.0;
+  return pick;
+}
+
+// The same over up to 65 chunks, the last one's value (`behind`) apart; total: the
+// sum of all.
+__device__ __forceinline__ int pick_chunk(double v, double behind, double u, double& before, double& total) {
+  const double front = lane_value(wave_scan(v), 63);
+  total = front + behind;
+  const double target = u * total;
+  if (behind > 0.0 && !(front > target)) {
+    before = front;
+    return 64;
+  }
+  return pick_lane(v, target, before);
+}
+
+// The id of a chunk at which the running sum of f(logit, id) exceeds target, in the
+// order of the ids (vector by vector, thread by thread).
+template <typename T, typename F>
+__device__ __forceinline__ int pick_in_chunk(PickShared& s, const Piece<T>& p, const F& f, double target) {
+  constexpr int kVec = Piece<T>::kVec, kVectors = kPer / kVec;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  double part[kVectors];
+  __syncthreads();   // s is free
+#pragma unroll
+  for (int j = 0; j < kVectors; ++j) {
+    part[j] = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) part[j] += f(p.z[j * kVec + i], p.id(j * kVec + i));
+    const double sum = wave_sum(part[j]);
+    if (lane == 0) s.seg[j * kSampleWaves + wv] = sum;
+  }
+  __syncthreads();
+  double before, in_wave;
+  const int seg = pick_lane(lane < kVectors * kSampleWaves ? s.seg[lane] : 0.0, target, before);
+  if (wv == seg % kSampleWaves) {
+    double mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j)
+      if (j == seg / kSampleWaves) mine = part[j];
+    target -= before;
+    const int l = pick_lane(mine, target, in_wave);
+    if (lane == l) {
+      target -= in_wave;
+      double run = 0.0;
+      int found = -1, last = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i / kVec == seg / kSampleWaves) {
+          const double v = f(p.z[i], p.id(i));
+          run += v;
+          if (v > 0.0) last = p.id(i);
+          if (v > 0.0 && found < 0 && run > target) found = p.id(i);
+        }
+      s.found = found >= 0 ? found : last;
+    }
+  }
+  __syncthreads();
+  return s.found;
+}
+
+// v0 (places 0 .. 1023) and v1 (1024 .. 2047) of all threads in descending order; N, a
+// power of two, is the number of places in use.  Bitonic: exchanges within a wave by
+// moves between lanes, others through LDS.
+__device__ __forceinline__ uint64_t exchange(uint64_t v, uint64_t other, int place, int size, int step) {
+  const bool larger = ((place & step) == 0) == ((place & size) == 0);
+  return (v > other) == larger ? v : other;
+}
+// Of lane ^ 16 (rows swapped) or lane ^ 32 (halves).
+__device__ __forceinline__ uint32_t across_u32(uint32_t v, int step) {
+  if (step == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? p[0] : p[1];
+  }
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return (threadIdx.x & 32) ? p[0] : p[1];
+}
+__device__ __forceinline__ uint64_t across_u64(uint64_t v, int step) {
+  return ((uint64_t)across_u32((uint32_t)(v >> 32), step) << 32) | across_u32((uint32_t)v, step);
+}
+__device__ __forceinline__ void wave_stages(uint64_t& v, int place, int size) {
+#pragma unroll
+  for (int step = 32; step > 0; step /= 2)
+    if (size > step) {
+      const uint64_t other = step == 1   ? dpp_u64<0xB1>(v)                   // quad_perm [1,0,3,2]
+                             : step == 2 ? dpp_u64<0x4E>(v)                   // quad_perm [2,3,0,1]
+                             : step == 4 ? dpp_u64<0x1B>(dpp_u64<0x141>(v))   // half rows and quads mirrored
+                             : step == 8 ? dpp_u64<0x128>(v)                  // row_ror 8
+                                         : across_u64(v, step);
+      v = exchange(v, other, place, size, step);
+    }
+}
+__device__ __forceinline__ void sort_descending(uint64_t* s_v, uint64_t& v0, uint64_t& v1, int N) {
+  const int tid = threadIdx.x;
+  for (int size = 2; size <= N; size *= 2) {
+    if (size > kSampleThreads) {   // step 1024: the thread's own two
+      const uint64_t a = v0, b = v1;
+      v0 = a > b ? a : b;
+      v1 = a > b ? b : a;
+    }
+    for (int step = min(size, kSampleThreads) / 2; step >= 64; step /= 2) {
+      __syncthreads();
+      s_v[tid] = v0;
+      if (N > kSampleThreads) s_v[tid + kSampleThreads] = v1;
+      __syncthreads();
+      v0 = exchange(v0, s_v[tid ^ step], tid, size, step);
+      if (N > kSampleThreads)
+        v1 = exchange(v1, s_v[(tid ^ step) + kSampleThreads], tid + kSampleThreads, size, step);
+    }
+    if (tid < N) wave_stages(v0, tid, size);
+    if (N > kSampleThreads) wave_stages(v1, tid + kSampleThreads, size);
+  }
+}
+
+// Inclusive running sums over the places: all v0, then all v1 (where the N places in
+// use reach them).
+__device__ __forceinline__ void running_sums(double& v0, double& v1, int N, double* s_wave, double& total) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  total = 0.0;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (half == 1 && N <= kSampleThreads) break;
+    const double c = wave_scan(half == 0 ? v0 : v1);
+    __syncthreads();
+    if (lane == 63) s_wave[wv] = c;
+    __syncthreads();
+    double before = total;
+    for (int v = 0; v < kSampleWaves; ++v) {
+      if (v < wv) before += s_wave[v];
+      total += s_wave[v];
+    }
+    (half == 0 ? v0 : v1) = c + before;
+  }
+}
+
+__device__ __forceinline__ int power_of_two(int n) { return n <= 64 ? 64 : 1 << (32 - __builtin_clz(n - 1)); }
+
+// ------------------------------------------------------- a row by its histograms
+struct WholeShared {
+  uint64_t v[kSortMost];
+  double scale[kMostChunks], sums[kMostChunks];
+  int shift[kMostChunks];
+  double scan[kSampleWaves];
+  PickShared pick;
+  int bin, n, ok;
+  unsigned long long last;
+  double above;
+};
+
+// The first bin at which the running sum of the threads' values (a bin each) reaches
+// need (kFine: none does), and the sum before it.
+__device__ __forceinline__ int reach_bin(WholeShared& s, double v, double need, double& above) {
+  double c = v, none = 0.0, total;
+  running_sums(c, none, kSampleThreads, s.scan, total);
+  if (threadIdx.x == 0) s.bin = kFine;
+  __syncthreads();
+  if (v > 0.0 && c >= need) atomicMin(&s.bin, (int)threadIdx.x);
+  __syncthreads();
+  const int bin = s.bin;
+  if ((int)threadIdx.x == bin) s.above = c - v;
+  __syncthreads();
+  above = s.above;
+  return bin;
+}
+
+// False: the histograms do not say, or a bin holds too many.
+template <typename T>
+__device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, const SampleWork& w, const Row<T>& row,
+                                       int64_t r, const Settings& set, const Weight& weight, double all) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const double ref = weight.steps(weight.top);
+  const ChunkInfo* info = w.info + r * w.chunks;
+  const unsigned long long* mass = w.mass + r * w.chunks * kFine;
+  const uint16_t* count = w.count + r * w.chunks * kFine;
+  __syncthreads();
+  if (tid == 0) s.ok = 1;
+  __syncthreads();
+  if (tid < w.chunks) {
+    const ChunkInfo f = info[tid];
+    const double shift = ref - f.ref;
+    s.scale[tid] = f.top == 0 ? 0.0 : weight(f.top) * (1.0 / kFixed);
+    s.shift[tid] = f.top == 0 || !(shift < kFine) ? kFine : (int)shift;
+    if (f.top > 0 && f.ref != f.ref) s.ok = 0;
+  }
+  __syncthreads();
+  if (!s.ok) return false;
+  const auto bin_of = [&](double z) {
+    const double d = ref - weight.steps(z);
+    return d < kFine - 1 ? (int)d : kFine - 1;
+  };
+  // the row's histograms, a bin a thread (the last bin is not used)
+  const bool use_k = set.k < a.vocab, use_p = set.p < 1.0;
+  double row_mass = 0.0, row_count = 0.0;
+  if (tid < kFine - 1)
+    for (int c = 0; c < w.chunks; ++c) {
+      const int b = tid - s.shift[c];
+      if (b < 0) continue;
+      row_mass += (double)mass[c * kFine + b] * s.scale[c];
+      if (use_k) row_count += (double)count[c * kFine + b];
+    }
+  uint64_t v0 = 0, v1 = 0;
+  int listed = -1, N = 64;
+  // the logits of a bin, sorted
+  const auto list = [&](int bin) {
+    if (bin == listed) return true;
+    listed = bin;
+    __syncthreads();
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    for_chunks(row, w.chunks, [&](const Piece<T>& p) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (bin_of((double)p.z[i]) == bin) {
+          const int at = atomicAdd(&s.n, 1);
+          if (at < kSortMost) s.v[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
+        }
+    });
+    __syncthreads();
+    const int n = s.n;
+    if (n > kSortMost) return false;
+    N = power_of_two(n);
+    v0 = tid < n ? s.v[tid] : 0;
+    v1 = tid + kSampleThreads < n ? s.v[tid + kSampleThreads] : 0;
+    sort_descending(s.v, v0, v1, N);
+    return true;
+  };
+  // the listed weights, those behind `last` left out, and their running sums
+  unsigned long long last = 0;   // the last one kept, as key << 32 | ~id; smaller ones are not
+  double w0, w1, c0, c1, listed_sum;
+  const auto listed_sums = [&]() {
+    c0 = w0 = v0 > 0 && v0 >= last ? weight((uint32_t)(v0 >> 32)) : 0.0;
+    c1 = w1 = v1 > 0 && v1 >= last ? weight((uint32_t)(v1 >> 32)) : 0.0;
+    running_sums(c0, c1, N, s.scan, listed_sum);
+  };
+  int bin = kFine - 1;   // the last one's
+  double above, sum = all;
+  if (use_k) {
+    bin = reach_bin(s, row_count, (double)set.k, above);
+    if (bin >= kFine - 1 || !list(bin)) return false;
+    const int at = set.k - (int)above - 1;
+    if (at == tid) s.last = v0;
+    if (at == tid + kSampleThreads) s.last = v1;
+    __syncthreads();
+    last = s.last;
+    if (use_p) {
+      listed_sums();
+      double before = tid < bin ? row_mass : 0.0, none = 0.0;
+      running_sums(before, none, kSampleThreads, s.scan, sum);
+      sum += listed_sum;
+    }
+  }
+  if (use_p) {
+    const double need = set.p * sum;
+    const int reached = reach_bin(s, row_mass, need, above);
+    if (reached >= kFine - 1 || reached > bin || !list(reached)) return false;
+    bin = reached;
+    listed_sums();
+    // the first place that reaches it, else the last one
+    const unsigned long long before = last;
+    __syncthreads();
+    if (tid == 0) s.last = before;
+    __syncthreads();
+    if (w0 > 0.0 && above + c0 >= need) atomicMax(&s.last, (unsigned long long)v0);
+    if (w1 > 0.0 && above + c1 >= need) atomicMax(&s.last, (unsigned long long)v1);
+    __syncthreads();
+    last = s.last;
+  }
+  if (set.few > 0.0) {
+    // the weight's place among the logits
+    const int at = bin_of(weight.top + log2(set.few) / weight.per);
+    if (at <= bin) {
+      if (at >= kFine - 1 || !list(at)) return false;
+      bin = at;
+      w0 = v0 > 0 ? weight((uint32_t)(v0 >> 32)) : 0.0;
+      w1 = v1 > 0 ? weight((uint32_t)(v1 >> 32)) : 0.0;
+      __syncthreads();
+      if (tid == 0) s.last = ~0ull;
+      __syncthreads();
+      if (w0 >= set.few && v0 >= last) atomicMin(&s.last, (unsigned long long)v0);
+      if (w1 >= set.few && v1 >= last) atomicMin(&s.last, (unsigned long long)v1);
+      __syncthreads();
+      last = s.last;   // (none of the bin: all of it is behind)
+    }
+  }
+  if (bin >= kFine - 1) return false;
+  // the kept weights of each chunk: whole bins, and the listed ones
+  __syncthreads();
+  if (v0 > 0) s.v[tid] = v0;
+  if (v1 > 0) s.v[tid + kSampleThreads] = v1;
+  __syncthreads();
+  const int n = s.n;
+  for (int c = wv; c < w.chunks; c += kSampleWaves) {
+    unsigned long long whole = 0;
+    for (int b = lane; b < bin - s.shift[c]; b += 64) whole += mass[c * kFine + b];
+    double part = (double)wave_sum(whole) * s.scale[c], in_bin = 0.0;
+    for (int i = lane; i < n; i += 64) {
+      const uint64_t v = s.v[i];
+      if (v >= last && (int)((~(uint32_t)v + row.in_front()) / kChunk) == c) in_bin += weight((uint32_t)(v >> 32));
+    }
+    part += wave_sum(in_bin);
+    if (lane == 0) s.sums[c] = part;
+  }
+  __syncthreads();
+  double before, total;
+  const int c = pick_chunk(lane < min(w.chunks, 64) ? s.sums[lane] : 0.0, w.chunks > 64 ? s.sums[64] : 0.0, set.u, before,
+                           total);
+  // kept: whole bins above, and in the bin up to the last one
+  const auto share = [&](float z, int id) {
+    const int b = bin_of((double)z);
+    if (b > bin || (b == bin && (((uint64_t)order_key(z) << 32) | (uint32_t)~id) < last)) return 0.0;
+    return weight.of(z);
+  };
+  const Piece<T> p(row, c);
+  const int token = pick_in_chunk(s.pick, p, share, set.u * total - before);
+  if (tid == 0) {
+    a.tokens[r] = token;
+    if (a.logprobs) a.logprobs[r] = (float)log(weight.of(row.value(token)) / total);
+  }
+  return true;
+}
+
+// --------------------------------------------------- a row by a radix select
+struct RadixShared {
   unsigned long long bins[kBins];
   double seg[kSampleWaves];
   unsigned long long scan[kSampleWaves];
-  uint32_t u32[kSampleWaves];
   int pick;
   unsigned long long above;
   int found;
@@ -138,13 +693,13 @@ struct Shared {
 // piece in which the running sum first exceeds target, else the last one that is
 // not 0; `before`: the sum of the pieces before it.
 template <typename F>
-__device__ int pick_piece(Shared& s, const F& f, int lo, int hi, int piece, double target, double& before,
+__device__ int pick_piece(RadixShared& s, const F& f, int lo, int hi, int piece, double target, double& before,
                           double& total) {
   const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int b = min(hi, lo + wv * piece), e = min(hi, b + piece);
   double sum = 0;
   for (int i = b + lane; i < e; i += 64) sum += f(i);
-  sum = wave_sum_f64(sum);
+  sum = wave_sum(sum);
   __syncthreads();
   if (lane == 0) s.seg[wv] = sum;
   __syncthreads();
@@ -179,7 +734,7 @@ __device__ __forceinline__ int piece_of(int n) { return ((n + kSampleWaves - 1) 
 // whole sum (or `target`, where share is negative); the last one with f > 0 if
 // none does.
 template <typename F>
-__device__ int find_id(Shared& s, const F& f, int lo, int hi, double share, double target, double& total) {
+__device__ int find_id(RadixShared& s, const F& f, int lo, int hi, double share, double target, double& total) {
   int piece = piece_of(hi - lo);
   double before, ignored;
   if (share >= 0) {
@@ -203,16 +758,11 @@ __device__ int find_id(Shared& s, const F& f, int lo, int hi, double share, doub
     int found = -1, last = lo;
     for (int i0 = lo; i0 < hi && found < 0; i0 += 64) {
       const double v = i0 + lane < hi ? f(i0 + lane) : 0.0;
-      double c = v;
-#pragma unroll
-      for (int o = 1; o < 64; o *= 2) {
-        const double x = shfl_f64(c, (lane - o) & 63);
-        if (lane >= o) c += x;
-      }
+      const double c = wave_scan(v);
       const uint64_t past = __ballot(v > 0 && run + c > target), some = __ballot(v > 0);
       if (past) found = i0 + __builtin_ctzll(past);
       if (some) last = i0 + 63 - __builtin_clzll(some);
-      run += shfl_f64(c, 63);
+      run += lane_value(c, 63);
     }
     if (lane == 0) s.found = found >= 0 ? found : last;
   }
@@ -224,7 +774,7 @@ __device__ int find_id(Shared& s, const F& f, int lo, int hi, double share, doub
 // `need`; `above`: the sum over keys > t.  amount(key, i): 0 for ids that do not
 // take part.  Digits of 11, 11 and 10 bits.
 template <typename R, typename F>
-__device__ uint32_t radix_select(Shared& s, const R& row, const F& amount, unsigned long long need,
+__device__ uint32_t radix_select(RadixShared& s, const R& row, const F& amount, unsigned long long need,
                                  unsigned long long& above) {
   uint32_t prefix = 0;
   above = 0;
@@ -271,9 +821,9 @@ __device__ uint32_t radix_select(Shared& s, const R& row, const F& amount, unsig
   return prefix;
 }
 
-// A row by itself, whatever its filters.
+// For rows whose histograms do not say: many ties, infinities, extreme temperatures.
 template <typename T>
-__device__ void whole_row(Shared& s, const SampleArgs& a, const Row<T>& row, int64_t r, const Settings& set,
+__device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, const Row<T>& row, int64_t r, const Settings& set,
                           const Weight& weight) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   // kept: keys above t, and ids up to `upto` at t
@@ -289,12 +839,11 @@ __device__ void whole_row(Shared& s, const SampleArgs& a, const Row<T>& row, int
   }
   if (set.p < 1.0) {
     const auto amount = [&](uint32_t key, int i) {
-      return kept(key, i) ? (unsigned long long)(weight(key) * kFixed + 0.5) : 0ull;
+      return kept(key, i) ? fixed_of(weight(key)) : 0ull;
     };
     unsigned long long sum = 0;
     for (int i = tid; i < row.n; i += kSampleThreads) sum += amount(row.key(i), i);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    sum = wave_sum(sum);
     __syncthreads();
     if (lane == 0) s.scan[wv] = sum;
     __syncthreads();
@@ -305,7 +854,7 @@ __device__ void whole_row(Shared& s, const SampleArgs& a, const Row<T>& row, int
     const unsigned long long need = part > 1.0 ? (unsigned long long)__builtin_ceil(part) : 1ull;
     unsigned long long above;
     const uint32_t tp = radix_select(s, row, amount, need, above);
-    const unsigned long long each = (unsigned long long)(weight(tp) * kFixed + 0.5);
+    const unsigned long long each = fixed_of(weight(tp));
     if (each > 0) {
       const double ties = (double)((need - above + each - 1) / each);
       upto = find_id(s, [&](int i) { return row.key(i) == tp ? 1.0 : 0.0; }, 0, row.n, -1.0, ties - 1.0, ignored);
@@ -326,248 +875,27 @@ __device__ void whole_row(Shared& s, const SampleArgs& a, const Row<T>& row, int
   }
 }
 
-// ---------------------------------------------------------------------- scan
-constexpr int kPer = 16;                               // logits a thread
-constexpr int kChunk = kSampleThreads * kPer;
-constexpr int kGroups = 256;                           // of 4 threads each
-constexpr int kListMost = 512;                         // candidates of a chunk
-constexpr int kSortMost = 2048;                        // candidates of a row
-constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
-
-struct ChunkInfo {
-  double sum;        // of the weights beside top
-  uint32_t top;      // largest key; 0: no logit above -infinity
-  int32_t arg;       // the lowest id that has it
-  uint32_t bound;    // every logit from this key up is in the list; 1: every one
-  int32_t n;         // candidates; more than the list holds: it is not whole
-};
-
-int chunks_of(int64_t vocab) { return (int)((vocab + 7 + kChunk - 1) / kChunk); }   // a row starts inside 16 bytes
-__host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSmallVocab ? kSmallVocab : kListMost; }
-
-struct SampleWork {
-  ChunkInfo* info;   // [rows][chunks]
-  uint64_t* list;    // [rows][chunks][list_most]: key << 32 | ~id
-  int chunks;
-};
-
-// The thread's logits of a chunk as keys (0: none), and their ids.  Chunks are cut at
-// multiples of 16 bytes.
-template <typename T>
-struct Piece {
-  static constexpr int kVec = 16 / sizeof(T);
-  uint32_t key[kPer];
-  int first;   // id of the chunk's first place
-  __device__ __forceinline__ int id(int i) const {
-    return first + (i / kVec * kSampleThreads + (int)threadIdx.x) * kVec + i % kVec;
-  }
-  __device__ __forceinline__ Piece(const T* z, int n, int chunk) {
-    first = chunk * kChunk - (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
-    u32x4 v[kPer / kVec];
-#pragma unroll
-    for (int j = 0; j < kPer / kVec; ++j) {
-      const int at = id(j * kVec);
-      if (at >= 0 && at + kVec <= n) {
-        v[j] = *reinterpret_cast<const u32x4*>(z + at);
-      } else {   // the row's first and last pieces; -infinity counts as no logit
-        uint32_t e[kVec];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const bool in = at + i >= 0 && at + i < n;
-          if constexpr (sizeof(T) == 2) e[i] = in ? z[at + i] : 0xFF80u;
-          else e[i] = in ? __float_as_uint(z[at + i]) : 0xFF800000u;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = sizeof(T) == 2 ? e[(2 * i) % kVec] | (e[(2 * i + 1) % kVec] << 16) : e[i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
-      const uint32_t bits = sizeof(T) == 2 ? (i % 2 ? word & 0xFFFF0000u : word << 16) : word;
-      const uint32_t k = order_key(__uint_as_float(bits));
-      key[i] = k == kNegInfKey ? 0u : k;
-    }
-  }
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kSampleThreads) sample_scan_kernel(SampleArgs a, SampleWork w) {
-  __shared__ uint32_t s_top[kSampleWaves];
-  __shared__ int s_arg, s_n;
-  __shared__ double s_sum[kSampleWaves];
-  __shared__ __align__(16) uint32_t s_group[kGroups];
-  __shared__ uint32_t s_bound;
-  const int64_t r = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const Piece<T> z(static_cast<const T*>(a.logits) + r * a.stride, a.vocab, blockIdx.x);
-  const Settings set = settings_of(a, r);
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) top = max(top, z.key[i]);
-  const uint32_t mine = top;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-    if (o == 2 && (lane & 3) == 0) s_group[tid / 4] = top;
-  }
-  if (lane == 0) s_top[wv] = top;
-  if (tid == 0) {
-    s_arg = INT32_MAX;
-    s_n = 0;
-    s_bound = 1;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < kSampleWaves; ++v) top = max(top, s_top[v]);
-  if (mine == top) {
-    int arg = INT32_MAX;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (z.key[i] == top) arg = z.id(i);
-    atomicMin(&s_arg, arg);
-  }
-  const bool sums = !set.greedy() && set.k >= a.vocab && (set.p < 1.0 || set.few == 0.0) && top != kNanKey;
-  const bool lists = !set.greedy() && set.filters(a.vocab);
-  // the bound: the rank-th largest of the groups' maxima (a lower one is a candidate
-  // of the row only where `rank` of this chunk are above it)
-  if (lists && a.vocab > kSmallVocab && tid < kGroups) {
-    const int rank = set.k < a.vocab ? min(max(set.k, 16), kGroups) : 128;
-    const uint32_t g = s_group[tid];
-    int before = 0, some = 0;   // groups above this one; groups with a logit
-#pragma unroll 4
-    for (int j = 0; j < kGroups / 4; ++j) {
-      const u32x4 o = reinterpret_cast<const u32x4*>(s_group)[j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        before += o[i] > g || (o[i] == g && 4 * j + i < tid);
-        some += o[i] > 0;
-      }
-    }
-    if (before == min(rank, some) - 1) s_bound = g;
-  }
-  double sum = 0.0;
-  if (sums && top > 0) {
-    const Weight weight = set.weight(top);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += weight(z.key[i]);
-    sum = wave_sum_f64(sum);
-  }
-  if (lane == 0) s_sum[wv] = sum;
-  __syncthreads();
-  const uint32_t bound = a.vocab > kSmallVocab ? s_bound : 1u;
-  const int64_t at = r * w.chunks + blockIdx.x;
-  if (lists && mine >= bound) {
-    uint64_t* list = w.list + at * list_most(a.vocab);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (z.key[i] >= bound) {
-        const int n = atomicAdd(&s_n, 1);
-        if (n < list_most(a.vocab)) list[n] = ((uint64_t)z.key[i] << 32) | (uint32_t)~z.id(i);
-      }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    sum = 0.0;
-    for (int v = 0; v < kSampleWaves; ++v) sum += s_sum[v];
-    w.info[at] = {sum, top, s_arg, bound, s_n};
-  }
-}
-
-// ---------------------------------------------------------------------- draw
-// v sorted in descending order, N (a power of two, 64 to 2048) of them in s_v, by
-// the first N / 2 threads or fewer: bitonic, two values a thread; exchanges
-// within a wave's 128 values need no barrier.
-__device__ __forceinline__ void sort_descending(uint64_t* s_v, int N) {
-  const int i = threadIdx.x;
-  for (int size = 2; size <= N; size *= 2)
-    for (int step = size / 2; step > 0; step /= 2) {
-      if (step >= 64 || size == 2) __syncthreads();
-      else {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
-      if (i < N / 2) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const uint64_t x = s_v[lo], y = s_v[hi];
-        const bool down = (lo & size) == 0;
-        if ((x < y) == down) {
-          s_v[lo] = y;
-          s_v[hi] = x;
-        }
-      }
-      if (step >= 64 && step / 2 < 64) __syncthreads();
-    }
-  __syncthreads();
-}
-
-// Inclusive running sums of the pairs (v0, v1) that each thread holds.
-__device__ __forceinline__ void running_sums(double& v0, double& v1, double* s_wave, double& total) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  double c = v0 + v1;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const double x = shfl_f64(c, (lane - o) & 63);
-    if (lane >= o) c += x;
-  }
-  __syncthreads();
-  if (lane == 63) s_wave[wv] = c;
-  __syncthreads();
-  double before = 0.0;
-  total = 0.0;
-  for (int v = 0; v < kSampleWaves; ++v) {
-    if (v < wv) before += s_wave[v];
-    total += s_wave[v];
-  }
-  const double upto = shfl_f64(c, (lane - 1) & 63);
-  v0 += before + (lane > 0 ? upto : 0.0);
-  v1 += v0;
-}
-
-union DrawShared {
-  Shared whole;
-  struct {
-    uint64_t v[kSortMost];
-    double sum[kSampleWaves];
-    uint32_t top, bound;
-    int n, kept, cut, token;
-    bool ready;
-  } draw;
-};
-
+// ------------------------------------------------------------------ the draw
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs a, SampleWork w) {
-  __shared__ DrawShared s;
+  __shared__ uint64_t s_v[kSortMost];
+  __shared__ double s_sum[kSampleWaves];
+  __shared__ int s_n, s_kept, s_token, s_cut;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const ChunkInfo* info = w.info + r * w.chunks;
-  const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
   const Settings set = settings_of(a, r);
-  // the chunks' figures, up to 64 chunks a lane each
-  uint32_t top = 0, bound = 0;
-  int arg = INT32_MAX;
-  bool whole = true;
-  for (int c = lane; c < w.chunks; c += 64) {
-    const ChunkInfo f = info[c];
-    if (f.top > top) {
-      top = f.top;
-      arg = f.arg;
-    }
-    bound = max(bound, f.bound);
-    whole = whole && f.n <= list_most(a.vocab);
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const uint32_t t = (uint32_t)__shfl_xor((int)top, o, 64);
-    const int g = __shfl_xor(arg, o, 64);
-    if (t > top || (t == top && g < arg)) {
-      top = t;
-      arg = g;
-    }
-    bound = max(bound, (uint32_t)__shfl_xor((int)bound, o, 64));
-  }
-  whole = __ballot(!whole) == 0;
+  // the chunks' figures, one a lane (and the 65th)
+  ChunkInfo mine{}, behind{};
+  if (lane < w.chunks) mine = info[lane];
+  if (w.chunks > 64) behind = info[64];
+  const uint32_t top = max(wave_max_of_quads(quad_max(mine.top)), behind.top);
+  const uint32_t bound = max(wave_max_of_quads(quad_max(mine.bound)), behind.bound);
+  if (tid == 0) w.todo[r] = 0;
   if (top == kNanKey || top == 0 || set.greedy()) {
+    // the lowest id that has it: that of the first chunk
+    const uint64_t have = __ballot(mine.top == top);
+    const int arg = have ? __builtin_amdgcn_readlane(mine.arg, __builtin_ctzll(have | 1ull << 63)) : behind.arg;
     if (tid == 0) {
       const bool none = top == kNanKey || top == 0;
       a.tokens[r] = none ? -1 : arg;
@@ -576,155 +904,199 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
     return;
   }
   const Weight weight = set.weight(top);
-  const bool sums = set.k >= a.vocab && (set.p < 1.0 || set.few == 0.0);
-  double all = 0.0;   // of the whole row
-  const auto chunk_sum = [&](int c) {
-    const ChunkInfo f = info[c];
-    return f.top == 0 ? 0.0 : f.sum * weight(f.top);
-  };
-  if (sums)
-    for (int c = 0; c < w.chunks; ++c) all += chunk_sum(c);
+  double all = 0.0, before = 0.0;   // of the whole row's weights
+  int chunk = 0;
+  if (set.sums(a.vocab)) {
+    const double last = behind.top == 0 ? 0.0 : behind.sum * weight(behind.top);
+    chunk = pick_chunk(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), last, set.u, before, all);
+  }
   if (!set.filters(a.vocab)) {
-    const double target = set.u * all;
-    double run = 0.0, before = 0.0;
-    int pick = -1, last = 0;
-    double last_before = 0.0;
-    for (int c = 0; c < w.chunks && pick < 0; ++c) {
-      const double v = chunk_sum(c);
-      if (run + v > target) {
-        pick = c;
-        before = run;
-      }
-      if (v > 0.0) {
-        last = c;
-        last_before = run;
-      }
-      run += v;
+    if (tid >= 64) return;   // one wave reads on: the segment, and the logit
+    const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
+    const int64_t at = r * w.chunks + chunk;
+    const double scale = weight(info[chunk].top);
+    double target = set.u * all - before, in_front;
+    const int seg = pick_lane(w.segment[at * kMostSegments + lane] * scale, target, in_front);
+    target -= in_front;
+    constexpr int kVec = Piece<T>::kVec;
+    const int first = chunk * kChunk - row.in_front() +
+                      (seg / kSampleWaves * kSampleThreads + seg % kSampleWaves * 64 + lane) * kVec;
+    double own[kVec], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int id = first + i;
+      own[i] = id >= 0 && id < a.vocab ? weight.of(row.value(id)) : 0.0;
+      sum += own[i];
     }
-    if (pick < 0) {
-      pick = last;
-      before = last_before;
-    }
-    const int first = pick * kChunk - (int)((reinterpret_cast<uintptr_t>(row.z) & 15u) / sizeof(T));
-    double ignored;
-    const int token = find_id(s.whole, [&](int i) { return weight(row.key(i)); }, max(first, 0),
-                              min(a.vocab, first + kChunk), -1.0, target - before, ignored);
-    if (tid == 0) {
-      a.tokens[r] = token;
-      if (a.logprobs) a.logprobs[r] = (float)log(weight(row.key(token)) / all);
+    const int l = pick_lane(sum, target, in_front);
+    if (lane == l) {
+      target -= in_front;
+      double run = 0.0, share = 0.0;
+      int found = -1, last = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        run += own[i];
+        if (own[i] > 0.0 && found < 0) {   // up to the one that exceeds it, else the last one
+          last = first + i;
+          share = own[i];
+          if (run > target) found = last;
+        }
+      }
+      a.tokens[r] = last;
+      if (a.logprobs) a.logprobs[r] = (float)log(share / all);
     }
     return;
   }
 
   // candidates from the bound up
-  if (tid == 0) s.draw.n = 0;
+  const bool whole = __ballot(mine.n > list_most(a.vocab)) == 0 && behind.n <= list_most(a.vocab);
+  if (tid == 0) s_n = 0;
   __syncthreads();
   if (whole) {
     for (int c = tid / 64; c < w.chunks; c += kSampleWaves) {
-      const int n = info[c].n;
+      const int n = c < 64 ? __builtin_amdgcn_readlane(mine.n, c) : behind.n;
       const uint64_t* list = w.list + (r * w.chunks + c) * list_most(a.vocab);
       for (int i = lane; i < n; i += 64) {
         const uint64_t v = list[i];
         if ((uint32_t)(v >> 32) >= bound) {
-          const int at = atomicAdd(&s.draw.n, 1);
-          if (at < kSortMost) s.draw.v[at] = v;
+          const int at = atomicAdd(&s_n, 1);
+          if (at < kSortMost) s_v[at] = v;
         }
       }
     }
   }
   __syncthreads();
-  const int n = s.draw.n;
-  bool ready = whole && n <= kSortMost && (set.k >= a.vocab || n >= set.k || bound == 1);
-  int N = 64;
-  while (N < n) N *= 2;
+  const int n = s_n;
+  const bool complete = bound == kLowestKey;   // every logit is a candidate
+  bool ready = whole && n <= kSortMost && (set.k >= a.vocab || n >= set.k || complete);
   if (ready) {
-    for (int i = n + tid; i < N; i += kSampleThreads) s.draw.v[i] = 0;
-    sort_descending(s.draw.v, N);
-    // how many of the first ones stay
-    const int i0 = 2 * tid, most = min(n, set.k);
-    double w0 = i0 < most ? weight((uint32_t)(s.draw.v[i0] >> 32)) : 0.0;
-    double w1 = i0 + 1 < most ? weight((uint32_t)(s.draw.v[i0 + 1] >> 32)) : 0.0;
-    double c0 = w0, c1 = w1, total;
-    running_sums(c0, c1, s.draw.sum, total);
-    if (tid == 0) s.draw.kept = most;
-    __syncthreads();
-    if (set.p < 1.0) {
-      const double need = set.p * (set.k < a.vocab || bound == 1 ? total : all);
-      // the first place whose running sum reaches it
-      if (c0 >= need && i0 < most) atomicMin(&s.draw.kept, i0 + 1);
-      else if (c1 >= need && i0 + 1 < most) atomicMin(&s.draw.kept, i0 + 2);
-      ready = total >= need;
-    }
-    if (set.few > 0.0) {
-      if (i0 < most && w0 < set.few) atomicMin(&s.draw.kept, i0);
-      else if (i0 + 1 < most && w1 < set.few) atomicMin(&s.draw.kept, i0 + 1);
-    }
-    __syncthreads();
-    const int kept = s.draw.kept;
-    // nothing below the bound would stay either
-    ready = bound == 1 || kept < n || (set.k < a.vocab && kept == set.k) || (set.p < 1.0 && ready);
-    ready = ready && kept > 0;
-    if (ready) {
-      // the kept ones in the order of their ids
-      int M = 64;
-      while (M < kept) M *= 2;
-      const uint64_t x0 = i0 < kept ? s.draw.v[i0] : 0, x1 = i0 + 1 < kept ? s.draw.v[i0 + 1] : 0;
-      __syncthreads();
-      if (i0 < M) {   // ~id above the key: descending order is ascending in the id
-        s.draw.v[i0] = x0 << 32 | x0 >> 32;
-        s.draw.v[i0 + 1] = x1 << 32 | x1 >> 32;
+    // First in the order of the logits: how many of the first ones stay; then those in
+    // the order of their ids (~id above the key): the draw.
+    const int i0 = tid, i1 = tid + kSampleThreads;
+    uint64_t v0 = i0 < n ? s_v[i0] : 0, v1 = i1 < n ? s_v[i1] : 0;
+    int most = min(n, set.k), N = power_of_two(n);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      sort_descending(s_v, v0, v1, N);
+      const int key_at = pass == 0 ? 32 : 0;
+      const double w0 = i0 < most ? weight((uint32_t)(v0 >> key_at)) : 0.0;
+      const double w1 = i1 < most ? weight((uint32_t)(v1 >> key_at)) : 0.0;
+      double c0 = w0, c1 = w1, total;
+      running_sums(c0, c1, N, s_sum, total);
+      if (pass == 0) {
+        if (tid == 0) {
+          s_kept = most;
+          s_token = INT32_MAX;
+          s_cut = 0;
+        }
+        __syncthreads();
+        if (set.p < 1.0) {
+          const double need = set.p * (set.k < a.vocab || complete ? total : all);
+          // the first place whose running sum reaches it
+          if (i0 < most && c0 >= need) atomicMin(&s_kept, i0 + 1);
+          if (i1 < most && c1 >= need) atomicMin(&s_kept, i1 + 1);
+          ready = total >= need;
+        }
+        if (set.few > 0.0) {
+          if (i0 < most && w0 < set.few) atomicMin(&s_kept, i0);
+          if (i1 < most && w1 < set.few) atomicMin(&s_kept, i1);
+        }
+        __syncthreads();
+        const int kept = s_kept;
+        // nothing below the bound would stay either
+        ready = complete || kept < n || (set.k < a.vocab && kept == set.k) || (set.p < 1.0 && ready);
+        if (!ready) break;
+        most = kept;
+        N = power_of_two(kept);
+        v0 = i0 < kept ? v0 << 32 | v0 >> 32 : 0;
+        v1 = i1 < kept ? v1 << 32 | v1 >> 32 : 0;
+      } else {
+        const double target = set.u * total;
+        if (w0 > 0.0) {
+          if (c0 > target) atomicMin(&s_token, i0);
+          atomicMax(&s_cut, i0);
+        }
+        if (w1 > 0.0) {
+          if (c1 > target) atomicMin(&s_token, i1);
+          atomicMax(&s_cut, i1);
+        }
+        __syncthreads();
+        const int at = min(s_token, s_cut);
+        if (at == i0 || at == i1) {
+          a.tokens[r] = (int32_t)~(uint32_t)((at == i0 ? v0 : v1) >> 32);
+          if (a.logprobs) a.logprobs[r] = (float)log((at == i0 ? w0 : w1) / total);
+        }
+        return;
       }
-      if (tid == 0) {
-        s.draw.token = INT32_MAX;
-        s.draw.cut = -1;
-      }
-      sort_descending(s.draw.v, M);
-      w0 = i0 < kept ? weight((uint32_t)s.draw.v[i0]) : 0.0;
-      w1 = i0 + 1 < kept ? weight((uint32_t)s.draw.v[i0 + 1]) : 0.0;
-      c0 = w0;
-      c1 = w1;
-      running_sums(c0, c1, s.draw.sum, total);
-      const double target = set.u * total;
-      if (w0 > 0.0) {
-        if (c0 > target) atomicMin(&s.draw.token, i0);
-        atomicMax(&s.draw.cut, i0);
-      }
-      if (w1 > 0.0) {
-        if (c1 > target) atomicMin(&s.draw.token, i0 + 1);
-        atomicMax(&s.draw.cut, i0 + 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        const uint64_t v = s.draw.v[min(s.draw.token, s.draw.cut)];
-        a.tokens[r] = (int32_t)~(uint32_t)(v >> 32);
-        if (a.logprobs) a.logprobs[r] = (float)log(weight((uint32_t)v) / total);
-      }
-      return;
     }
   }
+  if (tid == 0) w.todo[r] = 1;
+}
+
+// ---------------------------------------------------------------------- rest
+union RestShared {
+  RadixShared radix;
+  WholeShared whole;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs a, SampleWork w) {
+  __shared__ RestShared s;
+  const int64_t r = blockIdx.x;
+  if (!w.todo[r]) return;
+  const int lane = threadIdx.x & 63;
+  const ChunkInfo* info = w.info + r * w.chunks;
+  const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
+  const Settings set = settings_of(a, r);
+  ChunkInfo mine{}, behind{};
+  if (lane < w.chunks) mine = info[lane];
+  if (w.chunks > 64) behind = info[64];
+  const uint32_t top = max(wave_max_of_quads(quad_max(mine.top)), behind.top);
+  const Weight weight = set.weight(top);
+  double all = 0.0, before;
+  if (set.sums(a.vocab)) {
+    const double last = behind.top == 0 ? 0.0 : behind.sum * weight(behind.top);
+    pick_chunk(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), last, set.u, before, all);
+  }
+  if (set.bins(a.vocab) && whole_row(s.whole, a, w, row, r, set, weight, all)) return;
   __syncthreads();
-  whole_row(s.whole, a, row, r, set, weight);
+  radix_row(s.radix, a, row, r, set, weight);
+}
+
+size_t workspace_parts(int64_t rows, int64_t vocab, SampleWork& w, char* base) {
+  w.chunks = chunks_of(vocab);
+  const size_t n = (size_t)rows * w.chunks;
+  w.list = reinterpret_cast<uint64_t*>(base);
+  w.info = reinterpret_cast<ChunkInfo*>(w.list + n * list_most(vocab));
+  w.segment = reinterpret_cast<double*>(w.info + n);
+  w.mass = reinterpret_cast<unsigned long long*>(w.segment + n * kMostSegments);
+  const size_t bins = vocab > kSmallVocab ? n * kFine : 0;
+  w.count = reinterpret_cast<uint16_t*>(w.mass + bins);
+  w.todo = reinterpret_cast<int32_t*>(w.count + bins);
+  return (size_t)(reinterpret_cast<char*>(w.todo + rows) - base);
 }
 
 }  // namespace
 
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab) {
-  return (size_t)rows * chunks_of(vocab) * (sizeof(ChunkInfo) + list_most(vocab) * sizeof(uint64_t));
+  SampleWork w{};
+  return workspace_parts(rows, vocab, w, nullptr);
 }
 
 void launch_sample(const SampleArgs& a, void* ws, hipStream_t stream) {
   SampleWork w{};
-  w.chunks = chunks_of(a.vocab);
-  w.list = static_cast<uint64_t*>(ws);
-  w.info = reinterpret_cast<ChunkInfo*>(w.list + a.rows * w.chunks * list_most(a.vocab));
-  const dim3 scan((unsigned)w.chunks, (unsigned)a.rows), draw((unsigned)a.rows);
-  if (a.dtype == W4_OUT_F32) {
-    sample_scan_kernel<float><<<scan, kSampleThreads, 0, stream>>>(a, w);
-    sample_draw_kernel<float><<<draw, kSampleThreads, 0, stream>>>(a, w);
-  } else {
-    sample_scan_kernel<uint16_t><<<scan, kSampleThreads, 0, stream>>>(a, w);
-    sample_draw_kernel<uint16_t><<<draw, kSampleThreads, 0, stream>>>(a, w);
-  }
+  workspace_parts(a.rows, a.vocab, w, static_cast<char*>(ws));
+  const dim3 scan((unsigned)w.chunks, (unsigned)a.rows), rows((unsigned)a.rows);
+  // rows without filters, and rows whose logits are all candidates, are never left over
+  const bool rest = (a.top_k || a.top_p || a.min_p) && a.vocab > kSmallVocab;
+  const auto launch = [&](auto type) {
+    using T = decltype(type);
+    sample_scan_kernel<T><<<scan, kSampleThreads, 0, stream>>>(a, w);
+    sample_draw_kernel<T><<<rows, kSampleThreads, 0, stream>>>(a, w);
+    if (rest) sample_rest_kernel<T><<<rows, kSampleThreads, 0, stream>>>(a, w);
+  };
+  if (a.dtype == W4_OUT_F32) launch(0.0f);
+  else launch((uint16_t)0);
 }
 
 }  // namespace w4
