@@ -40,7 +40,7 @@ constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kPer = 16;                               // logits a thread
 constexpr int kChunk = kSampleThreads * kPer;
-constexpr int kMostChunks = ((1 << 20) + 7 + kChunk - 1) / kChunk;
+constexpr int kMostChunks = (1 << 20) / kChunk;        // one a lane
 constexpr int kGroups = 256;                           // of 4 threads each
 constexpr int kListMost = 512;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
@@ -148,36 +148,39 @@ struct Row {
     else return z[i];
   }
   __device__ __forceinline__ uint32_t key(int i) const { return order_key(value(i)); }
-  // Places of the row's first chunk in front of the row: chunks are cut at multiples of 16 bytes.
-  __device__ __forceinline__ int in_front() const { return (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T)); }
 };
 
-// The thread's logits of a chunk (-infinity where there is none), and their ids.
+// The thread's logits of a chunk (-infinity where there is none), and their ids, in
+// vectors of 16 bytes (at any multiple of the type's size).  A vector that would pass
+// the row's end is moved back to end there, and what belongs to the vectors before it
+// counts as none.
+typedef u32x4 LooseVector __attribute__((aligned(2)));
+
 template <typename T>
 struct Piece {
   static constexpr int kVec = 16 / sizeof(T);
   float z[kPer];
-  int first;   // id of the chunk's first place
-  __device__ __forceinline__ int id(int i) const {
-    return first + (i / kVec * kSampleThreads + (int)threadIdx.x) * kVec + i % kVec;
-  }
-  __device__ __forceinline__ Piece(const Row<T>& row, int chunk) {
-    first = chunk * kChunk - row.in_front();
-    if (first >= 0 && first + kChunk <= row.n) {
+  int first, end;   // id of the chunk's first place; the row's length
+  __device__ __forceinline__ int place(int j) const { return first + (j * kSampleThreads + (int)threadIdx.x) * kVec; }
+  __device__ __forceinline__ int id(int i) const { return min(place(i / kVec), end - kVec) + i % kVec; }
+  __device__ __forceinline__ Piece(const Row<T>& row, int chunk) : first(chunk * kChunk), end(row.n) {
+    if (end >= kVec) {
       u32x4 v[kPer / kVec];
 #pragma unroll
-      for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const u32x4*>(row.z + id(j * kVec));
+      for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const LooseVector*>(row.z + id(j * kVec));
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
         z[i] = __uint_as_float(sizeof(T) == 4 ? word : i % 2 ? word & 0xFFFF0000u : word << 16);
       }
-    } else {   // the row's first or last chunk: value by value
+      if (first + kChunk > end) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int at = id(i);
-        z[i] = at >= 0 && at < row.n ? row.value(at) : -INFINITY;
+        for (int i = 0; i < kPer; ++i) z[i] = id(i) < place(i / kVec) ? -INFINITY : z[i];
       }
+    } else {   // less than a vector: the first thread's first places
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        z[i] = i < kVec && threadIdx.x == 0 && id(i) >= 0 ? row.value(id(i)) : -INFINITY;
     }
   }
 };
@@ -202,7 +205,7 @@ struct ChunkInfo {
   int32_t n;         // candidates; more than the list holds: it is not whole
 };
 
-int chunks_of(int64_t vocab) { return (int)((vocab + 7 + kChunk - 1) / kChunk); }   // a row starts inside 16 bytes
+int chunks_of(int64_t vocab) { return (int)((vocab + kChunk - 1) / kChunk); }
 __host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSmallVocab ? kSmallVocab : kListMost; }
 
 // A chunk's weights are summed in segments, a vector of each thread of a wave, which
@@ -361,17 +364,10 @@ __device__ __forceinline__ int pick_lane(double v, double target, double& before
   return pick;
 }
 
-// The same over up to 65 chunks, the last one's value (`behind`) apart; total: the
-// sum of all.
-__device__ __forceinline__ int pick_chunk(double v, double behind, double u, double& before, double& total) {
-  const double front = lane_value(wave_scan(v), 63);
-  total = front + behind;
-  const double target = u * total;
-  if (behind > 0.0 && !(front > target)) {
-    before = front;
-    return 64;
-  }
-  return pick_lane(v, target, before);
+// The same with a share of the whole sum for the target.
+__device__ __forceinline__ int pick_share(double v, double u, double& before, double& total) {
+  total = lane_value(wave_scan(v), 63);
+  return pick_lane(v, u * total, before);
 }
 
 // The id of a chunk at which the running sum of f(logit, id) exceeds target, in the
@@ -655,15 +651,14 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     double part = (double)wave_sum(whole) * s.scale[c], in_bin = 0.0;
     for (int i = lane; i < n; i += 64) {
       const uint64_t v = s.v[i];
-      if (v >= last && (int)((~(uint32_t)v + row.in_front()) / kChunk) == c) in_bin += weight((uint32_t)(v >> 32));
+      if (v >= last && (int)(~(uint32_t)v / kChunk) == c) in_bin += weight((uint32_t)(v >> 32));
     }
     part += wave_sum(in_bin);
     if (lane == 0) s.sums[c] = part;
   }
   __syncthreads();
   double before, total;
-  const int c = pick_chunk(lane < min(w.chunks, 64) ? s.sums[lane] : 0.0, w.chunks > 64 ? s.sums[64] : 0.0, set.u, before,
-                           total);
+  const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set.u, before, total);
   // kept: whole bins above, and in the bin up to the last one
   const auto share = [&](float z, int id) {
     const int b = bin_of((double)z);
@@ -885,17 +880,15 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   const int tid = threadIdx.x, lane = tid & 63;
   const ChunkInfo* info = w.info + r * w.chunks;
   const Settings set = settings_of(a, r);
-  // the chunks' figures, one a lane (and the 65th)
-  ChunkInfo mine{}, behind{};
+  // the chunks' figures, one a lane
+  ChunkInfo mine{};
   if (lane < w.chunks) mine = info[lane];
-  if (w.chunks > 64) behind = info[64];
-  const uint32_t top = max(wave_max_of_quads(quad_max(mine.top)), behind.top);
-  const uint32_t bound = max(wave_max_of_quads(quad_max(mine.bound)), behind.bound);
+  const uint32_t top = wave_max_of_quads(quad_max(mine.top));
+  const uint32_t bound = wave_max_of_quads(quad_max(mine.bound));
   if (tid == 0) w.todo[r] = 0;
   if (top == kNanKey || top == 0 || set.greedy()) {
     // the lowest id that has it: that of the first chunk
-    const uint64_t have = __ballot(mine.top == top);
-    const int arg = have ? __builtin_amdgcn_readlane(mine.arg, __builtin_ctzll(have | 1ull << 63)) : behind.arg;
+    const int arg = __builtin_amdgcn_readlane(mine.arg, __builtin_ctzll(__ballot(mine.top == top)));
     if (tid == 0) {
       const bool none = top == kNanKey || top == 0;
       a.tokens[r] = none ? -1 : arg;
@@ -907,8 +900,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   double all = 0.0, before = 0.0;   // of the whole row's weights
   int chunk = 0;
   if (set.sums(a.vocab)) {
-    const double last = behind.top == 0 ? 0.0 : behind.sum * weight(behind.top);
-    chunk = pick_chunk(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), last, set.u, before, all);
+    chunk = pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set.u, before, all);
   }
   if (!set.filters(a.vocab)) {
     if (tid >= 64) return;   // one wave reads on: the segment, and the logit
@@ -919,7 +911,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
     const int seg = pick_lane(w.segment[at * kMostSegments + lane] * scale, target, in_front);
     target -= in_front;
     constexpr int kVec = Piece<T>::kVec;
-    const int first = chunk * kChunk - row.in_front() +
+    const int first = chunk * kChunk +
                       (seg / kSampleWaves * kSampleThreads + seg % kSampleWaves * 64 + lane) * kVec;
     double own[kVec], sum = 0.0;
 #pragma unroll
@@ -949,12 +941,12 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   }
 
   // candidates from the bound up
-  const bool whole = __ballot(mine.n > list_most(a.vocab)) == 0 && behind.n <= list_most(a.vocab);
+  const bool whole = __ballot(mine.n > list_most(a.vocab)) == 0;
   if (tid == 0) s_n = 0;
   __syncthreads();
   if (whole) {
     for (int c = tid / 64; c < w.chunks; c += kSampleWaves) {
-      const int n = c < 64 ? __builtin_amdgcn_readlane(mine.n, c) : behind.n;
+      const int n = __builtin_amdgcn_readlane(mine.n, c);
       const uint64_t* list = w.list + (r * w.chunks + c) * list_most(a.vocab);
       for (int i = lane; i < n; i += 64) {
         const uint64_t v = list[i];
@@ -1048,15 +1040,13 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
   const ChunkInfo* info = w.info + r * w.chunks;
   const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
   const Settings set = settings_of(a, r);
-  ChunkInfo mine{}, behind{};
+  ChunkInfo mine{};
   if (lane < w.chunks) mine = info[lane];
-  if (w.chunks > 64) behind = info[64];
-  const uint32_t top = max(wave_max_of_quads(quad_max(mine.top)), behind.top);
+  const uint32_t top = wave_max_of_quads(quad_max(mine.top));
   const Weight weight = set.weight(top);
   double all = 0.0, before;
   if (set.sums(a.vocab)) {
-    const double last = behind.top == 0 ? 0.0 : behind.sum * weight(behind.top);
-    pick_chunk(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), last, set.u, before, all);
+    pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set.u, before, all);
   }
   if (set.bins(a.vocab) && whole_row(s.whole, a, w, row, r, set, weight, all)) return;
   __syncthreads();
