@@ -42,6 +42,7 @@ constexpr int kPer = 16;                               // logits a thread
 constexpr int kChunk = kSampleThreads * kPer;
 constexpr int kMostChunks = (1 << 20) / kChunk;        // one a lane
 constexpr int kGroups = 256;                           // of 4 threads each
+constexpr int kRankSure = 64, kRankMost = 192;
 constexpr int kListMost = 512;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
@@ -87,6 +88,21 @@ __device__ __forceinline__ uint32_t order_key(float z) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k); }
 
+// The rank of a chunk's bound.  Up to 64 it is top_k: then the chunk with the largest
+// bound has that many from there up, wherever the row's first ones lie.  Beyond, the
+// rank at which about 1.5 top_k logits of the row are candidates if its chunks are
+// alike (groups with one of e logits from the bound up: 256 (1 - exp(-e / 256))); a row
+// without top_k gets 64.  Ranks next to the number of groups make lists overflow.
+__device__ __forceinline__ int rank_of(int k, int n, int chunks, int groups) {
+  int rank = kRankSure;
+  if (k <= kRankSure) rank = max(k, 16);
+  else if (k < n) {
+    const float e = 1.5f * (float)k / (float)chunks;
+    rank = (int)fminf(fmaxf(kGroups * (1.0f - __expf(-e / kGroups)), kRankSure), kRankMost);
+  }
+  return max(1, min(rank, 3 * groups / 4));
+}
+
 // A row's weights: 2^((z - m) log2 e / T).  (Beside an infinite m all but its equals
 // are infinitely far below it, and weigh 0.)
 struct Weight {
@@ -96,10 +112,8 @@ struct Weight {
     return exp2_f64(z == m ? 0.0 : ((double)z - top) * per);
   }
   __device__ __forceinline__ double operator()(uint32_t key) const { return of(key_value(key)); }
-  // sixteenths of an octave, whole ones
-  __device__ __forceinline__ double steps(double z) const {
-    return __builtin_fma(z, 16.0 * per, kLarge) - kLarge;
-  }
+  // Sixteenths of an octave, whole ones: exact in fp32 below 2^24, and growing with z.
+  __device__ __forceinline__ float steps(float z) const { return __builtin_rintf(z * (float)(16.0 * per)); }
 };
 // A weight in multiples of 2^-43 (the last bits of a number between 2^9 and 2^10).
 __device__ __forceinline__ unsigned long long fixed_of(double w) {
@@ -117,7 +131,7 @@ struct Settings {
   // rows that need the sum of all weights, candidates, a histogram
   __device__ __forceinline__ bool sums(int n) const { return !greedy() && k >= n && (p < 1.0 || few == 0.0); }
   __device__ __forceinline__ bool lists(int n) const { return !greedy() && filters(n); }
-  __device__ __forceinline__ bool bins(int n) const { return lists(n) && n > kSmallVocab && k > kGroups; }
+  __device__ __forceinline__ bool bins(int n) const { return lists(n) && n > kSmallVocab && k > kRankSure; }
   __device__ __forceinline__ Weight weight(uint32_t top) const {
     const float m = key_value(top);
     return {m, (double)m, 0x1.71547652b82fep+0 / (double)temperature};
@@ -198,7 +212,7 @@ __device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, const 
 
 struct ChunkInfo {
   double sum;        // of the weights beside top
-  double ref;        // top in sixteenths of an octave, whole ones: the first bin; NaN: no histogram
+  float ref;         // top in sixteenths of an octave, whole ones: the first bin; NaN: no histogram
   uint32_t top;      // largest key; 0: no logit above -infinity
   int32_t arg;       // the lowest id that has it
   uint32_t bound;    // every logit from this key up is in the list
@@ -280,7 +294,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
       g[i] = s_group[64 * i + lane];
       some += __builtin_popcountll(__ballot(g[i] > 0));
     }
-    const int rank = max(1, min(some, set.k < a.vocab ? min(max(set.k, 16), kGroups) : 128));
+    const int rank = rank_of(set.k, a.vocab, w.chunks, some);
     uint32_t bound = 0;
     for (uint32_t bit = 1u << 31; bit >= 1u << 14; bit >>= 1) {
       int n = 0;
@@ -291,8 +305,8 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
     if (lane == 0) s_bound = max(bound, kLowestKey);
   }
   const Weight weight = set.weight(top);
-  const double ref = weight.steps(weight.top);
-  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 && __builtin_fabs(ref) < 0x1p30;
+  const float ref = weight.steps(weight.m);
+  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 && __builtin_fabsf(ref) < 0x1p22f;
   constexpr int kVec = Piece<T>::kVec;
   double part[kPer / kVec] = {};
   if (top >= kPosInfKey) {
@@ -304,8 +318,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
     for (int i = 0; i < kPer; ++i) {
       const double e = exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
       part[i / kVec] += e;
-      const double d = ref - weight.steps((double)piece.z[i]);
-      const int b = d < kFine - 1 ? (int)d : kFine - 1;
+      const int b = (int)fminf(ref - weight.steps(piece.z[i]), (float)(kFine - 1));
       const unsigned long long fixed = fixed_of(e);
       if (fixed > 0) atomicAdd(&s_mass[b], fixed);
       if (counts && piece.z[i] > -INFINITY) atomicAdd(&s_count[b], 1u);
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   if (wv == 0) {
     const double seg = lane < kSegments<T> ? s_sum[lane] : 0.0, sum = wave_sum(seg);
     if (sums) w.segment[at * kMostSegments + lane] = seg;
-    if (lane == 0) w.info[at] = {sum, bins ? ref : __builtin_nan(""), top, s_arg, bound, s_n};
+    if (lane == 0) w.info[at] = {sum, bins ? ref : __builtin_nanf(""), top, s_arg, bound, s_n};
   }
 }
 
@@ -416,14 +429,9 @@ __device__ __forceinline__ int pick_in_chunk(PickShared& s, const Piece<T>& p, c
 }
 
 // v0 (places 0 .. 1023) and v1 (1024 .. 2047) of all threads in descending order; N, a
-// power of two, is the number of places in use.  Bitonic: exchanges within a wave by
-// moves between lanes, others through LDS.
-__device__ __forceinline__ uint64_t exchange(uint64_t v, uint64_t other, int place, int size, int step) {
-  const bool larger = ((place & step) == 0) == ((place & size) == 0);
-  return (v > other) == larger ? v : other;
-}
-// Of lane ^ 16 (rows swapped) or lane ^ 32 (halves).
-__device__ __forceinline__ uint32_t across_u32(uint32_t v, int step) {
+// power of two from 64 up, is the number of places in use.  Bitonic: exchanges within
+// a wave by moves between lanes, others through LDS.
+__device__ __forceinline__ uint32_t across_u32(uint32_t v, int step) {   // of lane ^ 16 (rows swapped) or ^ 32 (halves)
   if (step == 16) {
     const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     return (threadIdx.x & 16) ? p[0] : p[1];
@@ -431,24 +439,36 @@ __device__ __forceinline__ uint32_t across_u32(uint32_t v, int step) {
   const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return (threadIdx.x & 32) ? p[0] : p[1];
 }
-__device__ __forceinline__ uint64_t across_u64(uint64_t v, int step) {
-  return ((uint64_t)across_u32((uint32_t)(v >> 32), step) << 32) | across_u32((uint32_t)v, step);
+// The value of lane ^ step, or one's own, whichever is larger (smaller).
+__device__ __forceinline__ uint64_t exchange(uint64_t v, int step, bool larger) {
+  const uint64_t other = step == 1   ? dpp_u64<0xB1>(v)                   // quad_perm [1,0,3,2]
+                         : step == 2 ? dpp_u64<0x4E>(v)                   // quad_perm [2,3,0,1]
+                         : step == 4 ? dpp_u64<0x1B>(dpp_u64<0x141>(v))   // half rows and quads mirrored
+                         : step == 8 ? dpp_u64<0x128>(v)                  // row_ror 8
+                                     : ((uint64_t)across_u32((uint32_t)(v >> 32), step) << 32) | across_u32((uint32_t)v, step);
+  return (v > other) == larger ? v : other;
 }
-__device__ __forceinline__ void wave_stages(uint64_t& v, int place, int size) {
+__device__ __forceinline__ uint64_t wave_merge(uint64_t v, bool descending) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int step = 32; step > 0; step /= 2)
-    if (size > step) {
-      const uint64_t other = step == 1   ? dpp_u64<0xB1>(v)                   // quad_perm [1,0,3,2]
-                             : step == 2 ? dpp_u64<0x4E>(v)                   // quad_perm [2,3,0,1]
-                             : step == 4 ? dpp_u64<0x1B>(dpp_u64<0x141>(v))   // half rows and quads mirrored
-                             : step == 8 ? dpp_u64<0x128>(v)                  // row_ror 8
-                                         : across_u64(v, step);
-      v = exchange(v, other, place, size, step);
-    }
+  for (int step = 32; step > 0; step /= 2) v = exchange(v, step, ((lane & step) == 0) == descending);
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_sort(uint64_t v, bool descending) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int size = 2; size < 64; size *= 2)
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2)
+      v = exchange(v, step, ((lane & step) == 0) == ((lane & size) == 0));
+  return wave_merge(v, descending);
 }
 __device__ __forceinline__ void sort_descending(uint64_t* s_v, uint64_t& v0, uint64_t& v1, int N) {
   const int tid = threadIdx.x;
-  for (int size = 2; size <= N; size *= 2) {
+  const bool two = N > kSampleThreads;
+  if (tid < N) v0 = wave_sort(v0, N == 64 || (tid & 64) == 0);
+  if (two) v1 = wave_sort(v1, (tid & 64) == 0);
+  for (int size = 128; size <= N; size *= 2) {
     if (size > kSampleThreads) {   // step 1024: the thread's own two
       const uint64_t a = v0, b = v1;
       v0 = a > b ? a : b;
@@ -457,14 +477,17 @@ __device__ __forceinline__ void sort_descending(uint64_t* s_v, uint64_t& v0, uin
     for (int step = min(size, kSampleThreads) / 2; step >= 64; step /= 2) {
       __syncthreads();
       s_v[tid] = v0;
-      if (N > kSampleThreads) s_v[tid + kSampleThreads] = v1;
+      if (two) s_v[tid + kSampleThreads] = v1;
       __syncthreads();
-      v0 = exchange(v0, s_v[tid ^ step], tid, size, step);
-      if (N > kSampleThreads)
-        v1 = exchange(v1, s_v[(tid ^ step) + kSampleThreads], tid + kSampleThreads, size, step);
+      const uint64_t o0 = s_v[tid ^ step];
+      v0 = (v0 > o0) == (((tid & step) == 0) == ((tid & size) == 0)) ? v0 : o0;
+      if (two) {
+        const uint64_t o1 = s_v[(tid ^ step) + kSampleThreads];
+        v1 = (v1 > o1) == (((tid & step) == 0) == (((tid + kSampleThreads) & size) == 0)) ? v1 : o1;
+      }
     }
-    if (tid < N) wave_stages(v0, tid, size);
-    if (N > kSampleThreads) wave_stages(v1, tid + kSampleThreads, size);
+    if (tid < N) v0 = wave_merge(v0, (tid & size) == 0);
+    if (two) v1 = wave_merge(v1, ((tid + kSampleThreads) & size) == 0);
   }
 }
 
@@ -524,7 +547,7 @@ template <typename T>
 __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, const SampleWork& w, const Row<T>& row,
                                        int64_t r, const Settings& set, const Weight& weight, double all) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const double ref = weight.steps(weight.top);
+  const float ref = weight.steps(weight.m);
   const ChunkInfo* info = w.info + r * w.chunks;
   const unsigned long long* mass = w.mass + r * w.chunks * kFine;
   const uint16_t* count = w.count + r * w.chunks * kFine;
@@ -533,17 +556,14 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   __syncthreads();
   if (tid < w.chunks) {
     const ChunkInfo f = info[tid];
-    const double shift = ref - f.ref;
+    const float shift = ref - f.ref;
     s.scale[tid] = f.top == 0 ? 0.0 : weight(f.top) * (1.0 / kFixed);
     s.shift[tid] = f.top == 0 || !(shift < kFine) ? kFine : (int)shift;
     if (f.top > 0 && f.ref != f.ref) s.ok = 0;
   }
   __syncthreads();
   if (!s.ok) return false;
-  const auto bin_of = [&](double z) {
-    const double d = ref - weight.steps(z);
-    return d < kFine - 1 ? (int)d : kFine - 1;
-  };
+  const auto bin_of = [&](float z) { return (int)fminf(ref - weight.steps(z), (float)(kFine - 1)); };
   // the row's histograms, a bin a thread (the last bin is not used)
   const bool use_k = set.k < a.vocab, use_p = set.p < 1.0;
   double row_mass = 0.0, row_count = 0.0;
@@ -566,7 +586,7 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     for_chunks(row, w.chunks, [&](const Piece<T>& p) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (bin_of((double)p.z[i]) == bin) {
+        if (bin_of(p.z[i]) == bin) {
           const int at = atomicAdd(&s.n, 1);
           if (at < kSortMost) s.v[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
         }
@@ -622,8 +642,14 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     last = s.last;
   }
   if (set.few > 0.0) {
-    // the weight's place among the logits
-    const int at = bin_of(weight.top + log2(set.few) / weight.per);
+    // the lowest key that weighs as much, and its bin
+    uint32_t lo = kLowestKey, hi = order_key(weight.m);
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if (weight(mid) >= set.few) hi = mid;
+      else lo = mid + 1;
+    }
+    const int at = bin_of(key_value(lo));
     if (at <= bin) {
       if (at >= kFine - 1 || !list(at)) return false;
       bin = at;
@@ -661,7 +687,7 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set.u, before, total);
   // kept: whole bins above, and in the bin up to the last one
   const auto share = [&](float z, int id) {
-    const int b = bin_of((double)z);
+    const int b = bin_of(z);
     if (b > bin || (b == bin && (((uint64_t)order_key(z) << 32) | (uint32_t)~id) < last)) return 0.0;
     return weight.of(z);
   };
