@@ -10,7 +10,7 @@
 //         bounds up are among the candidates: where that piece of the order decides
 //         the filters, it is sorted, cut, and the draw is made among what is left,
 //         in the order of the ids.  A row without filters needs no candidates, only
-//         the 256 or 512 logits in which the sums pass the number.
+//         the 1024 logits in which the sums pass the number.
 // Where that piece may be too short (a nucleus of thousands of tokens) the scan also
 // leaves a histogram of weights (and counts) over bins of a sixteenth of an octave,
 // and a third kernel (rest) takes the rows that the second left: the histogram tells
@@ -42,8 +42,8 @@ constexpr int kPer = 16;                               // logits a thread
 constexpr int kChunk = kSampleThreads * kPer;
 constexpr int kMostChunks = (1 << 20) / kChunk;        // one a lane
 constexpr int kGroups = 256;                           // of 4 threads each
-constexpr int kRankSure = 64, kRankMost = 192;
-constexpr int kListMost = 512;                         // candidates of a chunk
+constexpr int kRankSure = 64, kRankMost = 224;
+constexpr int kListMost = 768;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
@@ -93,14 +93,14 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 // rank at which about 1.5 top_k logits of the row are candidates if its chunks are
 // alike (groups with one of e logits from the bound up: 256 (1 - exp(-e / 256))); a row
 // without top_k gets 64.  Ranks next to the number of groups make lists overflow.
-__device__ __forceinline__ int rank_of(int k, int n, int chunks, int groups) {
+__device__ __forceinline__ int rank_of(int k, int n, int groups) {
   int rank = kRankSure;
   if (k <= kRankSure) rank = max(k, 16);
   else if (k < n) {
-    const float e = 1.5f * (float)k / (float)chunks;
+    const float e = 1.5f * kChunk * (float)k / (float)n;
     rank = (int)fminf(fmaxf(kGroups * (1.0f - __expf(-e / kGroups)), kRankSure), kRankMost);
   }
-  return max(1, min(rank, 3 * groups / 4));
+  return max(1, min(rank, 7 * groups / 8));
 }
 
 // A row's weights: 2^((z - m) log2 e / T).  (Beside an infinite m all but its equals
@@ -164,47 +164,54 @@ struct Row {
   __device__ __forceinline__ uint32_t key(int i) const { return order_key(value(i)); }
 };
 
-// The thread's logits of a chunk (-infinity where there is none), and their ids, in
-// vectors of 16 bytes (at any multiple of the type's size).  A vector that would pass
-// the row's end is moved back to end there, and what belongs to the vectors before it
-// counts as none.
+// The thread's logits of a chunk (-infinity where there is none), and their ids: a wave
+// has 1024 neighbouring ones, its lanes vectors of 16 bytes (at any multiple of the
+// type's size).  A vector that would pass the row's end is moved back to end there,
+// and what belongs to the vectors before it counts as none.
 typedef u32x4 LooseVector __attribute__((aligned(2)));
+constexpr int kWavePart = 64 * kPer;
 
 template <typename T>
 struct Piece {
   static constexpr int kVec = 16 / sizeof(T);
   float z[kPer];
-  int first, end;   // id of the chunk's first place; the row's length
-  __device__ __forceinline__ int place(int j) const { return first + (j * kSampleThreads + (int)threadIdx.x) * kVec; }
+  int first, end;   // id of the lane's first place; the row's length
+  __device__ __forceinline__ int place(int j) const { return first + j * 64 * kVec; }
   __device__ __forceinline__ int id(int i) const { return min(place(i / kVec), end - kVec) + i % kVec; }
-  __device__ __forceinline__ Piece(const Row<T>& row, int chunk) : first(chunk * kChunk), end(row.n) {
-    if (end >= kVec) {
-      u32x4 v[kPer / kVec];
-#pragma unroll
-      for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const LooseVector*>(row.z + id(j * kVec));
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
-        z[i] = __uint_as_float(sizeof(T) == 4 ? word : i % 2 ? word & 0xFFFF0000u : word << 16);
-      }
-      if (first + kChunk > end) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) z[i] = id(i) < place(i / kVec) ? -INFINITY : z[i];
-      }
-    } else {   // less than a vector: the first thread's first places
-#pragma unroll
+  // part: 1024 logits of the row
+  __device__ __forceinline__ Piece(const Row<T>& row, int part)
+      : first(part * kWavePart + (int)(threadIdx.x & 63) * kVec), end(row.n) {
+    if (__builtin_expect(end < kVec, 0)) {   // less than a vector: the first lane's first places
       for (int i = 0; i < kPer; ++i)
-        z[i] = i < kVec && threadIdx.x == 0 && id(i) >= 0 ? row.value(id(i)) : -INFINITY;
+        z[i] = i < kVec && first == 0 && id(i) >= 0 ? row.value(id(i)) : -INFINITY;
+      return;
+    }
+    u32x4 v[kPer / kVec];
+#pragma unroll
+    for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const LooseVector*>(row.z + id(j * kVec));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
+      z[i] = __uint_as_float(sizeof(T) == 4 ? word : i % 2 ? word & 0xFFFF0000u : word << 16);
+    }
+    if (part * kWavePart + kWavePart > end) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) z[i] = id(i) < place(i / kVec) ? -INFINITY : z[i];
     }
   }
 };
 
+// The wave's part of a chunk.
+__device__ __forceinline__ int part_of(int chunk) {
+  return chunk * kSampleWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
 // f of every chunk: the next one's loads are issued first.
 template <typename T, typename F>
 __device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, const F& f) {
-  Piece<T> now(row, 0);
+  Piece<T> now(row, part_of(0));
   for (int c = 0; c < chunks; ++c) {
-    const Piece<T> next(row, min(c + 1, chunks - 1));
+    const Piece<T> next(row, part_of(min(c + 1, chunks - 1)));
     f(now);
     now = next;
   }
@@ -222,15 +229,9 @@ struct ChunkInfo {
 int chunks_of(int64_t vocab) { return (int)((vocab + kChunk - 1) / kChunk); }
 __host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSmallVocab ? kSmallVocab : kListMost; }
 
-// A chunk's weights are summed in segments, a vector of each thread of a wave, which
-// follow one another in the order of the ids.
-template <typename T>
-constexpr int kSegments = kSampleWaves * kPer * (int)sizeof(T) / 16;
-constexpr int kMostSegments = kSampleWaves * kPer / 4;
-
 struct SampleWork {
   ChunkInfo* info;             // [rows][chunks]
-  double* segment;             // [rows][chunks][kMostSegments], beside the chunk's top
+  double* part;                // [rows][chunks][kSampleWaves]: the waves' sums, beside the chunk's top
   int32_t* todo;               // [rows]: left to the third kernel
   uint64_t* list;              // [rows][chunks][list_most]: key << 32 | ~id
   unsigned long long* mass;    // [rows][chunks][kFine]
@@ -243,7 +244,7 @@ template <typename T>
 __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleArgs a, SampleWork w) {
   __shared__ uint32_t s_top[kSampleWaves];
   __shared__ int s_arg, s_n;
-  __shared__ double s_sum[kMostSegments];
+  __shared__ double s_sum[kSampleWaves];
   __shared__ uint32_t s_group[kGroups];
   __shared__ uint32_t s_bound;
   __shared__ unsigned long long s_mass[kFine];
@@ -251,16 +252,12 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   const int64_t r = blockIdx.y, at = r * w.chunks + blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
-  const Piece<T> piece(row, blockIdx.x);
+  const Piece<T> piece(row, part_of(blockIdx.x));
   const Settings set = settings_of(a, r);
-  float m = piece.z[0];
-  bool nan = m != m;
+  float m = piece.z[0];   // (a NaN stays)
 #pragma unroll
-  for (int i = 1; i < kPer; ++i) {
-    nan |= piece.z[i] != piece.z[i];
-    m = fmaxf(m, piece.z[i]);
-  }
-  const uint32_t own = nan ? kNanKey : order_key(m), mine = own == kNegInfKey ? 0u : own;
+  for (int i = 1; i < kPer; ++i) m = __builtin_elementwise_maximum(m, piece.z[i]);
+  const uint32_t own = order_key(m), mine = own == kNegInfKey ? 0u : own;
   uint32_t top = quad_max(mine);
   if ((lane & 3) == 0) s_group[tid / 4] = top;
   top = wave_max_of_quads(top);
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
       g[i] = s_group[64 * i + lane];
       some += __builtin_popcountll(__ballot(g[i] > 0));
     }
-    const int rank = rank_of(set.k, a.vocab, w.chunks, some);
+    const int rank = rank_of(set.k, a.vocab, some);
     uint32_t bound = 0;
     for (uint32_t bit = 1u << 31; bit >= 1u << 14; bit >>= 1) {
       int n = 0;
@@ -307,36 +304,37 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   const Weight weight = set.weight(top);
   const float ref = weight.steps(weight.m);
   const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 && __builtin_fabsf(ref) < 0x1p22f;
-  constexpr int kVec = Piece<T>::kVec;
-  double part[kPer / kVec] = {};
+  double sum = 0.0;
   if (top >= kPosInfKey) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) part[i / kVec] += piece.z[i] == INFINITY ? 1.0 : 0.0;
+    for (int i = 0; i < kPer; ++i) sum += piece.z[i] == INFINITY ? 1.0 : 0.0;
   } else if (bins) {
     const bool counts = set.k < a.vocab;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const double e = exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
-      part[i / kVec] += e;
-      const int b = (int)fminf(ref - weight.steps(piece.z[i]), (float)(kFine - 1));
-      const unsigned long long fixed = fixed_of(e);
-      if (fixed > 0) atomicAdd(&s_mass[b], fixed);
-      if (counts && piece.z[i] > -INFINITY) atomicAdd(&s_count[b], 1u);
+    for (int i = 0; i < kPer; i += 4) {   // four series together share their coefficients
+      double e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = exp2_f64(((double)piece.z[i + j] - weight.top) * weight.per);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum += e[j];
+        const int b = (int)fminf(ref - weight.steps(piece.z[i + j]), (float)(kFine - 1));
+        const unsigned long long fixed = fixed_of(e[j]);
+        if (fixed > 0) atomicAdd(&s_mass[b], fixed);
+        if (counts && piece.z[i + j] > -INFINITY) atomicAdd(&s_count[b], 1u);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   } else if (sums && top > 0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      part[i / kVec] += exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
+      sum += exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
       // two at a time: with more of them under way registers run out for a CU's second workgroup
       if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
-#pragma unroll
-  for (int j = 0; j < kPer / kVec; ++j) {
-    const double sum = wave_sum(part[j]);
-    if (lane == 0) s_sum[j * kSampleWaves + wv] = sum;
-  }
+  sum = wave_sum(sum);
+  if (lane == 0) s_sum[wv] = sum;
   __syncthreads();
   const uint32_t bound = s_bound;
   if (lists && mine >= bound) {
@@ -355,18 +353,14 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   }
   __syncthreads();
   if (wv == 0) {
-    const double seg = lane < kSegments<T> ? s_sum[lane] : 0.0, sum = wave_sum(seg);
-    if (sums) w.segment[at * kMostSegments + lane] = seg;
+    const double part = lane < kSampleWaves ? s_sum[lane] : 0.0;
+    sum = wave_sum(part);
+    if (sums && lane < kSampleWaves) w.part[at * kSampleWaves + lane] = part;
     if (lane == 0) w.info[at] = {sum, bins ? ref : __builtin_nanf(""), top, s_arg, bound, s_n};
   }
 }
 
 // ---------------------------------------------------------------------- draw
-struct PickShared {
-  double seg[kSampleWaves * kPer / 4];
-  int found;
-};
-
 // The first of 64 values (one a lane) at which their running sum exceeds target, the
 // last positive one if none does; before: the sum of those in front of it.
 __device__ __forceinline__ int pick_lane(double v, double target, double& before) {
@@ -383,49 +377,51 @@ __device__ __forceinline__ int pick_share(double v, double u, double& before, do
   return pick_lane(v, u * total, before);
 }
 
-// The id of a chunk at which the running sum of f(logit, id) exceeds target, in the
-// order of the ids (vector by vector, thread by thread).
+// The id of a wave's part at which the running sum of f(logit, id) exceeds target, in
+// the order of the ids (vector by vector, lane by lane), the last one with f > 0 if none
+// does; share: f there.
 template <typename T, typename F>
-__device__ __forceinline__ int pick_in_chunk(PickShared& s, const Piece<T>& p, const F& f, double target) {
-  constexpr int kVec = Piece<T>::kVec, kVectors = kPer / kVec;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  double part[kVectors];
-  __syncthreads();   // s is free
+__device__ __forceinline__ int pick_in_part(const Piece<T>& p, const F& f, double target, double& share) {
+  constexpr int kVec = Piece<T>::kVec;
+  double own[kPer], chosen = 0.0, run = 0.0, before = 0.0;
+  int vector = 0;
+  bool found = false;
 #pragma unroll
-  for (int j = 0; j < kVectors; ++j) {
-    part[j] = 0.0;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) part[j] += f(p.z[j * kVec + i], p.id(j * kVec + i));
-    const double sum = wave_sum(part[j]);
-    if (lane == 0) s.seg[j * kSampleWaves + wv] = sum;
-  }
-  __syncthreads();
-  double before, in_wave;
-  const int seg = pick_lane(lane < kVectors * kSampleWaves ? s.seg[lane] : 0.0, target, before);
-  if (wv == seg % kSampleWaves) {
+  for (int j = 0; j < kPer / kVec; ++j) {
     double mine = 0.0;
 #pragma unroll
-    for (int j = 0; j < kVectors; ++j)
-      if (j == seg / kSampleWaves) mine = part[j];
-    target -= before;
-    const int l = pick_lane(mine, target, in_wave);
-    if (lane == l) {
-      target -= in_wave;
-      double run = 0.0;
-      int found = -1, last = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i / kVec == seg / kSampleWaves) {
-          const double v = f(p.z[i], p.id(i));
-          run += v;
-          if (v > 0.0) last = p.id(i);
-          if (v > 0.0 && found < 0 && run > target) found = p.id(i);
-        }
-      s.found = found >= 0 ? found : last;
+    for (int i = j * kVec; i < (j + 1) * kVec; ++i) {
+      own[i] = f(p.z[i], p.id(i));
+      mine += own[i];
     }
+    const double sum = wave_sum(mine);
+    if (sum > 0.0 && !found) {
+      vector = j;
+      chosen = mine;
+      before = run;
+      found = run + sum > target;
+    }
+    run += sum;
   }
-  __syncthreads();
-  return s.found;
+  double in_front;
+  const int lane = pick_lane(chosen, target - before, in_front);
+  target -= before + in_front;
+  int id = 0;
+  run = 0.0;
+  share = 0.0;
+  found = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i / kVec == vector) {
+      run += own[i];
+      if (own[i] > 0.0 && !found) {
+        id = p.id(i);
+        share = own[i];
+        found = run > target;
+      }
+    }
+  share = lane_value(share, lane);
+  return __builtin_amdgcn_readlane(id, lane);
 }
 
 // v0 (places 0 .. 1023) and v1 (1024 .. 2047) of all threads in descending order; N, a
@@ -520,7 +516,6 @@ struct WholeShared {
   double scale[kMostChunks], sums[kMostChunks];
   int shift[kMostChunks];
   double scan[kSampleWaves];
-  PickShared pick;
   int bin, n, ok;
   unsigned long long last;
   double above;
@@ -691,11 +686,19 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     if (b > bin || (b == bin && (((uint64_t)order_key(z) << 32) | (uint32_t)~id) < last)) return 0.0;
     return weight.of(z);
   };
-  const Piece<T> p(row, c);
-  const int token = pick_in_chunk(s.pick, p, share, set.u * total - before);
-  if (tid == 0) {
+  const Piece<T> p(row, part_of(c));
+  double part = 0.0, in_front, weighs;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) part += share(p.z[i], p.id(i));
+  part = wave_sum(part);
+  if (lane == 0) s.scan[wv] = part;
+  __syncthreads();
+  const int picked = pick_lane(lane < kSampleWaves ? s.scan[lane] : 0.0, set.u * total - before, in_front);
+  if (wv != picked) return true;
+  const int token = pick_in_part(p, share, set.u * total - before - in_front, weighs);
+  if (lane == 0) {
     a.tokens[r] = token;
-    if (a.logprobs) a.logprobs[r] = (float)log(weight.of(row.value(token)) / total);
+    if (a.logprobs) a.logprobs[r] = (float)log(weighs / total);
   }
   return true;
 }
@@ -929,38 +932,17 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
     chunk = pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set.u, before, all);
   }
   if (!set.filters(a.vocab)) {
-    if (tid >= 64) return;   // one wave reads on: the segment, and the logit
+    if (tid >= 64) return;   // one wave reads on: the part of the chunk, and its logits
     const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
-    const int64_t at = r * w.chunks + chunk;
     const double scale = weight(info[chunk].top);
-    double target = set.u * all - before, in_front;
-    const int seg = pick_lane(w.segment[at * kMostSegments + lane] * scale, target, in_front);
-    target -= in_front;
-    constexpr int kVec = Piece<T>::kVec;
-    const int first = chunk * kChunk +
-                      (seg / kSampleWaves * kSampleThreads + seg % kSampleWaves * 64 + lane) * kVec;
-    double own[kVec], sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int id = first + i;
-      own[i] = id >= 0 && id < a.vocab ? weight.of(row.value(id)) : 0.0;
-      sum += own[i];
-    }
-    const int l = pick_lane(sum, target, in_front);
-    if (lane == l) {
-      target -= in_front;
-      double run = 0.0, share = 0.0;
-      int found = -1, last = 0;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        run += own[i];
-        if (own[i] > 0.0 && found < 0) {   // up to the one that exceeds it, else the last one
-          last = first + i;
-          share = own[i];
-          if (run > target) found = last;
-        }
-      }
-      a.tokens[r] = last;
+    const double* parts = w.part + (r * w.chunks + chunk) * kSampleWaves;
+    double in_front, share;
+    const int part = pick_lane(lane < kSampleWaves ? parts[lane] * scale : 0.0, set.u * all - before, in_front);
+    const Piece<T> p(row, chunk * kSampleWaves + part);
+    const int token =
+        pick_in_part(p, [&](float z, int) { return weight.of(z); }, set.u * all - before - in_front, share);
+    if (lane == 0) {
+      a.tokens[r] = token;
       if (a.logprobs) a.logprobs[r] = (float)log(share / all);
     }
     return;
@@ -1084,8 +1066,8 @@ size_t workspace_parts(int64_t rows, int64_t vocab, SampleWork& w, char* base) {
   const size_t n = (size_t)rows * w.chunks;
   w.list = reinterpret_cast<uint64_t*>(base);
   w.info = reinterpret_cast<ChunkInfo*>(w.list + n * list_most(vocab));
-  w.segment = reinterpret_cast<double*>(w.info + n);
-  w.mass = reinterpret_cast<unsigned long long*>(w.segment + n * kMostSegments);
+  w.part = reinterpret_cast<double*>(w.info + n);
+  w.mass = reinterpret_cast<unsigned long long*>(w.part + n * kSampleWaves);
   const size_t bins = vocab > kSmallVocab ? n * kFine : 0;
   w.count = reinterpret_cast<uint16_t*>(w.mass + bins);
   w.todo = reinterpret_cast<int32_t*>(w.count + bins);
