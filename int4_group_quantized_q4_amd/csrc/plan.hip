@@ -10,10 +10,14 @@
 // given, and one scan gives the stack and row offsets.
 //
 // Bound by latency: one workgroup, a thread a sequence, as the stack's end and
-// the scans are common to all.
+// the scans are common to all.  A lane writes its sequence's few pages and rows
+// itself; more than that are written by the lanes of its wave together, one
+// sequence after another (with all sequences taken that way, 64 of one row took 29 us).
+// Many rows are left to a second kernel.
 
 #include "common.h"
 #include "serving.h"
+#include "wave.h"
 
 namespace w4 {
 
@@ -21,27 +25,34 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kAtOnce = 8;             // pages that a lane moves at once
+constexpr int kFew = 2;                // pages or rows that a lane writes for its own sequence
+constexpr int kRowsHere = 4096;        // up to as many rows are written by the planning workgroup
+constexpr int kRowThreads = 256;
 
-// Inclusive sums of v over the workgroup; total: that of all threads.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_t& total) {
+// Inclusive sums of v and w over the workgroup, and their totals.
+__device__ __forceinline__ void block_scan(int64_t& v, int64_t& w, int64_t (*s_wave)[2], int64_t& v_total,
+                                           int64_t& w_total) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const int64_t w = __shfl_up((long long)v, o, 64);
-    if (lane >= o) v += w;
-  }
+  v = wave_scan(v);
+  w = wave_scan(w);
   __syncthreads();   // s_wave of the scan before is read
-  if (lane == 63) s_wave[wv] = v;
-  __syncthreads();
-  int64_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) {
-    const int64_t s = s_wave[w];
-    if (w < wv) before += s;
-    total += s;
+  if (lane == 63) {
+    s_wave[wv][0] = v;
+    s_wave[wv][1] = w;
   }
-  return v + before;
+  __syncthreads();
+  v_total = w_total = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanWaves; ++i) {
+    const int64_t a = s_wave[i][0], b = s_wave[i][1];
+    if (i < wv) {
+      v += a;
+      w += b;
+    }
+    v_total += a;
+    w_total += b;
+  }
 }
 
 struct Seq {
@@ -69,10 +80,24 @@ __device__ __forceinline__ Seq load_seq(const PlanArgs& a, int i) {
   return s;
 }
 
+__device__ __forceinline__ void store_row(const PlanArgs& a, int64_t r, const int32_t* pages, int64_t p, int seq) {
+  a.slots[r] = ((int64_t)pages[p >> a.page_shift] << a.page_shift) + (p & (((int64_t)1 << a.page_shift) - 1));
+  a.positions[r] = (int32_t)p;
+  if (a.row_seqs) a.row_seqs[r] = seq;
+}
+
+__device__ __forceinline__ void store_pad(const PlanArgs& a, int64_t r) {
+  a.slots[r] = -1;
+  a.positions[r] = 0;
+  if (a.row_seqs) a.row_seqs[r] = -1;
+}
+
+template <bool ROWS>   // the rows too
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-  __shared__ int64_t s_wave[kPlanWaves];
+  __shared__ int64_t s_wave[kPlanWaves][2];
   __shared__ unsigned long long s_cut, s_given, s_bad, s_short;
   const int tid = threadIdx.x, lane = tid & 63;
+  const Seq first = load_seq(a, tid);
   int64_t held = a.free_count[0];
   held = held < 0 ? 0 : held > a.capacity ? a.capacity : held;
   if (tid == 0) {
@@ -86,17 +111,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   // pages of ended sequences onto the stack
   int64_t back = 0;
   for (int i0 = 0; i0 < a.seqs; i0 += kPlanThreads) {
-    const Seq s = load_seq(a, i0 + tid);
+    const Seq s = i0 == 0 ? first : load_seq(a, i0 + tid);
     const int64_t mine = s.ended ? s.have : 0;
-    int64_t total;
-    const int64_t at = held + back + block_scan(mine, s_wave, total) - mine;
+    if (!__syncthreads_or(mine > 0)) continue;
+    int64_t upto = mine, total, none = 0, none_total;
+    block_scan(upto, none, s_wave, total, none_total);
+    const int64_t at = held + back + upto - mine;
     back += total;
     for (uint64_t todo = __ballot(mine > 0); todo; todo &= todo - 1) {
       const int l = __builtin_ctzll(todo);
-      const int64_t n = __shfl((long long)mine, l, 64), to = __shfl((long long)at, l, 64);
+      const int64_t n = lane_value(mine, l), to = lane_value(at, l);
       const int32_t* from = a.table + (int64_t)(i0 + tid - lane + l) * a.width;
-      for (int64_t c = lane; c < n; c += 64)
-        if (to + c < a.capacity) a.free_pages[to + c] = from[c];
+      for (int64_t c0 = lane; c0 < n; c0 += 64 * kAtOnce) {   // the loads of a round together
+        int32_t page[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) page[j] = from[min(c0 + 64 * j, n - 1)];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (c0 + 64 * j < n && to + c0 + 64 * j < a.capacity) a.free_pages[to + c0 + 64 * j] = page[j];
+      }
     }
   }
   const int64_t lost = held + back > a.capacity ? held + back - a.capacity : 0;
@@ -106,56 +139,55 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   int64_t pages = 0, rows = 0;   // asked by the sequences before
   for (int i0 = 0; i0 < a.seqs; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const Seq s = load_seq(a, i);
-    int64_t total_pages, total_rows;
-    const int64_t upto = pages + block_scan(s.want, s_wave, total_pages);
-    const int64_t row_end = rows + block_scan(s.fresh, s_wave, total_rows);
+    const Seq s = i0 == 0 ? first : load_seq(a, i);
+    int64_t upto = s.want, row_end = s.fresh, total_pages, total_rows;
+    block_scan(upto, row_end, s_wave, total_pages, total_rows);
+    upto += pages;
+    row_end += rows;
     const bool fits = i < a.seqs && upto <= top && row_end <= a.max_rows;
     pages += total_pages;
     rows += total_rows;
-    if (fits) {
+    // the last sequence that fits has the largest sums
+    const uint64_t fit = __ballot(fits);
+    if (fit && lane == 63 - __builtin_clzll(fit)) {
       atomicMax(&s_cut, (unsigned long long)row_end);
       atomicMax(&s_given, (unsigned long long)upto);
     }
-    if (s.bad) atomicAdd(&s_bad, 1ull);
-    if (i < a.seqs && !fits && s.fresh > 0) atomicAdd(&s_short, 1ull);
-    __syncthreads();
+    const uint64_t bad = __ballot(s.bad), lacks = __ballot(i < a.seqs && !fits && s.fresh > 0);
+    if (lane == 0 && bad) atomicAdd(&s_bad, (unsigned long long)__builtin_popcountll(bad));
+    if (lane == 0 && lacks) atomicAdd(&s_short, (unsigned long long)__builtin_popcountll(lacks));
+    // new columns of the table
+    int32_t* table = a.table + (int64_t)i * a.width;
+    const int64_t from = top - 1 - (upto - s.want);
+    if (fits && s.want <= kFew)
+      for (int64_t c = 0; c < s.want; ++c) table[s.have + c] = a.free_pages[from - c];
+    for (uint64_t todo = __ballot(fits && s.want > kFew); todo; todo &= todo - 1) {
+      const int l = __builtin_ctzll(todo);
+      const int64_t n = lane_value(s.want, l), top_l = lane_value(from, l);
+      int32_t* to = a.table + (int64_t)(i0 + tid - lane + l) * a.width + lane_value(s.have, l);
+      for (int64_t c = lane; c < n; c += 64) to[c] = a.free_pages[top_l - c];
+    }
+    __syncthreads();   // the cut; the columns are read by other lanes
     const int64_t cut = (int64_t)s_cut;
     if (i < a.seqs) {
       a.offsets[i + 1] = (int32_t)(fits ? row_end : cut);
       a.lens_out[i] = (int32_t)(s.ended ? 0 : fits ? s.len + s.fresh : s.len);
     }
-    // new columns of the table, then the rows: a sequence's by the lanes of its wave
-    const int64_t first = top - 1 - (upto - s.want);
-    for (uint64_t todo = __ballot(fits && s.want > 0); todo; todo &= todo - 1) {
-      const int l = __builtin_ctzll(todo);
-      const int64_t n = __shfl((long long)s.want, l, 64), from = __shfl((long long)first, l, 64);
-      int32_t* to = a.table + (int64_t)(i0 + tid - lane + l) * a.width + __shfl((long long)s.have, l, 64);
-      for (int64_t c = lane; c < n; c += 64) to[c] = a.free_pages[from - c];
-    }
-    __syncthreads();   // the columns are read by other lanes
-    for (uint64_t todo = __ballot(fits && s.fresh > 0); todo; todo &= todo - 1) {
-      const int l = __builtin_ctzll(todo);
-      const int seq = i0 + tid - lane + l;
-      const int64_t n = __shfl((long long)s.fresh, l, 64), len = __shfl((long long)s.len, l, 64);
-      const int64_t to = __shfl((long long)(row_end - s.fresh), l, 64);
-      const int32_t* row = a.table + (int64_t)seq * a.width;
-      for (int64_t c = lane; c < n; c += 64) {
-        const int64_t p = len + c;
-        a.slots[to + c] = ((int64_t)row[p >> a.page_shift] << a.page_shift) + (p & (((int64_t)1 << a.page_shift) - 1));
-        a.positions[to + c] = (int32_t)p;
-        if (a.row_seqs) a.row_seqs[to + c] = seq;
+    if constexpr (ROWS) {
+      if (fits && s.fresh <= kFew)
+        for (int64_t c = 0; c < s.fresh; ++c) store_row(a, row_end - s.fresh + c, table, s.len + c, i);
+      for (uint64_t todo = __ballot(fits && s.fresh > kFew); todo; todo &= todo - 1) {
+        const int l = __builtin_ctzll(todo);
+        const int seq = i0 + tid - lane + l;
+        const int64_t n = lane_value(s.fresh, l), len = lane_value(s.len, l), to = lane_value(row_end, l) - n;
+        for (int64_t c = lane; c < n; c += 64) store_row(a, to + c, a.table + (int64_t)seq * a.width, len + c, seq);
       }
     }
   }
 
   __syncthreads();
-  const int64_t cut = (int64_t)s_cut;
-  for (int64_t r = cut + tid; r < a.max_rows; r += kPlanThreads) {
-    a.slots[r] = -1;
-    a.positions[r] = 0;
-    if (a.row_seqs) a.row_seqs[r] = -1;
-  }
+  if constexpr (ROWS)
+    for (int64_t r = (int64_t)s_cut + tid; r < a.max_rows; r += kPlanThreads) store_pad(a, r);
   if (tid == 0) {
     a.free_count_out[0] = (int32_t)(top - (int64_t)s_given);
     if (a.counters && s_bad + lost) atomicAdd(a.counters, s_bad + (unsigned long long)lost);
@@ -163,10 +195,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   }
 }
 
+// A row a thread, from what plan_kernel left.
+__global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(PlanArgs a) {
+  const int64_t r = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (r >= a.max_rows) return;
+  if (a.seqs == 0 || r >= a.offsets[a.seqs]) {
+    store_pad(a, r);
+    return;
+  }
+  int lo = 0, hi = a.seqs;   // the last sequence that starts at r or before: those without rows are passed over
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.offsets[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  store_row(a, r, a.table + (int64_t)lo * a.width, (int64_t)a.lens_out[lo] - (a.offsets[lo + 1] - r), lo);
+}
+
 }  // namespace
 
 void launch_plan(const PlanArgs& a, hipStream_t stream) {
-  plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  if (a.max_rows <= kRowsHere) {
+    plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
+    return;
+  }
+  plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
+  plan_rows_kernel<<<(unsigned)((a.max_rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, stream>>>(a);
 }
 
 }  // namespace w4

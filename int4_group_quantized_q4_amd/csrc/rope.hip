@@ -8,9 +8,11 @@
 // angle within an eighth of a turn that is good to its last bit, and the quarters
 // swap and negate them.
 //
-// Bound by memory for many rows: every element is read and written once.  The
-// angles of a row are common to its heads: a workgroup takes whole rows (or a
-// part of one) and computes each angle once, into LDS.
+// Bound by memory for many rows: every element is read and written once (8191 rows
+// of 20 heads of 256, half of each turned: 26.8 us, 6.3 TB/s), by latency for few (a
+// row of 40 heads of 128 2.5 us, 64 rows 3.3).  The angles of a row are common to its
+// heads: a workgroup takes whole rows (or a part of one) and computes each angle once,
+// into LDS.
 
 #include "common.h"
 #include "serving.h"
@@ -20,13 +22,17 @@ namespace w4 {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnits = 1;      // 16 dimensions of a head each, of one thread
+// Units, 16 dimensions of a head each, of one thread: two share an angle's cost (8191
+// rows as above 26.8 us, 32.7 with one, 27.5 with four), one where that leaves CUs
+// without work (64 rows 3.5 against 3.9 us in a graph).
+constexpr int kFewUnits = 256 * kRopeThreads * 2;
 
 struct RopeTile {
   int32_t units, q_units;      // units in a row, and in its queries
   int32_t head_units, turned;  // units in a head, and those of its turned dimensions
   int32_t rows;                // rows a workgroup takes
   int32_t parts;               // workgroups a row takes (rows == 1)
+  int32_t per;                 // units a workgroup takes of a row (rows == 1)
 };
 
 __device__ __forceinline__ float2 cos_sin(int32_t position, float freq) {
@@ -56,8 +62,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, RopeTile
     s_turn[i] = {cs.x * a.scale, cs.y * a.scale};
   }
   __syncthreads();
-  const int first = part * kRopeThreads * kRopeUnits;
-  const int end = t.rows == 1 ? min(t.units, first + kRopeThreads * kRopeUnits) : rows * t.units;
+  const int first = part * t.per;
+  const int end = t.rows == 1 ? min(t.units, first + t.per) : rows * t.units;
   for (int i = first + threadIdx.x; i < end; i += kRopeThreads) {
     const int r = i / t.units;
     int u = i - r * t.units;
@@ -108,9 +114,9 @@ void launch_rope(const RopeArgs& a, bool interleaved, hipStream_t stream) {
   t.turned = a.rotary / 16;
   t.q_units = a.q_heads * t.head_units;
   t.units = t.q_units + a.k_heads * t.head_units;
-  constexpr int kPer = kRopeThreads * kRopeUnits;
-  t.rows = t.units >= kPer ? 1 : min(16, kPer / t.units);
-  t.parts = t.rows == 1 ? (t.units + kPer - 1) / kPer : 1;
+  t.per = a.rows * t.units > kFewUnits ? 2 * kRopeThreads : kRopeThreads;
+  t.rows = t.units >= t.per ? 1 : min(16, t.per / t.units);
+  t.parts = t.rows == 1 ? (t.units + t.per - 1) / t.per : 1;
   const size_t lds = (size_t)t.rows * (a.rotary / 2) * sizeof(float2);
   // a launch holds fewer than 2^32 threads
   const int64_t slice = ((int64_t)1 << 23) / t.parts * t.rows;
