@@ -645,31 +645,38 @@ def w4a16_lora_workspace(rows, K, N, adapters, rank):
     return int(lib().w4a16_lora_workspace(rows, K, N, adapters, rank))
 
 
-def _row_matrix(t, name):
-    """Pointer and row stride of t [rows, width] bf16 whose rows are contiguous."""
+def _row_matrix(t, name, rows, width, device):
+    """Pointer and row stride (elements) of t [rows, width] bf16 whose rows are
+    contiguous; the rows themselves may be apart."""
+    if isinstance(t, torch.Tensor) and t.dtype in _BF16_LIKE and t.get_device() == device >= 0:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2 and stride[1] == 1 and stride[0] >= width == shape[1] and shape[0] == rows:
+            return t.data_ptr(), stride[0]
+    # the checks one by one, for their errors and the layouts of single rows and columns
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dim() != 2:
-        raise ValueError("%s must be [rows, width], got %s" % (name, tuple(t.shape)))
-    return _rows(t.unsqueeze(1), name, _BF16_LIKE)
+    if t.dim() != 2 or tuple(t.shape) != (rows, width):
+        raise ValueError("%s is %s, expected [%d, %d]" % (name, tuple(t.shape), rows, width))
+    p, step = _rows(t.unsqueeze(1), name, _BF16_LIKE)
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, expected device %d" % (name, t.device, device))
+    return p, step
 
 
 def w4a16_lora_add(x, adapter_ids, a, b, scaling, y, out, ws=None, stream=None):
     """out = bf16(y + scaling[i] (x a[i]^T) b[i]^T) for every row of x [rows, K],
     y and out [rows, N], i its adapter: a [adapters, rank, K], b [adapters, N,
     rank]."""
-    xp, xs = _row_matrix(x, "x")
-    yp, ys = _row_matrix(y, "y")
-    op, os_ = _row_matrix(out, "out")
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError("a and b must be [adapters, rank, K] and [adapters, N, rank]")
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x, a and b must be [rows, K], [adapters, rank, K] and [adapters, N, rank]")
     (rows, K), (adapters, rank, ak), (bn, N, br), d = x.shape, a.shape, b.shape, x.get_device()
-    if ak != K or bn != adapters or br != rank or y.shape != (rows, N) or out.shape != (rows, N):
-        raise ValueError("x %s, a %s, b %s, y %s and out %s do not fit together" % tuple(
-            tuple(t.shape) for t in (x, a, b, y, out)))
-    if y.get_device() != d or out.get_device() != d:
-        raise ValueError("x, y and out must be on one device")
-    _on_device(x, "x")
+    if ak != K or bn != adapters or br != rank:
+        raise ValueError("x %s, a %s and b %s do not fit together" % (tuple(x.shape), tuple(a.shape), tuple(b.shape)))
+    xp, xs = _row_matrix(x, "x", rows, K, d)
+    yp, ys = _row_matrix(y, "y", rows, N, d)
+    op, os_ = _row_matrix(out, "out", rows, N, d)
+    if d < 0:
+        _on_device(x, "x")
     _call("w4a16_lora_add", d, stream, xp, xs, rows, K, _arg(adapter_ids, "adapter_ids", _I32, rows * 4, d, False),
           _arg(a, "a", _BF16_LIKE, 0, d, False), _arg(b, "b", _BF16_LIKE, 0, d, False),
           _arg(scaling, "scaling", _F32, adapters * 4, d), adapters, rank, N, yp, ys, op, os_,
