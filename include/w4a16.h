@@ -690,7 +690,8 @@ int kv_cache_attention(const uint16_t* q, int64_t seqs, int64_t q_stride, int32_
  *                   pages or rows
  * seq_lens_out may be seq_lens and free_count_out may be free_count.  With other
  * memory for both, a step can be planned again from the same state.  Page ids are
- * passed on as they are.  Every other overlap of an output with another argument
+ * passed on as they are: a page that several ended sequences hold comes back once for
+ * each of them.  Every other overlap of an output with another argument
  * is W4_ERR_ARG.  int32 arrays 4-byte, slots 8-byte aligned.
  * Requires seqs <= 65535, page_size a power of two from 16 to 65536, table_width
  * * page_size < 2^31, capacity < 2^31, max_rows <= 2^26.
@@ -745,7 +746,8 @@ int w4a16_rope(const uint16_t* q, int64_t q_stride, int32_t q_heads, const uint1
  *   ws           w4a16_lora_workspace(...) bytes, 16-byte aligned; its contents do not
  *                matter.  Calls that overlap in time need one each.
  * Strides are multiples of 8 and at least the row's width.  Rows do not depend on
- * one another: NaN and infinities of one leave the others as they are.
+ * one another: NaN and infinities of one leave the others as they are.  Where b holds
+ * an infinity the sum is not finite, or a NaN.
  * Requires K % 32 == 0, K >= 32, N % 16 == 0, rank % 8 == 0, 8 <= rank <= 256, K and N <=
  * 2^20, adapters <= 4096, rows <= 2^20, rows * stride <= 2^48.
  */
@@ -780,7 +782,8 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
  *                matter.  Calls that overlap in time need one each.
  * Weights and sums are 64-bit, so that a draw next to a border between two tokens falls
- * on its side of it.  A logit of -infinity is never drawn; beside logits of +infinity no
+ * on its side of it; where top_p keeps so many tokens that their weights are summed in
+ * bins, each enters as a multiple of 2^-43 of the largest one.  A logit of -infinity is never drawn; beside logits of +infinity no
  * other is.  A row with a NaN, and one without a logit above -infinity: token -1, log
  * probability NaN.
  * int32 and fp32 arrays 4-byte aligned.  No output may overlap another argument

@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
             const bf16x8 h = __builtin_bit_cast(bf16x8, s_terms[(g * steps + s) * 64 + lane]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint16_t* b = bs + (int64_t)min(nb + 32 * (i / 2) + 8 * (m / 4) + 4 * (i % 2) + m % 4, l.N - 1) * l.rank;
-              const bf16x8 v = *reinterpret_cast<const bf16x8*>(b + 8 * ch);
+              const int n = min(nb + 32 * (i / 2) + 8 * (m / 4) + 4 * (i % 2) + m % 4, l.N - 1);
+              const bf16x8 v = *reinterpret_cast<const bf16x8*>(bs + (int64_t)n * l.rank + 8 * ch);
               acc[i] = mfma16x16x32(none ? bf16x8{} : v, h, acc[i]);
             }
           }

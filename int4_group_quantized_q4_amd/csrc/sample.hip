@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   }
   const Weight weight = set.weight(top);
   const float ref = weight.steps(weight.m);
-  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 && __builtin_fabsf(ref) < 0x1p22f;
+  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 &&
+                    __builtin_fabsf(ref) < 0x1p22f;
   double sum = 0.0;
   if (top >= kPosInfKey) {
 #pragma unroll
@@ -441,7 +442,8 @@ __device__ __forceinline__ uint64_t exchange(uint64_t v, int step, bool larger) 
                          : step == 2 ? dpp_u64<0x4E>(v)                   // quad_perm [2,3,0,1]
                          : step == 4 ? dpp_u64<0x1B>(dpp_u64<0x141>(v))   // half rows and quads mirrored
                          : step == 8 ? dpp_u64<0x128>(v)                  // row_ror 8
-                                     : ((uint64_t)across_u32((uint32_t)(v >> 32), step) << 32) | across_u32((uint32_t)v, step);
+                                     : ((uint64_t)across_u32((uint32_t)(v >> 32), step) << 32) |
+                                           across_u32((uint32_t)v, step);
   return (v > other) == larger ? v : other;
 }
 __device__ __forceinline__ uint64_t wave_merge(uint64_t v, bool descending) {
@@ -847,8 +849,8 @@ __device__ uint32_t radix_select(RadixShared& s, const R& row, const F& amount, 
 
 // For rows whose histograms do not say: many ties, infinities, extreme temperatures.
 template <typename T>
-__device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, const Row<T>& row, int64_t r, const Settings& set,
-                          const Weight& weight) {
+__device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, const Row<T>& row, int64_t r,
+                                          const Settings& set, const Weight& weight) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   // kept: keys above t, and ids up to `upto` at t
   uint32_t t = 0;

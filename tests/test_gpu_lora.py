@@ -188,3 +188,46 @@ def test_graph_replays_with_other_ids(rows):
         want = w4.lora_add(x, ids, a, b, scaling, y)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows", [64, 200, 700])
+@pytest.mark.parametrize("rank", [16, 64])
+def test_a_row_does_not_depend_on_its_place(rows, rank):
+    """In calls of the same size a row's result is the same bit for bit, whatever adapters the others have and wherever
+    the row stands; and so it is from run to run."""
+    rng = np.random.default_rng(rows + rank)
+    K, N, n = 1024, 320, 5
+    x, a, b, y = rnd(rng, rows, K), rnd(rng, n, rank, K), rnd(rng, n, N, rank), rnd(rng, rows, N)
+    ad, bd = bf16_dev(a), bf16_dev(b)
+    ids = rng.integers(0, n, rows)
+    first = bits_host(w4.lora_add(bf16_dev(x), i32(ids), ad, bd, None, bf16_dev(y)))
+    torch.cuda.synchronize()
+    again = bits_host(w4.lora_add(bf16_dev(x), i32(ids), ad, bd, None, bf16_dev(y)))
+    assert np.array_equal(first, again)
+    order = rng.permutation(rows)
+    moved = bits_host(w4.lora_add(bf16_dev(x[order]), i32(ids[order]), ad, bd, None, bf16_dev(y[order])))
+    assert np.array_equal(moved, first[order])
+    other = np.where(np.arange(rows) % 3 == 0, ids, rng.integers(-1, n, rows))
+    mixed = bits_host(w4.lora_add(bf16_dev(x), i32(other), ad, bd, None, bf16_dev(y)))
+    assert np.array_equal(mixed[::3], first[::3])
+
+
+def test_two_streams_at_once():
+    """Calls that overlap in time, each with a workspace of its own, as they are one after another."""
+    rng = np.random.default_rng(3)
+    K, N, n, rank = 2048, 2048, 6, 32
+    a, b = bf16_dev(rnd(rng, n, rank, K)), bf16_dev(rnd(rng, n, N, rank))
+    sets = []
+    for rows in (600, 40):
+        x, y, ids = bf16_dev(rnd(rng, rows, K)), bf16_dev(rnd(rng, rows, N)), i32(rng.integers(-1, n, rows))
+        ws = torch.empty(w4.w4a16_lora_workspace(rows, K, N, n, rank), dtype=torch.uint8, device=dev())
+        want = w4.lora_add(x, ids, a, b, None, y)
+        sets.append((x, ids, y, torch.zeros_like(y), ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, ids, y, out, ws, _, s in sets:
+            with torch.cuda.stream(s):
+                w4.w4a16_lora_add(x, ids, a, b, None, y, out, ws)
+    torch.cuda.synchronize()
+    for *_, out, _, want, _ in sets:
+        assert torch.equal(out, want)

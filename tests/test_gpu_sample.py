@@ -193,3 +193,72 @@ def test_graph_replays(rows, V):
         want, wlp = w4.sample(z, u, None, k, p)
         torch.cuda.synchronize()
         assert torch.equal(tokens, want) and torch.equal(lp, wlp)
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 7, 8, 9, 15, 17, 1023, 1025, 2048, 2049, 2060, 4500, 16384, 16385, 17000,
+                               32768])
+def test_vocabularies_around_the_pieces(V):
+    rng = np.random.default_rng(V)
+    for dtype in ("f32", "bf16"):
+        z = logits(rng, 12, V, dtype, sigma=1.0, peak=6.0)
+        u = rng.random(12).astype(np.float32)
+        run(z, uniform=u, dtype=dtype, stride=1)
+        run(z, top_k=rng.integers(1, V + 2, 12), uniform=u, dtype=dtype, stride=3)
+        run(z, top_p=rng.uniform(0, 1, 12).astype(np.float32), uniform=u, dtype=dtype, stride=7)
+        run(z, min_p=np.exp(rng.uniform(-8, 0, 12)).astype(np.float32), uniform=u, dtype=dtype)
+
+
+@pytest.mark.parametrize("where", ["spread", "together"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cuts_of_every_length(where, dtype):
+    """top_k, top_p and min_p that keep from one token to most of them, the likely ones spread over the vocabulary or
+    next to one another: whichever way the row is cut."""
+    rng = np.random.default_rng(7)
+    V, n = 40000, 24
+    z = logits(rng, n, V, dtype, sigma=1.5, peak=10.0)
+    if where == "together":
+        z = np.sort(z, axis=1)[:, ::-1].copy()
+        z = np.concatenate([z[:, 300:20300], z[:, :300], z[:, 20300:]], 1)
+    u = rng.random(n).astype(np.float32)
+    ks = [1, 2, 16, 17, 50, 63, 64, 65, 66, 100, 191, 192, 193, 256, 500, 1000, 1500, 2000, 2048, 2049, 5000, 20000,
+          39999, 40000]
+    ps = 1 - np.exp(np.linspace(np.log(0.9), np.log(1e-7), n))
+    ms = np.exp(np.linspace(-0.01, -20, n))
+    run(z, top_k=ks, uniform=u, dtype=dtype)
+    run(z, top_p=ps.astype(np.float32), uniform=u, dtype=dtype)
+    run(z, min_p=ms.astype(np.float32), uniform=u, dtype=dtype)
+    run(z, 1.7, ks, ps[::-1].astype(np.float32), None, u, dtype)
+    run(z, 0.6, ks[::-1], ps.astype(np.float32), ms.astype(np.float32), u, dtype)
+    run(z, 2.5, None, ps.astype(np.float32), ms[::-1].astype(np.float32), u, dtype)
+
+
+def test_masked_beside_filters():
+    """Most of the vocabulary at -infinity, or at the type's lowest value: fewer logits than top_k, chunks without any."""
+    rng = np.random.default_rng(8)
+    V = 70000
+    z = logits(rng, 9, V, "f32")
+    for i, share in enumerate([0.5, 0.9, 0.99, 0.999, 0.9999, 0.99999]):
+        z[i, rng.random(V) < share] = -np.inf
+        z[i, 69999 - i] = 1.0
+    z[6, 16384:] = -np.inf
+    z[7, :65536] = -np.inf
+    z[8, 100:] = -np.finfo(np.float32).max
+    u = rng.random(9).astype(np.float32)
+    for kw in (dict(), dict(top_k=50), dict(top_k=1000), dict(top_p=0.95), dict(top_p=0.9999, temperature=2.0),
+               dict(min_p=0.001), dict(top_k=3000, top_p=0.99, min_p=1e-6)):
+        run(z, uniform=u, **kw)
+
+
+def test_the_same_from_run_to_run():
+    """Sums do not depend on the order in which workgroups and atomics finish: tokens and log probabilities are equal
+    bit for bit, in rows cut in every way."""
+    rng = np.random.default_rng(9)
+    z = torch.tensor(logits(rng, 40, 60000, "f32", sigma=1.5, peak=9.0), dtype=torch.float32, device=dev())
+    pick = lambda values, t: torch.tensor(rng.choice(values, 40), dtype=t, device=dev())
+    k, p = pick([0, 0, 40, 70, 1000, 9000], torch.int32), pick([1.0, 0.9, 0.99, 0.9999], torch.float32)
+    m, u = pick([0.0, 0.0, 1e-3], torch.float32), torch.rand(40, device=dev())
+    tokens, lp = w4.sample(z, u, None, k, p, m)
+    for _ in range(5):
+        again, lp2 = w4.sample(z, u, None, k, p, m)
+        torch.cuda.synchronize()
+        assert torch.equal(tokens, again) and torch.equal(lp, lp2)
