@@ -776,7 +776,8 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *   top_p        in, nullable (off)  [rows] fp32; off at 1 and above and for a NaN
  *   min_p        in, nullable (off)  [rows] fp32; off at 0 and below and for a NaN, above
  *                1 as 1
- *   uniforms     in  [rows] fp32 in [0, 1); others are cut to [0, 1], a NaN is 0
+ *   uniforms     in  [rows] fp32 in [0, 1); others are cut to [0, 1], a NaN is 0; 1 draws the
+ *                last kept token of positive weight
  *   tokens       out [rows] int32
  *   logprobs     out, nullable  [rows] fp32: log of the token's share of the kept weights
  *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not

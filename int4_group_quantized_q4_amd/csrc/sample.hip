@@ -8,20 +8,30 @@
 //         the rank-th largest of the maxima of 256 groups, cut to its leading bits;
 //   draw  a workgroup a row.  All of the row's logits from the largest of the chunks'
 //         bounds up are among the candidates: where that piece of the order decides
-//         the filters, it is sorted, cut, and the draw is made among what is left,
-//         in the order of the ids.  A row without filters needs no candidates, only
-//         the 1024 logits in which the sums pass the number.
-// Where that piece may be too short (a nucleus of thousands of tokens) the scan also
-// leaves a histogram of weights (and counts) over bins of a sixteenth of an octave,
-// and a third kernel (rest) takes the rows that the second left: the histogram tells
-// the bin of the last kept logit; the row is read again for the logits of that bin,
-// and they are sorted.  Where the bin holds too many (ties), a radix select over the
-// logits' order keys takes the histogram's place.
+//         the filters, it is cut, and the draw is made among what is left, in the
+//         order of the ids.  Cuts and draw look for a place at which a running sum
+//         reaches a border; the candidates are summed by 2048 bins of the order, and
+//         only those of the bin with the border are compared (sorted are they where
+//         that bin has more than 256: ties).  A row without filters needs no
+//         candidates, only the 1024 logits in which the sums pass the number.
+// Where that piece may be too short (a nucleus of thousands of tokens) a third kernel
+// (rest) takes the row: several workgroups make histograms of its chunks' weights
+// (and counts) over bins of a sixteenth of an octave, and the last one finds in them
+// the bin of the last kept logit, reads the row again for that bin's logits, and sorts
+// them.  Where the bin holds too many (ties), a radix select over the logits' order
+// keys takes the histogram's place.
+//
+// Rows of 131072 fp32 logits, 54 to 64 of them, in us for the kernels: without filters
+// scan 11.4 (of which the 64-bit series take half: greedy rows 5.0), draw 5.6; top_k 50
+// and top_p 0.95 9.0 and 10.8; top_k 1000 9.3 and 13.7 (28.3 with all candidates
+// sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 71,
+// with 54 such rows 87.  (With the histograms made by every scan it took 61 for those,
+// but the scan 19 to 36 for all rows with a long filter.)  256 rows without filters:
+// 39 and 5.3, 3.4 TB/s, bound by the series' instructions.
 //
 // The second kernel's time is that of fetching its code as much as of running it (a
-// workgroup passes through it once), so it is kept short: one loop for its two sorts.
-// With the third kernel's code called from it, it took 8 us more, for a stack that
-// no row used.
+// workgroup passes through it once).  With the third kernel's code called from it, it
+// took 8 us more, for a stack that no row used.
 //
 // Weights are 2^((z - m) log2 e / T) in 64 bits.  Where they are added by atomics
 // (the histograms) they are whole multiples of 2^-43 of the largest one, so that the
@@ -45,8 +55,13 @@ constexpr int kGroups = 256;                           // of 4 threads each
 constexpr int kRankSure = 64, kRankMost = 224;
 constexpr int kListMost = 768;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
+constexpr int kBinMost = 256;                          // candidates of a bin that are compared with one another
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
+// Workgroups of the third kernel, up to one a chunk: each ends with a fence that writes its XCD's L2 back, so more of
+// them cost as well (54 rows that need it 150 us with 512, 87 with 256, 91 with 128, 109 with one a row; one row of 52
+// 65, 71, 81, 102).
+constexpr int kRestGroups = 256;
 constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
 
@@ -128,6 +143,8 @@ struct Settings {
   double u;
   __device__ __forceinline__ bool greedy() const { return temperature == 0.f; }
   __device__ __forceinline__ bool filters(int n) const { return k < n || p < 1.0 || few > 0.0; }
+  // what a running sum has to exceed; a number of 1 takes the last kept token, however little it weighs
+  __device__ __forceinline__ double target(double total) const { return u < 1.0 ? u * total : INFINITY; }
   // rows that need the sum of all weights, candidates, a histogram
   __device__ __forceinline__ bool sums(int n) const { return !greedy() && k >= n && (p < 1.0 || few == 0.0); }
   __device__ __forceinline__ bool lists(int n) const { return !greedy() && filters(n); }
@@ -219,7 +236,6 @@ __device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, const 
 
 struct ChunkInfo {
   double sum;        // of the weights beside top
-  float ref;         // top in sixteenths of an octave, whole ones: the first bin; NaN: no histogram
   uint32_t top;      // largest key; 0: no logit above -infinity
   int32_t arg;       // the lowest id that has it
   uint32_t bound;    // every logit from this key up is in the list
@@ -232,7 +248,7 @@ __host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSm
 struct SampleWork {
   ChunkInfo* info;             // [rows][chunks]
   double* part;                // [rows][chunks][kSampleWaves]: the waves' sums, beside the chunk's top
-  int32_t* todo;               // [rows]: left to the third kernel
+  int32_t *todo, *done;        // [rows]: left to the third kernel; its workgroups that have made their histograms
   uint64_t* list;              // [rows][chunks][list_most]: key << 32 | ~id
   unsigned long long* mass;    // [rows][chunks][kFine]
   uint16_t* count;             // [rows][chunks][kFine]
@@ -247,8 +263,6 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   __shared__ double s_sum[kSampleWaves];
   __shared__ uint32_t s_group[kGroups];
   __shared__ uint32_t s_bound;
-  __shared__ unsigned long long s_mass[kFine];
-  __shared__ uint32_t s_count[kFine];
   const int64_t r = blockIdx.y, at = r * w.chunks + blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
@@ -267,8 +281,6 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
     s_n = 0;
     s_bound = kLowestKey;
   }
-  s_mass[tid] = 0;
-  s_count[tid] = 0;
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < kSampleWaves; ++v) top = max(top, s_top[v]);
@@ -302,30 +314,10 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
     if (lane == 0) s_bound = max(bound, kLowestKey);
   }
   const Weight weight = set.weight(top);
-  const float ref = weight.steps(weight.m);
-  const bool bins = set.bins(a.vocab) && top > 0 && top < kPosInfKey && weight.per > 0.0 &&
-                    __builtin_fabsf(ref) < 0x1p22f;
   double sum = 0.0;
   if (top >= kPosInfKey) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += piece.z[i] == INFINITY ? 1.0 : 0.0;
-  } else if (bins) {
-    const bool counts = set.k < a.vocab;
-#pragma unroll
-    for (int i = 0; i < kPer; i += 4) {   // four series together share their coefficients
-      double e[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = exp2_f64(((double)piece.z[i + j] - weight.top) * weight.per);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum += e[j];
-        const int b = (int)fminf(ref - weight.steps(piece.z[i + j]), (float)(kFine - 1));
-        const unsigned long long fixed = fixed_of(e[j]);
-        if (fixed > 0) atomicAdd(&s_mass[b], fixed);
-        if (counts && piece.z[i + j] > -INFINITY) atomicAdd(&s_count[b], 1u);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
   } else if (sums && top > 0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -338,26 +330,31 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   if (lane == 0) s_sum[wv] = sum;
   __syncthreads();
   const uint32_t bound = s_bound;
-  if (lists && mine >= bound) {
-    uint64_t* list = w.list + at * list_most(a.vocab);
+  if (lists && __ballot(mine >= bound)) {
     const float z = key_value(bound);
+    uint32_t reach = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) reach |= piece.z[i] >= z ? 1u << i : 0u;
+    const int own_n = __builtin_popcount(reach);
+    const int upto = (int)wave_scan((int64_t)own_n);
+    int at_list = 0;
+    if (lane == 63) at_list = atomicAdd(&s_n, upto);
+    at_list = __builtin_amdgcn_readlane(at_list, 63) + upto - own_n;
+    uint64_t* list = w.list + at * list_most(a.vocab);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (piece.z[i] >= z) {
-        const int n = atomicAdd(&s_n, 1);
-        if (n < list_most(a.vocab)) list[n] = ((uint64_t)order_key(piece.z[i]) << 32) | (uint32_t)~piece.id(i);
+      if (reach >> i & 1) {
+        if (at_list < list_most(a.vocab))
+          list[at_list] = ((uint64_t)order_key(piece.z[i]) << 32) | (uint32_t)~piece.id(i);
+        ++at_list;
       }
-  }
-  if (bins) {
-    w.mass[at * kFine + tid] = s_mass[tid];
-    if (set.k < a.vocab) w.count[at * kFine + tid] = (uint16_t)s_count[tid];
   }
   __syncthreads();
   if (wv == 0) {
     const double part = lane < kSampleWaves ? s_sum[lane] : 0.0;
     sum = wave_sum(part);
     if (sums && lane < kSampleWaves) w.part[at * kSampleWaves + lane] = part;
-    if (lane == 0) w.info[at] = {sum, bins ? ref : __builtin_nanf(""), top, s_arg, bound, s_n};
+    if (lane == 0) w.info[at] = {sum, top, s_arg, bound, s_n};
   }
 }
 
@@ -372,10 +369,10 @@ __device__ __forceinline__ int pick_lane(double v, double target, double& before
   return pick;
 }
 
-// The same with a share of the whole sum for the target.
-__device__ __forceinline__ int pick_share(double v, double u, double& before, double& total) {
+// The same for the settings' share of the whole sum.
+__device__ __forceinline__ int pick_share(double v, const Settings& set, double& before, double& total) {
   total = lane_value(wave_scan(v), 63);
-  return pick_lane(v, u * total, before);
+  return pick_lane(v, set.target(total), before);
 }
 
 // The id of a wave's part at which the running sum of f(logit, id) exceeds target, in
@@ -513,12 +510,38 @@ __device__ __forceinline__ void running_sums(double& v0, double& v1, int N, doub
 __device__ __forceinline__ int power_of_two(int n) { return n <= 64 ? 64 : 1 << (32 - __builtin_clz(n - 1)); }
 
 // ------------------------------------------------------- a row by its histograms
+// The weights of a chunk's logits (and their number) by bins, beside its largest one.
+// The last bin takes all the lower ones and is not used.
+template <typename T>
+__device__ __forceinline__ void add_to_bins(const Piece<T>& piece, const Weight& weight, unsigned long long* s_mass,
+                                            uint32_t* s_count, bool counts) {
+  const float ref = weight.steps(weight.m);
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {   // four series together share their coefficients
+    double e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = exp2_f64(((double)piece.z[i + j] - weight.top) * weight.per);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = (int)fminf(ref - weight.steps(piece.z[i + j]), (float)(kFine - 1));
+      const unsigned long long fixed = fixed_of(e[j]);
+      if (fixed > 0 && b < kFine - 1) atomicAdd(&s_mass[b], fixed);
+      if (counts && b < kFine - 1) atomicAdd(&s_count[b], 1u);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+// Whether bins hold the row's weights.
+__device__ __forceinline__ bool has_bins(const Weight& weight) {
+  return weight.m < INFINITY && weight.per > 0.0 && __builtin_fabsf(weight.steps(weight.m)) < 0x1p22f;
+}
+
 struct WholeShared {
   uint64_t v[kSortMost];
   double scale[kMostChunks], sums[kMostChunks];
   int shift[kMostChunks];
   double scan[kSampleWaves];
-  int bin, n, ok;
+  int bin, n;
   unsigned long long last;
   double above;
 };
@@ -548,21 +571,16 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   const ChunkInfo* info = w.info + r * w.chunks;
   const unsigned long long* mass = w.mass + r * w.chunks * kFine;
   const uint16_t* count = w.count + r * w.chunks * kFine;
-  __syncthreads();
-  if (tid == 0) s.ok = 1;
-  __syncthreads();
+  const bool use_k = set.k < a.vocab, use_p = set.p < 1.0;
   if (tid < w.chunks) {
-    const ChunkInfo f = info[tid];
-    const float shift = ref - f.ref;
-    s.scale[tid] = f.top == 0 ? 0.0 : weight(f.top) * (1.0 / kFixed);
-    s.shift[tid] = f.top == 0 || !(shift < kFine) ? kFine : (int)shift;
-    if (f.top > 0 && f.ref != f.ref) s.ok = 0;
+    const uint32_t top = info[tid].top;
+    const float shift = ref - weight.steps(key_value(top));
+    s.scale[tid] = top == 0 ? 0.0 : weight(top) * (1.0 / kFixed);
+    s.shift[tid] = top == 0 || !(shift < kFine) ? kFine : (int)shift;
   }
   __syncthreads();
-  if (!s.ok) return false;
   const auto bin_of = [&](float z) { return (int)fminf(ref - weight.steps(z), (float)(kFine - 1)); };
   // the row's histograms, a bin a thread (the last bin is not used)
-  const bool use_k = set.k < a.vocab, use_p = set.p < 1.0;
   double row_mass = 0.0, row_count = 0.0;
   if (tid < kFine - 1)
     for (int c = 0; c < w.chunks; ++c) {
@@ -681,7 +699,7 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   }
   __syncthreads();
   double before, total;
-  const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set.u, before, total);
+  const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set, before, total);
   // kept: whole bins above, and in the bin up to the last one
   const auto share = [&](float z, int id) {
     const int b = bin_of(z);
@@ -695,9 +713,9 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   part = wave_sum(part);
   if (lane == 0) s.scan[wv] = part;
   __syncthreads();
-  const int picked = pick_lane(lane < kSampleWaves ? s.scan[lane] : 0.0, set.u * total - before, in_front);
+  const int picked = pick_lane(lane < kSampleWaves ? s.scan[lane] : 0.0, set.target(total) - before, in_front);
   if (wv != picked) return true;
-  const int token = pick_in_part(p, share, set.u * total - before - in_front, weighs);
+  const int token = pick_in_part(p, share, set.target(total) - before - in_front, weighs);
   if (lane == 0) {
     a.tokens[r] = token;
     if (a.logprobs) a.logprobs[r] = (float)log(weighs / total);
@@ -765,7 +783,7 @@ __device__ int find_id(RadixShared& s, const F& f, int lo, int hi, double share,
   double before, ignored;
   if (share >= 0) {
     pick_piece(s, f, lo, hi, piece, 0.0, before, total);
-    target = share * total;
+    target = share < 1.0 ? share * total : INFINITY;
   }
   int w = pick_piece(s, f, lo, hi, piece, target, before, total);
   target -= before;
@@ -901,12 +919,98 @@ __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, c
   }
 }
 
+// ------------------------------------------------- many candidates, not sorted
+// The candidates of a row by 2048 bins in the order asked for: the bins' sums tell
+// the bin in which the running sum reaches a border, and the candidates of that bin
+// are compared with one another.
+struct DrawShared {
+  uint64_t v[kSortMost];
+  unsigned long long bins[kSortMost];
+  uint64_t bin_v[kBinMost];
+  unsigned long long bin_x[kBinMost];
+  unsigned long long scan[kSampleWaves], above;
+  uint64_t last;
+  int bin, n;
+};
+
+// Two candidates a thread with order values v (descending; their bins b ascend) and
+// amounts x: the v of the first one at which the running sum of x is need(total) or
+// more; 0 if the sums do not reach that, or if a bin holds too many (need: 0).
+template <typename F>
+__device__ __forceinline__ uint64_t reach(DrawShared& s, const uint64_t (&v)[2], const int (&b)[2],
+                                          const unsigned long long (&x)[2], unsigned long long& total, const F& need_of) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  __syncthreads();   // what was read of the call before
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s.bins[tid + i * kSampleThreads] = 0;
+  if (tid == 0) {
+    s.n = 0;
+    s.last = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0) atomicAdd(&s.bins[b[i]], x[i]);
+  __syncthreads();
+  const unsigned long long first = s.bins[2 * tid], second = s.bins[2 * tid + 1];
+  unsigned long long upto = wave_scan(first + second);
+  if (lane == 63) s.scan[wv] = upto;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleWaves; ++i) {
+    const unsigned long long sum = s.scan[i];
+    if (i < wv) upto += sum;
+    total += sum;
+  }
+  const unsigned long long need = need_of(total);
+  if (need == 0) return 0;
+  const unsigned long long before = upto - first - second;
+  if (before < need && upto >= need) {
+    const bool in_first = before + first >= need;
+    s.bin = 2 * tid + (in_first ? 0 : 1);
+    s.above = in_first ? before : before + first;
+  }
+  __syncthreads();
+  const int bin = s.bin;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0 && b[i] == bin) {
+      const int at = atomicAdd(&s.n, 1);
+      if (at < kBinMost) {
+        s.bin_v[at] = v[i];
+        s.bin_x[at] = x[i];
+      }
+    }
+  __syncthreads();
+  const int n = s.n;
+  if (n > kBinMost) return 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0 && b[i] == bin) {
+      unsigned long long run = s.above;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) run += s.bin_v[j] >= v[i] ? s.bin_x[j] : 0;
+      if (run >= need && run - x[i] < need) s.last = v[i];
+    }
+  __syncthreads();
+  return s.last;
+}
+
+// A weight in multiples of 2^-52, none of a positive one: 2048 of at most 1 stay below 2^64.
+__device__ __forceinline__ unsigned long long finer_of(double w) {
+  const unsigned long long x = __builtin_bit_cast(unsigned long long, w + 1.0) -
+                               __builtin_bit_cast(unsigned long long, 1.0);
+  return w > 0.0 && x == 0 ? 1 : x;
+}
+
 // ------------------------------------------------------------------ the draw
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs a, SampleWork w) {
-  __shared__ uint64_t s_v[kSortMost];
+  __shared__ DrawShared s;
   __shared__ double s_sum[kSampleWaves];
   __shared__ int s_n, s_kept, s_token, s_cut;
+  uint64_t* const s_v = s.v;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const ChunkInfo* info = w.info + r * w.chunks;
@@ -916,7 +1020,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   if (lane < w.chunks) mine = info[lane];
   const uint32_t top = wave_max_of_quads(quad_max(mine.top));
   const uint32_t bound = wave_max_of_quads(quad_max(mine.bound));
-  if (tid == 0) w.todo[r] = 0;
+  if (tid == 0) w.todo[r] = w.done[r] = 0;
   if (top == kNanKey || top == 0 || set.greedy()) {
     // the lowest id that has it: that of the first chunk
     const int arg = __builtin_amdgcn_readlane(mine.arg, __builtin_ctzll(__ballot(mine.top == top)));
@@ -931,7 +1035,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   double all = 0.0, before = 0.0;   // of the whole row's weights
   int chunk = 0;
   if (set.sums(a.vocab)) {
-    chunk = pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set.u, before, all);
+    chunk = pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set, before, all);
   }
   if (!set.filters(a.vocab)) {
     if (tid >= 64) return;   // one wave reads on: the part of the chunk, and its logits
@@ -939,10 +1043,10 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
     const double scale = weight(info[chunk].top);
     const double* parts = w.part + (r * w.chunks + chunk) * kSampleWaves;
     double in_front, share;
-    const int part = pick_lane(lane < kSampleWaves ? parts[lane] * scale : 0.0, set.u * all - before, in_front);
+    const int part = pick_lane(lane < kSampleWaves ? parts[lane] * scale : 0.0, set.target(all) - before, in_front);
     const Piece<T> p(row, chunk * kSampleWaves + part);
     const int token =
-        pick_in_part(p, [&](float z, int) { return weight.of(z); }, set.u * all - before - in_front, share);
+        pick_in_part(p, [&](float z, int) { return weight.of(z); }, set.target(all) - before - in_front, share);
     if (lane == 0) {
       a.tokens[r] = token;
       if (a.logprobs) a.logprobs[r] = (float)log(share / all);
@@ -971,6 +1075,71 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
   const int n = s_n;
   const bool complete = bound == kLowestKey;   // every logit is a candidate
   bool ready = whole && n <= kSortMost && (set.k >= a.vocab || n >= set.k || complete);
+  if (ready) {
+    const uint64_t v[2] = {tid < n ? s_v[tid] : 0, tid + kSampleThreads < n ? s_v[tid + kSampleThreads] : 0};
+    // the bins of the values: from the largest one down to the bound, or (no bound) to weights of 2^-60
+    const float range = complete ? (float)(60.0 / weight.per) : weight.m - key_value(bound);
+    const float scale = (float)(kSortMost - 1) / range;
+    unsigned long long x[2], total;
+    double wt[2];
+    int b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t key = (uint32_t)(v[i] >> 32);
+      b[i] = (int)fminf((weight.m - key_value(key)) * scale, (float)(kSortMost - 1));
+      wt[i] = v[i] > 0 ? weight(key) : 0.0;
+      x[i] = v[i] > 0;
+    }
+    uint64_t last = 0;
+    bool found = true, reached = false;   // no bin held too many; top_p falls among the candidates
+    if (n > set.k) {
+      last = reach(s, v, b, x, total, [&](unsigned long long) { return (unsigned long long)set.k; });
+      found = last > 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = v[i] > 0 && v[i] >= last ? finer_of(wt[i]) : 0;
+    if (found && set.p < 1.0) {
+      last = reach(s, v, b, x, total, [&](unsigned long long sum) {
+        const double need = set.p * (set.k < a.vocab || complete ? (double)sum : all * 0x1p52);
+        reached = need <= (double)sum;
+        return !reached ? 0ull : need > 1.0 ? min(sum, (unsigned long long)__builtin_ceil(need)) : 1ull;
+      });
+      found = !reached || last > 0;
+    }
+    if (found) {
+      bool dropped = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (v[i] < last || wt[i] < set.few) {
+          dropped |= v[i] > 0;
+          x[i] = 0;
+        }
+      }
+      // nothing below the bound would stay either
+      ready = complete || set.k < a.vocab || reached || __syncthreads_or(dropped);
+    }
+    if (found && ready) {
+      const int shift = max(0, 32 - __builtin_clz(a.vocab - 1) - 11);
+      uint64_t by_id[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        by_id[i] = v[i] << 32 | v[i] >> 32;
+        b[i] = (int)(~(uint32_t)v[i] >> shift) & (kSortMost - 1);
+      }
+      last = reach(s, by_id, b, x, total, [&](unsigned long long sum) {
+        return set.u < 1.0 ? min(sum, (unsigned long long)(set.u * (double)sum) + 1) : sum;
+      });
+      found = last > 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (found && x[i] > 0 && by_id[i] == last) {
+          a.tokens[r] = (int32_t)~(uint32_t)v[i];
+          if (a.logprobs) a.logprobs[r] = (float)log(wt[i] / ((double)total * 0x1p-52));
+        }
+    }
+    if (found && ready) return;
+    ready = !found;   // sorted then
+  }
   if (ready) {
     // First in the order of the logits: how many of the first ones stay; then those in
     // the order of their ids (~id above the key): the draw.
@@ -1013,7 +1182,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
         v0 = i0 < kept ? v0 << 32 | v0 >> 32 : 0;
         v1 = i1 < kept ? v1 << 32 | v1 >> 32 : 0;
       } else {
-        const double target = set.u * total;
+        const double target = set.target(total);
         if (w0 > 0.0) {
           if (c0 > target) atomicMin(&s_token, i0);
           atomicMax(&s_cut, i0);
@@ -1036,7 +1205,12 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
 }
 
 // ---------------------------------------------------------------------- rest
+struct BinsShared {
+  unsigned long long mass[kFine];
+  uint32_t count[kFine];
+};
 union RestShared {
+  BinsShared bins;
   RadixShared radix;
   WholeShared whole;
 };
@@ -1044,9 +1218,10 @@ union RestShared {
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs a, SampleWork w) {
   __shared__ RestShared s;
-  const int64_t r = blockIdx.x;
+  __shared__ int s_last;
+  const int64_t r = blockIdx.y;
   if (!w.todo[r]) return;
-  const int lane = threadIdx.x & 63;
+  const int tid = threadIdx.x, lane = tid & 63;
   const ChunkInfo* info = w.info + r * w.chunks;
   const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
   const Settings set = settings_of(a, r);
@@ -1054,11 +1229,38 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
   if (lane < w.chunks) mine = info[lane];
   const uint32_t top = wave_max_of_quads(quad_max(mine.top));
   const Weight weight = set.weight(top);
+  const bool bins = set.bins(a.vocab) && has_bins(weight);
+  if (bins) {
+    // a histogram of every chunk, by the row's workgroups together; the last one goes on
+    for (int c = blockIdx.x; c < w.chunks; c += gridDim.x) {
+      const uint32_t chunk_top = info[c].top;
+      if (chunk_top == 0) continue;
+      __syncthreads();
+      s.bins.mass[tid] = 0;
+      s.bins.count[tid] = 0;
+      __syncthreads();
+      add_to_bins(Piece<T>(row, part_of(c)), set.weight(chunk_top), s.bins.mass, s.bins.count, set.k < a.vocab);
+      __syncthreads();
+      w.mass[(r * w.chunks + c) * kFine + tid] = s.bins.mass[tid];
+      w.count[(r * w.chunks + c) * kFine + tid] = (uint16_t)s.bins.count[tid];
+    }
+    __syncthreads();
+    if (tid == 0) {   // one wave's fences hold for the workgroup (by every wave 250 us more: they write the L2 back)
+      __threadfence();
+      s_last = atomicAdd(&w.done[r], 1) == (int)gridDim.x - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
+  } else if (blockIdx.x > 0) {
+    return;
+  }
   double all = 0.0, before;
   if (set.sums(a.vocab)) {
-    pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set.u, before, all);
+    pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set, before, all);
   }
-  if (set.bins(a.vocab) && whole_row(s.whole, a, w, row, r, set, weight, all)) return;
+  // (numbers of 0 and 1 ask for the first and the last weight, where multiples of 2^-43 will not do)
+  if (bins && set.u > 0.0 && set.u < 1.0 && whole_row(s.whole, a, w, row, r, set, weight, all)) return;
   __syncthreads();
   radix_row(s.radix, a, row, r, set, weight);
 }
@@ -1073,7 +1275,8 @@ size_t workspace_parts(int64_t rows, int64_t vocab, SampleWork& w, char* base) {
   const size_t bins = vocab > kSmallVocab ? n * kFine : 0;
   w.count = reinterpret_cast<uint16_t*>(w.mass + bins);
   w.todo = reinterpret_cast<int32_t*>(w.count + bins);
-  return (size_t)(reinterpret_cast<char*>(w.todo + rows) - base);
+  w.done = w.todo + rows;
+  return (size_t)(reinterpret_cast<char*>(w.done + rows) - base);
 }
 
 }  // namespace
@@ -1087,13 +1290,15 @@ void launch_sample(const SampleArgs& a, void* ws, hipStream_t stream) {
   SampleWork w{};
   workspace_parts(a.rows, a.vocab, w, static_cast<char*>(ws));
   const dim3 scan((unsigned)w.chunks, (unsigned)a.rows), rows((unsigned)a.rows);
+  const int64_t share = kRestGroups / a.rows, parts = share < 1 ? 1 : share < w.chunks ? share : w.chunks;
+  const dim3 left((unsigned)parts, (unsigned)a.rows);
   // rows without filters, and rows whose logits are all candidates, are never left over
   const bool rest = (a.top_k || a.top_p || a.min_p) && a.vocab > kSmallVocab;
   const auto launch = [&](auto type) {
     using T = decltype(type);
     sample_scan_kernel<T><<<scan, kSampleThreads, 0, stream>>>(a, w);
     sample_draw_kernel<T><<<rows, kSampleThreads, 0, stream>>>(a, w);
-    if (rest) sample_rest_kernel<T><<<rows, kSampleThreads, 0, stream>>>(a, w);
+    if (rest) sample_rest_kernel<T><<<left, kSampleThreads, 0, stream>>>(a, w);
   };
   if (a.dtype == W4_OUT_F32) launch(0.0f);
   else launch((uint16_t)0);

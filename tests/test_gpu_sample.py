@@ -262,3 +262,74 @@ def test_the_same_from_run_to_run():
         again, lp2 = w4.sample(z, u, None, k, p, m)
         torch.cuda.synchronize()
         assert torch.equal(tokens, again) and torch.equal(lp, lp2)
+
+
+@pytest.mark.parametrize("V", [2048, 70000])
+def test_many_candidates_alike(V):
+    """Hundreds of equal logits around the cuts, and nearly equal ones beside a far larger one: candidates that share a
+    bin of the order."""
+    rng = np.random.default_rng(V)
+    z = np.full((6, V), -4.0)
+    for i, n in enumerate([200, 256, 257, 300, 900, 1500]):
+        z[i, rng.permutation(V)[:n]] = 2.0
+        z[i, rng.permutation(V)[:40]] = 2.5
+    u = rng.random(6).astype(np.float32)
+    for k in (30, 100, 290, 700, 1300):
+        run(z, top_k=k, uniform=u)
+        run(z, 0.7, k, 0.8, None, u)
+    run(z, top_p=0.5, uniform=u)
+    run(z, top_p=0.5, min_p=0.7, uniform=u)
+    z = (rng.standard_normal((6, V)) * 1e-3).astype(np.float32).astype(np.float64)
+    z[:, V // 2] = 30.0
+    for k in (60, 500, 1000):
+        run(z, top_k=k, uniform=u)
+        run(z, 40.0, k, 0.9, None, u)
+
+
+def test_weights_far_below_the_largest():
+    """Positive weights under 2^-53 of the largest one are kept and counted like others, and drawn by numbers at the
+    end."""
+    V = 40000
+    rng = np.random.default_rng(3)
+    z = np.full((4, V), -300.0)
+    at = rng.permutation(V)[:600]
+    z[:, at] = -60.0 - np.sort(rng.random(600)).astype(np.float32)
+    z[:, 20000] = 0.0
+    u = np.array([0.0, 0.5, 1.0 - 2.0 ** -24, 1.0])
+    for k in (100, 400, 601):
+        run(z, top_k=k, uniform=u)
+        run(z, 0.5, k, uniform=u)
+    run(z, top_p=1.0 - 2.0 ** -24, uniform=u)
+    run(z, min_p=1e-30, uniform=u)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20, 100, 300])
+def test_long_nuclei_in_every_number_of_rows(rows):
+    """Rows that the candidates do not decide, among others that they do, however many workgroups share them; one
+    workspace for all calls, in a graph beside eager calls of other rows."""
+    rng = np.random.default_rng(rows)
+    V = 40000
+    z = logits(rng, rows, V, "f32", sigma=1.0, peak=7.0)
+    u = rng.random(rows).astype(np.float32)
+    p = np.where(np.arange(rows) % 3 == 0, 0.99, 0.5).astype(np.float32)
+    k = np.where(np.arange(rows) % 5 == 2, 9000, 0)
+    tokens, lp = run(z, 1.5, k, p, None, u)
+    d = lambda v, t: torch.tensor(np.ascontiguousarray(v), dtype=t, device=dev())
+    ws = torch.empty(w4.w4a16_sample_workspace(rows, V), dtype=torch.uint8, device=dev())
+    out, out_lp = torch.empty(rows, dtype=torch.int32, device=dev()), torch.empty(rows, device=dev())
+    args = [d(z, torch.float32), d(u, torch.float32), out, torch.full((rows,), 1.5, device=dev()), d(k, torch.int32),
+            d(p, torch.float32), None, out_lp, ws]
+    other = list(args)
+    other[0], other[2] = torch.flip(args[0], [0]).contiguous(), torch.empty_like(out)
+    w4.w4a16_sample(*args)
+    torch.cuda.synchronize()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        w4.w4a16_sample(*args)
+    for _ in range(3):
+        out.fill_(-7)
+        w4.w4a16_sample(*other)
+        g.replay()
+        torch.cuda.synchronize()
+        assert (out.cpu().numpy() == tokens).all() and (out_lp.cpu().numpy() == lp).all()
