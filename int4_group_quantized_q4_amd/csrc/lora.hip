@@ -3,8 +3,9 @@
 //
 // Bound by memory: y is read and out written once, and every adapter that occurs
 // is read once for each tile of its rows.  So rows of one adapter are gathered
-// into tiles of up to 64 (by a sort of the ids; up to 64 rows every workgroup
-// finds its tile's rows among them by itself), and the two products run on the
+// into tiles: of up to 64 by a sort of the ids, of up to 16 where there are at most
+// 128 rows, among which every workgroup finds its tile's by itself.  The two products
+// run on the
 // 16x16x32 matrix cores with the factors' rows as the left and the tokens as the
 // right operand, so that a lane ends with neighbouring r, or neighbouring n, of
 // one token.
@@ -15,6 +16,11 @@
 //           with B are exact in the fp32 accumulators; one term would round h to
 //           8 bits).  The terms lie one after another along the product's inner
 //           dimension: 3 rank / 32 steps.
+//
+// Figures, of both kernels in a graph (K 4096; rows, N, rank, adapters): 1 of 2816 by
+// 4096, rank 16: 8.6 us, two launches and as many round trips to memory.  64, 14336,
+// 16, 48 of their own: 13.8 us, 25 MB, 1.8 TB/s; all of one adapter 11.6 us.  4090,
+// 14336, 64, 7: 77 us, of which the sort 7, shrink 19, expand 49 (235 MB at 4.8 TB/s).
 
 #include "common.h"
 #include "serving.h"
@@ -26,9 +32,17 @@ namespace {
 constexpr int kLoraThreads = 256;
 constexpr int kWaves = kLoraThreads / 64;   // of the second product
 constexpr int kTile = 64;           // rows of one adapter in a tile
-constexpr int kFewRows = 64;        // up to as many rows are taken a group at a time
-constexpr int kDirectRows = 256;    // up to as many rows need no sort: 64-row pieces of the ids, one a lane
+// Up to as many rows need no sort (64-row pieces of the ids, one a lane).  With 256 in place of 128 that many rows took
+// 39 us for 29 (rank 64, one adapter; a workgroup a row looks for its tile), and 64 of 48 adapters 14.5 for 13.8; with
+// 64, 128 rows of 48 adapters 14.8 for 13.1.
+constexpr int kDirectRows = 128;
+// Their tiles: 64 rows of one adapter run side by side (rank 64, N 4096: 11.7 us; 29.9 in one tile, 24.8 in one with
+// the groups' operands in registers together, which costs 64 rows of 48 adapters 1 us).
+constexpr int kDirectTile = 16;
+// Parts of K at most, and workgroups that the parts are to make: 64 rows of one adapter as above 34.8 us with 4 parts,
+// 29.8 with 16, 35.5 with 32; 4090 rows 90 us with 128 workgroups, 77 with 256, 86 with 512.
 constexpr int kMaxSplits = 16;
+constexpr int kSplitGroups = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;  // bins of the sort (and one for rows without)
 
@@ -143,7 +157,7 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& l, const LoraWork& w, 
     return true;
   }
   // The j-th row leads a tile if the number of rows of its adapter before it is a
-  // multiple of 64; the tile is it and the next ones.
+  // multiple of 16; the tile is it and the next ones.
   int mine[kDirectRows / 64];
 #pragma unroll
   for (int q = 0; q < kDirectRows / 64; ++q) {
@@ -163,13 +177,13 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& l, const LoraWork& w, 
                                : 0;
     all += __builtin_popcountll(same);
   }
-  if (before % kTile != 0) return false;
-  count = min(kTile, all - before);
+  if (before % kDirectTile != 0) return false;
+  count = min(kDirectTile, all - before);
   if (threadIdx.x < 64) {
     if (lane >= count) s_rows[lane] = j;
 #pragma unroll
     for (int q = 0; q < kDirectRows / 64; ++q)
-      if (at[q] >= before && at[q] < before + kTile) s_rows[at[q] - before] = 64 * q + lane;
+      if (at[q] >= before && at[q] < before + kDirectTile) s_rows[at[q] - before] = 64 * q + lane;
   }
   __syncthreads();
   return true;
@@ -449,8 +463,7 @@ void launch_shrink(const LoraArgs& l, const LoraWork& w, int rt, dim3 grid, hipS
 template <int G>
 void launch_expand(const LoraArgs& l, const LoraWork& w, int blocks, dim3 grid, hipStream_t stream) {
   const int steps = (3 * (l.rank / 8) + 3) / 4;
-  const int groups = (int)((min(l.rows, (int64_t)kTile) + 15) / 16);
-  const size_t lds = (size_t)min(groups, G) * steps * 64 * sizeof(u32x4);
+  const size_t lds = (size_t)G * steps * 64 * sizeof(u32x4);
   switch (l.rank) {
     case 8: lora_expand_kernel<G, 1, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
     case 16: lora_expand_kernel<G, 2, 1><<<grid, kLoraThreads, lds, stream>>>(l, w, blocks); break;
@@ -463,13 +476,13 @@ void launch_expand(const LoraArgs& l, const LoraWork& w, int blocks, dim3 grid, 
 
 // Tiles that the rows make at most.
 int64_t most_tiles(int64_t rows, int64_t adapters) {
-  const int64_t each = rows / kTile + adapters + 1;
+  const int64_t each = rows / (rows > kDirectRows ? kTile : kDirectTile) + adapters + 1;
   return rows < each ? rows : each;
 }
 
 // Parts of K: enough workgroups for the chip where there are few tiles.
 int splits_of(int64_t rows, int64_t K, int64_t adapters) {
-  const int64_t want = 256 / most_tiles(rows, adapters), steps = K / 32;
+  const int64_t want = kSplitGroups / most_tiles(rows, adapters), steps = K / 32;
   int64_t s = want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want;
   if (s > (steps + 3) / 4) s = (steps + 3) / 4;   // a step for each of the four waves
   return (int)s;
@@ -504,15 +517,16 @@ void launch_lora(const LoraArgs& l, void* ws, hipStream_t stream) {
   const int rt = r_tiles <= 1 ? 1 : r_tiles <= 2 ? 2 : 4;
   const unsigned groups_of_rows = (unsigned)(l.rows > kDirectRows ? tiles : l.rows);
   const dim3 shrink((unsigned)(w.splits * ((r_tiles + rt - 1) / rt)), groups_of_rows);
-  if (l.rows <= kFewRows) launch_shrink<4, 1>(l, w, rt, shrink, stream);
+  if (l.rows <= kDirectRows) launch_shrink<4, 1>(l, w, rt, shrink, stream);
   else launch_shrink<8, 4>(l, w, rt, shrink, stream);
   const int64_t all = (l.N + 63) / 64;
+  // 64-column blocks a wave: its terms serve all of them, where workgroups abound (64 rows of 48 adapters, N 14336:
+  // 20.6 us with one, 15.6 with four; 64 rows of one, N 4096: 29.8 and 47.8)
   int64_t blocks = tiles * all / 4096;
   blocks = blocks >= 2 ? 4 : blocks >= 1 ? 2 : 1;
   const dim3 expand((unsigned)((all + kWaves * blocks - 1) / (kWaves * blocks)), groups_of_rows);
-  // Few rows are mostly alone with their adapter: one group at a time leaves the
-  // registers to more waves.  At most 64 KB of terms: four groups up to rank 168.
-  if (l.rows <= kFewRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
+  // At most 64 KB of terms: four groups up to rank 168.
+  if (l.rows <= kDirectRows) launch_expand<1>(l, w, (int)blocks, expand, stream);
   else if (l.rank <= 168) launch_expand<4>(l, w, (int)blocks, expand, stream);
   else launch_expand<2>(l, w, (int)blocks, expand, stream);
 }

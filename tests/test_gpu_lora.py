@@ -231,3 +231,15 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for *_, out, _, want, _ in sets:
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows", [15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 193, 257])
+@pytest.mark.parametrize("adapters", [1, 3])
+def test_rows_around_the_tiles(rows, adapters):
+    rng = np.random.default_rng(rows * 10 + adapters)
+    K, N, rank = 96, 80, 16
+    x, y, a, b = rnd(rng, rows, K), rnd(rng, rows, N), rnd(rng, adapters, rank, K), rnd(rng, adapters, N, rank)
+    s = rng.uniform(0.5, 2, adapters).astype(np.float32)
+    for ids in (np.zeros(rows, int), rng.integers(0, adapters, rows), np.arange(rows) * adapters // rows):
+        got = w4.lora_add(bf16_dev(x), i32(ids), bf16_dev(a), bf16_dev(b), torch.tensor(s, device=dev()), bf16_dev(y))
+        check(got, x, ids, a, b, s, y)
