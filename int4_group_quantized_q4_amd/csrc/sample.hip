@@ -27,7 +27,7 @@
 // sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 71,
 // with 54 such rows 87.  (With the histograms made by every scan it took 61 for those,
 // but the scan 19 to 36 for all rows with a long filter.)  256 rows without filters:
-// 39 and 5.3, 3.4 TB/s, bound by the series' instructions.
+// 35 and 5.3, 3.9 TB/s, the series' instructions beside the loads.
 //
 // The second kernel's time is that of fetching its code as much as of running it (a
 // workgroup passes through it once).  With the third kernel's code called from it, it
@@ -275,24 +275,13 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   uint32_t top = quad_max(mine);
   if ((lane & 3) == 0) s_group[tid / 4] = top;
   top = wave_max_of_quads(top);
-  if (lane == 0) s_top[wv] = top;
+  const bool sums = set.sums(a.vocab), lists = set.lists(a.vocab);
   if (tid == 0) {
     s_arg = INT32_MAX;
     s_n = 0;
     s_bound = kLowestKey;
   }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < kSampleWaves; ++v) top = max(top, s_top[v]);
-  if (mine == top) {
-    const float z = key_value(top);
-    int arg = INT32_MAX;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (piece.z[i] == z) arg = piece.id(i);
-    atomicMin(&s_arg, arg);
-  }
-  const bool sums = set.sums(a.vocab), lists = set.lists(a.vocab);
+  if (lists) __syncthreads();
   // the bound: the leading 18 bits of the rank-th largest of the groups' maxima, which
   // one wave finds bit by bit
   if (lists && a.vocab > kSmallVocab && wv == 0) {
@@ -313,21 +302,32 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
     }
     if (lane == 0) s_bound = max(bound, kLowestKey);
   }
-  const Weight weight = set.weight(top);
+  // beside the wave's own top, for which it need not wait (256 rows without filters 39 us, 44 beside the chunk's)
   double sum = 0.0;
   if (top >= kPosInfKey) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += piece.z[i] == INFINITY ? 1.0 : 0.0;
   } else if (sums && top > 0) {
+    const Weight weight = set.weight(top);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      sum += exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
-      // two at a time: with more of them under way registers run out for a CU's second workgroup
-      if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int i = 0; i < kPer; ++i) sum += exp2_f64(((double)piece.z[i] - weight.top) * weight.per);
   }
   sum = wave_sum(sum);
-  if (lane == 0) s_sum[wv] = sum;
+  if (lane == 0) {
+    s_top[wv] = top;
+    s_sum[wv] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kSampleWaves; ++v) top = max(top, s_top[v]);
+  if (mine == top) {
+    const float z = key_value(top);
+    int arg = INT32_MAX;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i)
+      if (piece.z[i] == z) arg = piece.id(i);
+    atomicMin(&s_arg, arg);
+  }
   __syncthreads();
   const uint32_t bound = s_bound;
   if (lists && __ballot(mine >= bound)) {
@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   }
   __syncthreads();
   if (wv == 0) {
-    const double part = lane < kSampleWaves ? s_sum[lane] : 0.0;
+    const uint32_t part_top = lane < kSampleWaves ? s_top[lane] : 0u;
+    const double part = part_top > 0 ? s_sum[lane] * set.weight(top)(part_top) : 0.0;
     sum = wave_sum(part);
     if (sums && lane < kSampleWaves) w.part[at * kSampleWaves + lane] = part;
     if (lane == 0) w.info[at] = {sum, top, s_arg, bound, s_n};
