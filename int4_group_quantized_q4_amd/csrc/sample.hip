@@ -49,13 +49,15 @@ namespace {
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kPer = 16;                               // logits a thread
-constexpr int kChunk = kSampleThreads * kPer;
+constexpr int kChunk = kSampleThreads * kPer;          // most logits of a chunk
 constexpr int kMostChunks = (1 << 20) / kChunk;        // one a lane
 constexpr int kGroups = 256;                           // of 4 threads each
+constexpr int kGroup = 4 * kPer;
 constexpr int kRankSure = 64, kRankMost = 224;
 constexpr int kListMost = 768;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
 constexpr int kBinMost = 256;                          // candidates of a bin that are compared with one another
+constexpr int kRestMost = 1024;                        // the same in the third kernel, which does not sort
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
 // Workgroups of the third kernel, up to one a chunk: each ends with a fence that writes its XCD's L2 back, so more of
@@ -106,14 +108,15 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 // The rank of a chunk's bound.  Up to 64 it is top_k: then the chunk with the largest
 // bound has that many from there up, wherever the row's first ones lie.  Beyond, the
 // rank at which about 1.5 top_k logits of the row are candidates if its chunks are
-// alike (groups with one of e logits from the bound up: 256 (1 - exp(-e / 256))); a row
+// alike (groups with one of e logits from the bound up: 256 (1 - exp(-e / 256)), as far
+// as the chunk has 256); a row
 // without top_k gets 64.  Ranks next to the number of groups make lists overflow.
-__device__ __forceinline__ int rank_of(int k, int n, int groups) {
+__device__ __forceinline__ int rank_of(int k, int n, int chunk, int groups) {
   int rank = kRankSure;
   if (k <= kRankSure) rank = max(k, 16);
   else if (k < n) {
-    const float e = 1.5f * kChunk * (float)k / (float)n;
-    rank = (int)fminf(fmaxf(kGroups * (1.0f - __expf(-e / kGroups)), kRankSure), kRankMost);
+    const float e = 1.5f * (float)chunk * (float)k / (float)n, all = (float)(chunk / kGroup);
+    rank = (int)fminf(fmaxf(all * (1.0f - __expf(-e / all)), kRankSure), kRankMost);
   }
   return max(1, min(rank, 7 * groups / 8));
 }
@@ -218,17 +221,19 @@ struct Piece {
   }
 };
 
-// The wave's part of a chunk.
-__device__ __forceinline__ int part_of(int chunk) {
-  return chunk * kSampleWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The wave's part of a chunk; chunks are of as many parts as there are for each, so that
+// none is short; a wave without a part has one behind the row's end.
+__device__ __forceinline__ int part_of(int chunk, int waves) {
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  return wv < waves ? chunk * waves + wv : (1 << 20) / kWavePart;
 }
 
 // f of every chunk: the next one's loads are issued first.
 template <typename T, typename F>
-__device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, const F& f) {
-  Piece<T> now(row, part_of(0));
+__device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, int waves, const F& f) {
+  Piece<T> now(row, part_of(0, waves));
   for (int c = 0; c < chunks; ++c) {
-    const Piece<T> next(row, part_of(min(c + 1, chunks - 1)));
+    const Piece<T> next(row, part_of(min(c + 1, chunks - 1), waves));
     f(now);
     now = next;
   }
@@ -242,7 +247,6 @@ struct ChunkInfo {
   int32_t n;         // candidates; more than the list holds: it is not whole
 };
 
-int chunks_of(int64_t vocab) { return (int)((vocab + kChunk - 1) / kChunk); }
 __host__ __device__ constexpr int list_most(int64_t vocab) { return vocab <= kSmallVocab ? kSmallVocab : kListMost; }
 
 struct SampleWork {
@@ -252,7 +256,7 @@ struct SampleWork {
   uint64_t* list;              // [rows][chunks][list_most]: key << 32 | ~id
   unsigned long long* mass;    // [rows][chunks][kFine]
   uint16_t* count;             // [rows][chunks][kFine]
-  int chunks;
+  int chunks, waves;           // parts of 1024 logits in a chunk
 };
 
 // ---------------------------------------------------------------------- scan
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   const int64_t r = blockIdx.y, at = r * w.chunks + blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const Row<T> row{static_cast<const T*>(a.logits) + r * a.stride, a.vocab};
-  const Piece<T> piece(row, part_of(blockIdx.x));
+  const Piece<T> piece(row, part_of(blockIdx.x, w.waves));
   const Settings set = settings_of(a, r);
   float m = piece.z[0];   // (a NaN stays)
 #pragma unroll
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
       g[i] = s_group[64 * i + lane];
       some += __builtin_popcountll(__ballot(g[i] > 0));
     }
-    const int rank = rank_of(set.k, a.vocab, some);
+    const int rank = rank_of(set.k, a.vocab, w.waves * kWavePart, some);
     uint32_t bound = 0;
     for (uint32_t bit = 1u << 31; bit >= 1u << 14; bit >>= 1) {
       int n = 0;
@@ -510,6 +514,94 @@ __device__ __forceinline__ void running_sums(double& v0, double& v1, int N, doub
 
 __device__ __forceinline__ int power_of_two(int n) { return n <= 64 ? 64 : 1 << (32 - __builtin_clz(n - 1)); }
 
+// ------------------------------------------------- many candidates, not sorted
+// The candidates of a row by 2048 bins in the order asked for: the bins' sums tell
+// the bin in which the running sum reaches a border, and the candidates of that bin
+// are compared with one another.
+template <int MOST>   // of a bin that are compared
+struct ReachShared {
+  uint64_t v[kSortMost];
+  unsigned long long bins[kSortMost];
+  uint64_t bin_v[MOST];
+  unsigned long long bin_x[MOST];
+  unsigned long long scan[kSampleWaves], above;
+  uint64_t last;
+  int bin, n;
+};
+
+// Two candidates a thread with order values v (descending; their bins b ascend) and
+// amounts x: the v of the first one at which the running sum of x is need(total) or
+// more; 0 if need is, or if a bin holds too many.  2 us, whether the candidates are 50 or
+// 1500; 128 of them compared with one another without bins took 3.5.
+template <int MOST, typename F>
+__device__ __forceinline__ uint64_t reach(ReachShared<MOST>& s, const uint64_t (&v)[2], const int (&b)[2],
+                                          const unsigned long long (&x)[2], unsigned long long& total,
+                                          const F& need_of) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  __syncthreads();   // what was read of the call before
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s.bins[tid + i * kSampleThreads] = 0;
+  if (tid == 0) {
+    s.n = 0;
+    s.last = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0) atomicAdd(&s.bins[b[i]], x[i]);
+  __syncthreads();
+  const unsigned long long first = s.bins[2 * tid], second = s.bins[2 * tid + 1];
+  unsigned long long upto = wave_scan(first + second);
+  if (lane == 63) s.scan[wv] = upto;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleWaves; ++i) {
+    const unsigned long long sum = s.scan[i];
+    if (i < wv) upto += sum;
+    total += sum;
+  }
+  const unsigned long long need = need_of(total);
+  if (need == 0) return 0;
+  const unsigned long long before = upto - first - second;
+  if (before < need && upto >= need) {
+    const bool in_first = before + first >= need;
+    s.bin = 2 * tid + (in_first ? 0 : 1);
+    s.above = in_first ? before : before + first;
+  }
+  __syncthreads();
+  const int bin = s.bin;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0 && b[i] == bin) {
+      const int at = atomicAdd(&s.n, 1);
+      if (at < MOST) {
+        s.bin_v[at] = v[i];
+        s.bin_x[at] = x[i];
+      }
+    }
+  __syncthreads();
+  const int n = s.n;
+  if (n > MOST) return 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0 && b[i] == bin) {
+      unsigned long long run = s.above;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) run += s.bin_v[j] >= v[i] ? s.bin_x[j] : 0;
+      if (run >= need && run - x[i] < need) s.last = v[i];
+    }
+  __syncthreads();
+  return s.last;
+}
+
+// A weight in multiples of 2^-52, none of a positive one: 2048 of at most 1 stay below 2^64.
+__device__ __forceinline__ unsigned long long finer_of(double w) {
+  const unsigned long long x = __builtin_bit_cast(unsigned long long, w + 1.0) -
+                               __builtin_bit_cast(unsigned long long, 1.0);
+  return w > 0.0 && x == 0 ? 1 : x;
+}
+
 // ------------------------------------------------------- a row by its histograms
 // The weights of a chunk's logits (and their number) by bins, beside its largest one.
 // The last bin takes all the lower ones and is not used.
@@ -538,12 +630,13 @@ __device__ __forceinline__ bool has_bins(const Weight& weight) {
 }
 
 struct WholeShared {
-  uint64_t v[kSortMost];
+  ReachShared<kRestMost> order;
   double scale[kMostChunks], sums[kMostChunks];
+  unsigned long long in_chunk[kMostChunks];
   int shift[kMostChunks];
   double scan[kSampleWaves];
+  unsigned long long fixed[kSampleWaves];
   int bin, n;
-  unsigned long long last;
   double above;
 };
 
@@ -563,6 +656,20 @@ __device__ __forceinline__ int reach_bin(WholeShared& s, double v, double need, 
   return bin;
 }
 
+// The least key of a logit above -infinity for which f holds; f holds for all from some
+// key on, the largest finite one's among them.  64 keys at a time, one a lane.
+template <typename F>
+__device__ __forceinline__ uint32_t least_key(const F& f) {
+  uint32_t lo = kLowestKey;
+  for (int shift = 26; shift >= 0; shift = shift > 6 ? shift - 6 : shift > 0 ? 0 : -1) {
+    const uint64_t key = lo + ((uint64_t)(threadIdx.x & 63) << shift);
+    const uint64_t no = __ballot(key < kPosInfKey && !f(key_value((uint32_t)key)));
+    if (no) lo += ((uint32_t)(63 - __builtin_clzll(no)) << shift) + (shift == 0 ? 1 : 0);
+    else if (shift == 0) break;
+  }
+  return lo;
+}
+
 // False: the histograms do not say, or a bin holds too many.
 template <typename T>
 __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, const SampleWork& w, const Row<T>& row,
@@ -578,6 +685,7 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     const float shift = ref - weight.steps(key_value(top));
     s.scale[tid] = top == 0 ? 0.0 : weight(top) * (1.0 / kFixed);
     s.shift[tid] = top == 0 || !(shift < kFine) ? kFine : (int)shift;
+    s.in_chunk[tid] = 0;
   }
   __syncthreads();
   const auto bin_of = [&](float z) { return (int)fminf(ref - weight.steps(z), (float)(kFine - 1)); };
@@ -590,55 +698,64 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
       row_mass += (double)mass[c * kFine + b] * s.scale[c];
       if (use_k) row_count += (double)count[c * kFine + b];
     }
-  uint64_t v0 = 0, v1 = 0;
-  int listed = -1, N = 64;
-  // the logits of a bin, sorted
+  // the logits of a bin, two a thread, with their weights and places among 2048 of the bin
+  uint64_t v[2] = {0, 0};
+  double wt[2];
+  int place[2], listed = -1;
   const auto list = [&](int bin) {
     if (bin == listed) return true;
     listed = bin;
+    const float lo = key_value(least_key([&](float z) { return bin_of(z) <= bin; }));
+    const float end = bin > 0 ? key_value(least_key([&](float z) { return bin_of(z) < bin; })) : INFINITY;
     __syncthreads();
     if (tid == 0) s.n = 0;
     __syncthreads();
-    for_chunks(row, w.chunks, [&](const Piece<T>& p) {
+    for_chunks(row, w.chunks, w.waves, [&](const Piece<T>& p) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (bin_of(p.z[i]) == bin) {
+        if (p.z[i] >= lo && p.z[i] < end) {
           const int at = atomicAdd(&s.n, 1);
-          if (at < kSortMost) s.v[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
+          if (at < kSortMost) s.order.v[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
         }
     });
     __syncthreads();
-    const int n = s.n;
-    if (n > kSortMost) return false;
-    N = power_of_two(n);
-    v0 = tid < n ? s.v[tid] : 0;
-    v1 = tid + kSampleThreads < n ? s.v[tid + kSampleThreads] : 0;
-    sort_descending(s.v, v0, v1, N);
+    if (s.n > kSortMost) return false;
+    const float first = fminf(end, weight.m), scale = (float)(kSortMost - 1) / (first - lo);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = tid + i * kSampleThreads;
+      v[i] = at < s.n ? s.order.v[at] : 0;
+      const uint32_t key = (uint32_t)(v[i] >> 32);
+      wt[i] = v[i] > 0 ? weight(key) : 0.0;
+      place[i] = (int)fminf((first - key_value(key)) * scale, (float)(kSortMost - 1));
+    }
     return true;
   };
-  // the listed weights, those behind `last` left out, and their running sums
-  unsigned long long last = 0;   // the last one kept, as key << 32 | ~id; smaller ones are not
-  double w0, w1, c0, c1, listed_sum;
-  const auto listed_sums = [&]() {
-    c0 = w0 = v0 > 0 && v0 >= last ? weight((uint32_t)(v0 >> 32)) : 0.0;
-    c1 = w1 = v1 > 0 && v1 >= last ? weight((uint32_t)(v1 >> 32)) : 0.0;
-    running_sums(c0, c1, N, s.scan, listed_sum);
+  unsigned long long last = 0, x[2], total;   // last: of the last one kept, key << 32 | ~id; smaller ones are not
+  const auto kept = [&]() {                   // the listed weights, those behind `last` left out
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = v[i] > 0 && v[i] >= last ? finer_of(wt[i]) : 0;
   };
   int bin = kFine - 1;   // the last one's
   double above, sum = all;
   if (use_k) {
     bin = reach_bin(s, row_count, (double)set.k, above);
     if (bin >= kFine - 1 || !list(bin)) return false;
-    const int at = set.k - (int)above - 1;
-    if (at == tid) s.last = v0;
-    if (at == tid + kSampleThreads) s.last = v1;
-    __syncthreads();
-    last = s.last;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = v[i] > 0;
+    last = reach(s.order, v, place, x, total, [&](unsigned long long) { return (unsigned long long)set.k - (int)above; });
+    if (last == 0) return false;
     if (use_p) {
-      listed_sums();
+      kept();
+      unsigned long long here = wave_sum(x[0] + x[1]);
+      __syncthreads();
+      if (lane == 0) s.fixed[wv] = here;
+      __syncthreads();
+      here = 0;
+      for (int i = 0; i < kSampleWaves; ++i) here += s.fixed[i];
       double before = tid < bin ? row_mass : 0.0, none = 0.0;
       running_sums(before, none, kSampleThreads, s.scan, sum);
-      sum += listed_sum;
+      sum += (double)here * 0x1p-52;
     }
   }
   if (use_p) {
@@ -646,80 +763,64 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     const int reached = reach_bin(s, row_mass, need, above);
     if (reached >= kFine - 1 || reached > bin || !list(reached)) return false;
     bin = reached;
-    listed_sums();
+    kept();
     // the first place that reaches it, else the last one
-    const unsigned long long before = last;
-    __syncthreads();
-    if (tid == 0) s.last = before;
-    __syncthreads();
-    if (w0 > 0.0 && above + c0 >= need) atomicMax(&s.last, (unsigned long long)v0);
-    if (w1 > 0.0 && above + c1 >= need) atomicMax(&s.last, (unsigned long long)v1);
-    __syncthreads();
-    last = s.last;
+    const double rest = __builtin_ceil((need - above) * 0x1p52);
+    last = reach(s.order, v, place, x, total, [&](unsigned long long here) {
+      return rest < (double)here ? (unsigned long long)__builtin_fmax(rest, 1.0) : here;
+    });
+    if (last == 0) return false;
   }
   if (set.few > 0.0) {
-    // the lowest key that weighs as much, and its bin
-    uint32_t lo = kLowestKey, hi = order_key(weight.m);
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (weight(mid) >= set.few) hi = mid;
-      else lo = mid + 1;
-    }
-    const int at = bin_of(key_value(lo));
+    const uint32_t least = least_key([&](float z) { return z >= weight.m || weight.of(z) >= set.few; });
+    const int at = bin_of(key_value(least));
     if (at <= bin) {
       if (at >= kFine - 1 || !list(at)) return false;
       bin = at;
-      w0 = v0 > 0 ? weight((uint32_t)(v0 >> 32)) : 0.0;
-      w1 = v1 > 0 ? weight((uint32_t)(v1 >> 32)) : 0.0;
-      __syncthreads();
-      if (tid == 0) s.last = ~0ull;
-      __syncthreads();
-      if (w0 >= set.few && v0 >= last) atomicMin(&s.last, (unsigned long long)v0);
-      if (w1 >= set.few && v1 >= last) atomicMin(&s.last, (unsigned long long)v1);
-      __syncthreads();
-      last = s.last;   // (none of the bin: all of it is behind)
     }
+    const unsigned long long from = (unsigned long long)least << 32;
+    last = from > last ? from : last;
   }
   if (bin >= kFine - 1) return false;
   // the kept weights of each chunk: whole bins, and the listed ones
+  kept();
+  const int per = w.waves * kWavePart;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (x[i] > 0) atomicAdd(&s.in_chunk[(int)~(uint32_t)v[i] / per], x[i]);
   __syncthreads();
-  if (v0 > 0) s.v[tid] = v0;
-  if (v1 > 0) s.v[tid + kSampleThreads] = v1;
-  __syncthreads();
-  const int n = s.n;
   for (int c = wv; c < w.chunks; c += kSampleWaves) {
     unsigned long long whole = 0;
-    for (int b = lane; b < bin - s.shift[c]; b += 64) whole += mass[c * kFine + b];
-    double part = (double)wave_sum(whole) * s.scale[c], in_bin = 0.0;
-    for (int i = lane; i < n; i += 64) {
-      const uint64_t v = s.v[i];
-      if (v >= last && (int)(~(uint32_t)v / kChunk) == c) in_bin += weight((uint32_t)(v >> 32));
+    const int most = bin - s.shift[c];
+#pragma unroll
+    for (int i = 0; i < kFine / 64; ++i) {
+      const int b = 64 * i + lane;
+      if (b < most) whole += mass[c * kFine + b];
     }
-    part += wave_sum(in_bin);
+    const double part = (double)wave_sum(whole) * s.scale[c] + (double)s.in_chunk[c] * 0x1p-52;
     if (lane == 0) s.sums[c] = part;
   }
   __syncthreads();
-  double before, total;
-  const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set, before, total);
-  // kept: whole bins above, and in the bin up to the last one
+  double before, sum_kept;
+  const int c = pick_share(lane < w.chunks ? s.sums[lane] : 0.0, set, before, sum_kept);
+  const float last_z = key_value((uint32_t)(last >> 32));
+  const int last_id = (int)~(uint32_t)last;   // (-1 where the key alone decides: as far as any id)
   const auto share = [&](float z, int id) {
-    const int b = bin_of(z);
-    if (b > bin || (b == bin && (((uint64_t)order_key(z) << 32) | (uint32_t)~id) < last)) return 0.0;
-    return weight.of(z);
+    return z > last_z || (z == last_z && (uint32_t)id <= (uint32_t)last_id) ? weight.of(z) : 0.0;
   };
-  const Piece<T> p(row, part_of(c));
+  const Piece<T> p(row, part_of(c, w.waves));
   double part = 0.0, in_front, weighs;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) part += share(p.z[i], p.id(i));
   part = wave_sum(part);
   if (lane == 0) s.scan[wv] = part;
   __syncthreads();
-  const int picked = pick_lane(lane < kSampleWaves ? s.scan[lane] : 0.0, set.target(total) - before, in_front);
+  const int picked = pick_lane(lane < kSampleWaves ? s.scan[lane] : 0.0, set.target(sum_kept) - before, in_front);
   if (wv != picked) return true;
-  const int token = pick_in_part(p, share, set.target(total) - before - in_front, weighs);
+  const int token = pick_in_part(p, share, set.target(sum_kept) - before - in_front, weighs);
   if (lane == 0) {
     a.tokens[r] = token;
-    if (a.logprobs) a.logprobs[r] = (float)log(weighs / total);
+    if (a.logprobs) a.logprobs[r] = (float)log(weighs / sum_kept);
   }
   return true;
 }
@@ -920,97 +1021,10 @@ __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, c
   }
 }
 
-// ------------------------------------------------- many candidates, not sorted
-// The candidates of a row by 2048 bins in the order asked for: the bins' sums tell
-// the bin in which the running sum reaches a border, and the candidates of that bin
-// are compared with one another.
-struct DrawShared {
-  uint64_t v[kSortMost];
-  unsigned long long bins[kSortMost];
-  uint64_t bin_v[kBinMost];
-  unsigned long long bin_x[kBinMost];
-  unsigned long long scan[kSampleWaves], above;
-  uint64_t last;
-  int bin, n;
-};
-
-// Two candidates a thread with order values v (descending; their bins b ascend) and
-// amounts x: the v of the first one at which the running sum of x is need(total) or
-// more; 0 if need is, or if a bin holds too many.  2 us, whether the candidates are 50 or
-// 1500; 128 of them compared with one another without bins took 3.5.
-template <typename F>
-__device__ __forceinline__ uint64_t reach(DrawShared& s, const uint64_t (&v)[2], const int (&b)[2],
-                                          const unsigned long long (&x)[2], unsigned long long& total,
-                                          const F& need_of) {
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  __syncthreads();   // what was read of the call before
-#pragma unroll
-  for (int i = 0; i < 2; ++i) s.bins[tid + i * kSampleThreads] = 0;
-  if (tid == 0) {
-    s.n = 0;
-    s.last = 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (x[i] > 0) atomicAdd(&s.bins[b[i]], x[i]);
-  __syncthreads();
-  const unsigned long long first = s.bins[2 * tid], second = s.bins[2 * tid + 1];
-  unsigned long long upto = wave_scan(first + second);
-  if (lane == 63) s.scan[wv] = upto;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWaves; ++i) {
-    const unsigned long long sum = s.scan[i];
-    if (i < wv) upto += sum;
-    total += sum;
-  }
-  const unsigned long long need = need_of(total);
-  if (need == 0) return 0;
-  const unsigned long long before = upto - first - second;
-  if (before < need && upto >= need) {
-    const bool in_first = before + first >= need;
-    s.bin = 2 * tid + (in_first ? 0 : 1);
-    s.above = in_first ? before : before + first;
-  }
-  __syncthreads();
-  const int bin = s.bin;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (x[i] > 0 && b[i] == bin) {
-      const int at = atomicAdd(&s.n, 1);
-      if (at < kBinMost) {
-        s.bin_v[at] = v[i];
-        s.bin_x[at] = x[i];
-      }
-    }
-  __syncthreads();
-  const int n = s.n;
-  if (n > kBinMost) return 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (x[i] > 0 && b[i] == bin) {
-      unsigned long long run = s.above;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) run += s.bin_v[j] >= v[i] ? s.bin_x[j] : 0;
-      if (run >= need && run - x[i] < need) s.last = v[i];
-    }
-  __syncthreads();
-  return s.last;
-}
-
-// A weight in multiples of 2^-52, none of a positive one: 2048 of at most 1 stay below 2^64.
-__device__ __forceinline__ unsigned long long finer_of(double w) {
-  const unsigned long long x = __builtin_bit_cast(unsigned long long, w + 1.0) -
-                               __builtin_bit_cast(unsigned long long, 1.0);
-  return w > 0.0 && x == 0 ? 1 : x;
-}
-
 // ------------------------------------------------------------------ the draw
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs a, SampleWork w) {
-  __shared__ DrawShared s;
+  __shared__ ReachShared<kBinMost> s;
   __shared__ double s_sum[kSampleWaves];
   __shared__ int s_n, s_kept, s_token, s_cut;
   uint64_t* const s_v = s.v;
@@ -1047,7 +1061,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
     const double* parts = w.part + (r * w.chunks + chunk) * kSampleWaves;
     double in_front, share;
     const int part = pick_lane(lane < kSampleWaves ? parts[lane] * scale : 0.0, set.target(all) - before, in_front);
-    const Piece<T> p(row, chunk * kSampleWaves + part);
+    const Piece<T> p(row, chunk * w.waves + part);
     const int token =
         pick_in_part(p, [&](float z, int) { return weight.of(z); }, set.target(all) - before - in_front, share);
     if (lane == 0) {
@@ -1242,7 +1256,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
       s.bins.mass[tid] = 0;
       s.bins.count[tid] = 0;
       __syncthreads();
-      add_to_bins(Piece<T>(row, part_of(c)), set.weight(chunk_top), s.bins.mass, s.bins.count, set.k < a.vocab);
+      add_to_bins(Piece<T>(row, part_of(c, w.waves)), set.weight(chunk_top), s.bins.mass, s.bins.count, set.k < a.vocab);
       __syncthreads();
       w.mass[(r * w.chunks + c) * kFine + tid] = s.bins.mass[tid];
       w.count[(r * w.chunks + c) * kFine + tid] = (uint16_t)s.bins.count[tid];
@@ -1269,7 +1283,9 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
 }
 
 size_t workspace_parts(int64_t rows, int64_t vocab, SampleWork& w, char* base) {
-  w.chunks = chunks_of(vocab);
+  const int parts = (int)((vocab + kWavePart - 1) / kWavePart);
+  w.chunks = (parts + kSampleWaves - 1) / kSampleWaves;
+  w.waves = (parts + w.chunks - 1) / w.chunks;
   const size_t n = (size_t)rows * w.chunks;
   w.list = reinterpret_cast<uint64_t*>(base);
   w.info = reinterpret_cast<ChunkInfo*>(w.list + n * list_most(vocab));
