@@ -17,16 +17,16 @@
 // Where that piece may be too short (a nucleus of thousands of tokens) a third kernel
 // (rest) takes the row: several workgroups make histograms of its chunks' weights
 // (and counts) over bins of a sixteenth of an octave, and the last one finds in them
-// the bin of the last kept logit, reads the row again for that bin's logits, and sorts
-// them.  Where the bin holds too many (ties), a radix select over the logits' order
-// keys takes the histogram's place.
+// the bin of the last kept logit, reads the row again for that bin's logits, and cuts
+// among them as above.  Where the bin holds too many (ties), a radix select over the
+// logits' order keys takes the histogram's place.
 //
 // Rows of 131072 fp32 logits, 54 to 64 of them, in us for the kernels: without filters
 // scan 11.4 (of which the 64-bit series take half: greedy rows 5.0), draw 5.6; top_k 50
 // and top_p 0.95 9.0 and 10.8; top_k 1000 9.3 and 13.7 (28.3 with all candidates
-// sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 71,
-// with 54 such rows 87.  (With the histograms made by every scan it took 61 for those,
-// but the scan 19 to 36 for all rows with a long filter.)  256 rows without filters:
+// sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 52
+// (of which one CU's reading of the row takes 18), with 54 such rows 65.  (With the
+// histograms made by every scan that took 19 to 36 for all rows with a long filter.)  256 rows without filters:
 // 35 and 5.3, 3.9 TB/s, the series' instructions beside the loads.
 //
 // The second kernel's time is that of fetching its code as much as of running it (a
@@ -62,7 +62,7 @@ constexpr int kSmallVocab = kSortMost;                 // up to here every logit
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
 // Workgroups of the third kernel, up to one a chunk: each ends with a fence that writes its XCD's L2 back, so more of
 // them cost as well (54 rows that need it 150 us with 512, 87 with 256, 91 with 128, 109 with one a row; one row of 52
-// 65, 71, 81, 102).
+// 65, 71, 81, 102; when measured).
 constexpr int kRestGroups = 256;
 constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
@@ -199,16 +199,34 @@ struct Piece {
   __device__ __forceinline__ int place(int j) const { return first + j * 64 * kVec; }
   __device__ __forceinline__ int id(int i) const { return min(place(i / kVec), end - kVec) + i % kVec; }
   // part: 1024 logits of the row
-  __device__ __forceinline__ Piece(const Row<T>& row, int part)
-      : first(part * kWavePart + (int)(threadIdx.x & 63) * kVec), end(row.n) {
+  struct Raw {
+    u32x4 v[kPer / kVec];
+  };
+  static __device__ __forceinline__ int lane_first(int part) {
+    return part * kWavePart + (int)(threadIdx.x & 63) * kVec;
+  }
+  static __device__ __forceinline__ Raw load(const Row<T>& row, int part) {   // rows of a vector and more
+    Raw raw;
+#pragma unroll
+    for (int j = 0; j < kPer / kVec; ++j) {
+      const int at = min(lane_first(part) + j * 64 * kVec, row.n - kVec);
+      raw.v[j] = *reinterpret_cast<const LooseVector*>(row.z + at);
+    }
+    return raw;
+  }
+  __device__ __forceinline__ Piece(const Row<T>& row, int part) : first(lane_first(part)), end(row.n) {
     if (__builtin_expect(end < kVec, 0)) {   // less than a vector: the first lane's first places
       for (int i = 0; i < kPer; ++i)
         z[i] = i < kVec && first == 0 && id(i) >= 0 ? row.value(id(i)) : -INFINITY;
       return;
     }
-    u32x4 v[kPer / kVec];
-#pragma unroll
-    for (int j = 0; j < kPer / kVec; ++j) v[j] = *reinterpret_cast<const LooseVector*>(row.z + id(j * kVec));
+    take(load(row, part), part);
+  }
+  __device__ __forceinline__ Piece(const Row<T>& row, int part, const Raw& raw) : first(lane_first(part)), end(row.n) {
+    take(raw, part);
+  }
+  __device__ __forceinline__ void take(const Raw& raw, int part) {
+    const u32x4(&v)[kPer / kVec] = raw.v;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint32_t word = v[i / kVec][i % kVec * sizeof(T) / 4];
@@ -228,15 +246,37 @@ __device__ __forceinline__ int part_of(int chunk, int waves) {
   return wv < waves ? chunk * waves + wv : (1 << 20) / kWavePart;
 }
 
-// f of every chunk: the next one's loads are issued first.
+// f of every chunk of a row of a vector and more: the next two ones' loads are under way.
 template <typename T, typename F>
 __device__ __forceinline__ void for_chunks(const Row<T>& row, int chunks, int waves, const F& f) {
-  Piece<T> now(row, part_of(0, waves));
-  for (int c = 0; c < chunks; ++c) {
-    const Piece<T> next(row, part_of(min(c + 1, chunks - 1), waves));
-    f(now);
-    now = next;
+  using P = Piece<T>;
+  const auto part = [&](int c) { return part_of(min(c, chunks - 1), waves); };
+  typename P::Raw even = P::load(row, part(0)), odd = P::load(row, part(1));
+  for (int c = 0; c < chunks; c += 2) {
+    f(P(row, part(c), even));
+    even = P::load(row, part(c + 2));
+    if (c + 1 < chunks) f(P(row, part(c + 1), odd));
+    odd = P::load(row, part(c + 3));
   }
+}
+
+// The piece's logits for which f holds, as key << 32 | ~id, behind the *n entries of a
+// list that takes `most`; one atomic a wave.
+template <typename T, typename F>
+__device__ __forceinline__ void append(const Piece<T>& p, const F& f, int* n, uint64_t* list, int most) {
+  uint32_t those = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) those |= f(p.z[i]) ? 1u << i : 0u;
+  const int own = __builtin_popcount(those), upto = (int)wave_scan((int64_t)own);
+  int at = 0;
+  if ((threadIdx.x & 63) == 63 && upto > 0) at = atomicAdd(n, upto);
+  at = __builtin_amdgcn_readlane(at, 63) + upto - own;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (those >> i & 1) {
+      if (at < most) list[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
+      ++at;
+    }
 }
 
 struct ChunkInfo {
@@ -336,22 +376,7 @@ __global__ void __launch_bounds__(kSampleThreads, 8) sample_scan_kernel(SampleAr
   const uint32_t bound = s_bound;
   if (lists && __ballot(mine >= bound)) {
     const float z = key_value(bound);
-    uint32_t reach = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) reach |= piece.z[i] >= z ? 1u << i : 0u;
-    const int own_n = __builtin_popcount(reach);
-    const int upto = (int)wave_scan((int64_t)own_n);
-    int at_list = 0;
-    if (lane == 63) at_list = atomicAdd(&s_n, upto);
-    at_list = __builtin_amdgcn_readlane(at_list, 63) + upto - own_n;
-    uint64_t* list = w.list + at * list_most(a.vocab);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (reach >> i & 1) {
-        if (at_list < list_most(a.vocab))
-          list[at_list] = ((uint64_t)order_key(piece.z[i]) << 32) | (uint32_t)~piece.id(i);
-        ++at_list;
-      }
+    append(piece, [&](float v) { return v >= z; }, &s_n, w.list + at * list_most(a.vocab), list_most(a.vocab));
   }
   __syncthreads();
   if (wv == 0) {
@@ -692,11 +717,11 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
   // the row's histograms, a bin a thread (the last bin is not used)
   double row_mass = 0.0, row_count = 0.0;
   if (tid < kFine - 1)
+#pragma unroll 4
     for (int c = 0; c < w.chunks; ++c) {
-      const int b = tid - s.shift[c];
-      if (b < 0) continue;
-      row_mass += (double)mass[c * kFine + b] * s.scale[c];
-      if (use_k) row_count += (double)count[c * kFine + b];
+      const int b = tid - s.shift[c], at = c * kFine + max(b, 0);   // loads without branches: several under way
+      row_mass += b < 0 ? 0.0 : (double)mass[at] * s.scale[c];
+      if (use_k) row_count += b < 0 ? 0.0 : (double)count[at];
     }
   // the logits of a bin, two a thread, with their weights and places among 2048 of the bin
   uint64_t v[2] = {0, 0};
@@ -711,12 +736,7 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     if (tid == 0) s.n = 0;
     __syncthreads();
     for_chunks(row, w.chunks, w.waves, [&](const Piece<T>& p) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (p.z[i] >= lo && p.z[i] < end) {
-          const int at = atomicAdd(&s.n, 1);
-          if (at < kSortMost) s.order.v[at] = ((uint64_t)order_key(p.z[i]) << 32) | (uint32_t)~p.id(i);
-        }
+      append(p, [&](float z) { return z >= lo && z < end; }, &s.n, s.order.v, kSortMost);
     });
     __syncthreads();
     if (s.n > kSortMost) return false;
@@ -794,8 +814,8 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     const int most = bin - s.shift[c];
 #pragma unroll
     for (int i = 0; i < kFine / 64; ++i) {
-      const int b = 64 * i + lane;
-      if (b < most) whole += mass[c * kFine + b];
+      const unsigned long long m = mass[c * kFine + 64 * i + lane];
+      whole += 64 * i + lane < most ? m : 0;
     }
     const double part = (double)wave_sum(whole) * s.scale[c] + (double)s.in_chunk[c] * 0x1p-52;
     if (lane == 0) s.sums[c] = part;
