@@ -2,7 +2,7 @@
 //
 // The kept tokens are a first piece of the order (logit descending, id ascending),
 // so no sort of a row is needed.  Two kernels, that read the logits once:
-//   scan  a workgroup for 16384 logits: their largest one, the sum of their
+//   scan  a workgroup for up to 16384 logits (a row's chunks are alike in size): their largest one, the sum of their
 //         weights beside it (where the row needs the whole sum), and the
 //         candidates: all logits from a bound up that at least `rank` of them reach,
 //         the rank-th largest of the maxima of 256 groups, cut to its leading bits;
@@ -26,16 +26,17 @@
 // and top_p 0.95 9.0 and 10.8; top_k 1000 9.3 and 13.7 (28.3 with all candidates
 // sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 52
 // (of which one CU's reading of the row takes 18), with 54 such rows 65.  (With the
-// histograms made by every scan that took 19 to 36 for all rows with a long filter.)  256 rows without filters:
-// 35 and 5.3, 3.9 TB/s, the series' instructions beside the loads.
+// histograms made by every scan that took 19 to 36 for all rows with a long filter.)
+// 256 rows without filters: 35 and 5.3, 3.9 TB/s, the series' instructions beside the
+// loads.
 //
 // The second kernel's time is that of fetching its code as much as of running it (a
 // workgroup passes through it once).  With the third kernel's code called from it, it
 // took 8 us more, for a stack that no row used.
 //
-// Weights are 2^((z - m) log2 e / T) in 64 bits.  Where they are added by atomics
-// (the histograms) they are whole multiples of 2^-43 of the largest one, so that the
-// sums do not depend on the order; elsewhere sums have a fixed order.
+// Weights are 2^((z - m) log2 e / T) in 64 bits.  Where they are added by atomics they
+// are whole multiples of 2^-52 (the candidates) or 2^-43 (the histograms) of the largest
+// one, so that the sums do not depend on the order; elsewhere sums have a fixed order.
 
 #include "common.h"
 #include "serving.h"
@@ -53,7 +54,7 @@ constexpr int kChunk = kSampleThreads * kPer;          // most logits of a chunk
 constexpr int kMostChunks = (1 << 20) / kChunk;        // one a lane
 constexpr int kGroups = 256;                           // of 4 threads each
 constexpr int kGroup = 4 * kPer;
-constexpr int kRankSure = 64, kRankMost = 224;
+constexpr int kRankSure = 64, kRankMost = 224;         // (the last groups' maxima say little about the bound)
 constexpr int kListMost = 768;                         // candidates of a chunk
 constexpr int kSortMost = 2048;                        // logits that are sorted
 constexpr int kBinMost = 256;                          // candidates of a bin that are compared with one another
@@ -763,7 +764,8 @@ __device__ __forceinline__ bool whole_row(WholeShared& s, const SampleArgs& a, c
     if (bin >= kFine - 1 || !list(bin)) return false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) x[i] = v[i] > 0;
-    last = reach(s.order, v, place, x, total, [&](unsigned long long) { return (unsigned long long)set.k - (int)above; });
+    last = reach(s.order, v, place, x, total,
+                 [&](unsigned long long) { return (unsigned long long)set.k - (unsigned long long)above; });
     if (last == 0) return false;
     if (use_p) {
       kept();
@@ -1276,7 +1278,8 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
       s.bins.mass[tid] = 0;
       s.bins.count[tid] = 0;
       __syncthreads();
-      add_to_bins(Piece<T>(row, part_of(c, w.waves)), set.weight(chunk_top), s.bins.mass, s.bins.count, set.k < a.vocab);
+      add_to_bins(Piece<T>(row, part_of(c, w.waves)), set.weight(chunk_top), s.bins.mass, s.bins.count,
+                  set.k < a.vocab);
       __syncthreads();
       w.mass[(r * w.chunks + c) * kFine + tid] = s.bins.mass[tid];
       w.count[(r * w.chunks + c) * kFine + tid] = (uint16_t)s.bins.count[tid];

@@ -50,6 +50,11 @@ Parity status of each function (which pins it, see tests/test_oracle_*.py):
                                   composed from torch fp8 conversion and float64
                                   ops)
 
+  serving.plan                    pinned (hand-computed steps, cut and bad ones)
+  serving.rope                    pinned (multiplication of complex numbers)
+  serving.lora_add                pinned (torch float64)
+  serving.sample                  pinned (hand-computed draws; frequencies)
+
 The FP8 (W8A8) leg in fp8.py is the comparison path the pages set against
 W4A16 ([RQ] "What happened"; [VG] "2. What you can quantize").
 """
