@@ -25,7 +25,7 @@
 // scan 11.4 (of which the 64-bit series take half: greedy rows 5.0), draw 5.6; top_k 50
 // and top_p 0.95 9.0 and 10.8; top_k 1000 9.3 and 13.7 (28.3 with all candidates
 // sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 52
-// (of which one CU's reading of the row takes 18), with 54 such rows 65.  (With the
+// (of which one CU's reading of the row takes 18), with 54 such rows 61.  (With the
 // histograms made by every scan that took 19 to 36 for all rows with a long filter.)
 // 256 rows without filters: 35 and 5.3, 3.9 TB/s, the series' instructions beside the
 // loads.
@@ -61,9 +61,8 @@ constexpr int kBinMost = 256;                          // candidates of a bin th
 constexpr int kRestMost = 1024;                        // the same in the third kernel, which does not sort
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
-// Workgroups of the third kernel, up to one a chunk: each ends with a fence that writes its XCD's L2 back, so more of
-// them cost as well (54 rows that need it 150 us with 512, 87 with 256, 91 with 128, 109 with one a row; one row of 52
-// 65, 71, 81, 102; when measured).
+// Workgroups of the third kernel, up to one a chunk: each writes its XCD's L2 back, so more of them cost as well (54 rows
+// that need it 101 us with 512, 61 with 256; one row of 52 47.5 and 52, with 128 81 when 256 took 71).
 constexpr int kRestGroups = 256;
 constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
@@ -1284,11 +1283,16 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
       w.mass[(r * w.chunks + c) * kFine + tid] = s.bins.mass[tid];
       w.count[(r * w.chunks + c) * kFine + tid] = (uint16_t)s.bins.count[tid];
     }
+    // Every wave's stores have reached the L2; one wave writes it back (all of them: 250 us more) and waits for that
+    // before the count, and drops what its caches hold after it.
+    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (tid == 0) {   // one wave's fences hold for the workgroup (by every wave 250 us more: they write the L2 back)
-      __threadfence();
+    if (tid == 0) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+      __builtin_amdgcn_s_waitcnt(0);
       s_last = atomicAdd(&w.done[r], 1) == (int)gridDim.x - 1;
-      __threadfence();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      __builtin_amdgcn_s_waitcnt(0);
     }
     __syncthreads();
     if (!s_last) return;

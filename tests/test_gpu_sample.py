@@ -333,3 +333,28 @@ def test_long_nuclei_in_every_number_of_rows(rows):
         g.replay()
         torch.cuda.synchronize()
         assert (out.cpu().numpy() == tokens).all() and (out_lp.cpu().numpy() == lp).all()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap in time, each with its own workspace: long nuclei among their rows, whose histograms several
+    workgroups join."""
+    rng = np.random.default_rng(17)
+    rows, V = 12, 40000
+    u = rng.random(rows).astype(np.float32)
+    p = np.where(np.arange(rows) % 2 == 0, 0.99, 0.6).astype(np.float32)
+    calls = []
+    for sigma in (1.0, 1.3):
+        z = logits(rng, rows, V, "f32", sigma=sigma, peak=7.0)
+        tokens, lp = run(z, 1.5, None, p, None, u)
+        d = lambda v: torch.tensor(v, dtype=torch.float32, device=dev())
+        calls.append((tokens, lp, [d(z), d(u), torch.empty(rows, dtype=torch.int32, device=dev()), d(np.full(rows, 1.5)),
+                                   None, d(p), None, torch.empty(rows, device=dev()),
+                                   torch.empty(w4.w4a16_sample_workspace(rows, V), dtype=torch.uint8, device=dev())]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        for (_, _, args), s in zip(calls, streams):
+            w4.w4a16_sample(*args, stream=s)
+    torch.cuda.synchronize()
+    for tokens, lp, args in calls:
+        assert (args[2].cpu().numpy() == tokens).all() and (args[7].cpu().numpy() == lp).all()
