@@ -782,9 +782,10 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *   logprobs     out, nullable  [rows] fp32: log of the token's share of the kept weights
  *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
  *                matter.  Calls that overlap in time need one each.
- * Weights and sums are 64-bit, so that a draw next to a border between two tokens falls
- * on its side of it; where top_p keeps so many tokens that their weights are summed in
- * bins, each enters as a multiple of 2^-43 of the largest one.  A logit of -infinity is never drawn; beside logits of +infinity no
+ * Weights are 64-bit and so are their sums, into which each enters with an error of at
+ * most 2^-52 of the largest weight (2^-43 where top_p keeps so many tokens that they are
+ * summed in bins), so that a draw next to a border between two tokens falls on its side
+ * of it.  A logit of -infinity is never drawn; beside logits of +infinity no
  * other is.  A row with a NaN, and one without a logit above -infinity: token -1, log
  * probability NaN.
  * int32 and fp32 arrays 4-byte aligned.  No output may overlap another argument

@@ -61,8 +61,8 @@ constexpr int kBinMost = 256;                          // candidates of a bin th
 constexpr int kRestMost = 1024;                        // the same in the third kernel, which does not sort
 constexpr int kSmallVocab = kSortMost;                 // up to here every logit is a candidate
 constexpr int kFine = 1024;                            // bins of a 16th of an octave; the last one takes the rest
-// Workgroups of the third kernel, up to one a chunk: each writes its XCD's L2 back, so more of them cost as well (54 rows
-// that need it 101 us with 512, 61 with 256; one row of 52 47.5 and 52, with 128 81 when 256 took 71).
+// Workgroups of the third kernel, up to one a chunk: each writes its XCD's L2 back, so more of them cost as well (54
+// rows that need it 101 us with 512, 61 with 256; one row of 52 47.5 and 52, with 128 81 when 256 took 71).
 constexpr int kRestGroups = 256;
 constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64

@@ -347,9 +347,9 @@ def test_two_streams_at_once():
         z = logits(rng, rows, V, "f32", sigma=sigma, peak=7.0)
         tokens, lp = run(z, 1.5, None, p, None, u)
         d = lambda v: torch.tensor(v, dtype=torch.float32, device=dev())
-        calls.append((tokens, lp, [d(z), d(u), torch.empty(rows, dtype=torch.int32, device=dev()), d(np.full(rows, 1.5)),
-                                   None, d(p), None, torch.empty(rows, device=dev()),
-                                   torch.empty(w4.w4a16_sample_workspace(rows, V), dtype=torch.uint8, device=dev())]))
+        out, out_lp = torch.empty(rows, dtype=torch.int32, device=dev()), torch.empty(rows, device=dev())
+        ws = torch.empty(w4.w4a16_sample_workspace(rows, V), dtype=torch.uint8, device=dev())
+        calls.append((tokens, lp, [d(z), d(u), out, d(np.full(rows, 1.5)), None, d(p), None, out_lp, ws]))
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in calls]
     for _ in range(10):
