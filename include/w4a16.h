@@ -783,7 +783,7 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
  *                matter.  Calls that overlap in time need one each.
  * Weights are 64-bit and so are their sums, into which each enters with an error of at
- * most 2^-52 of the largest weight (2^-43 where top_p keeps so many tokens that they are
+ * most 2^-50 of the largest weight (2^-43 where top_p keeps so many tokens that they are
  * summed in bins), so that a draw next to a border between two tokens falls on its side
  * of it.  A logit of -infinity is never drawn; beside logits of +infinity no
  * other is.  A row with a NaN, and one without a logit above -infinity: token -1, log

@@ -68,26 +68,22 @@ constexpr int kBins = 2048;                            // of the radix select
 constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
 
 // 2^t for t <= 0; 0 below 2^-1074 and for a NaN.  The nearest whole number is what t
-// leaves in the low bits of a large sum; the series of 2^r to the 11th power, |r| <=
-// 1/2, leaves out less than 1e-14.
-struct Series {
-  double c[12];
-  constexpr Series() : c() {
-    double v = 1.0;
-    for (int k = 0; k < 12; ++k) {
-      c[k] = v;
-      v *= 0.693147180559945309417232121458 / (k + 1);
-    }
-  }
-};
+// leaves in the low bits of a large sum; 2^r, |r| <= 1/2, is 1 + r q(r) with the q of
+// degree 10 that meets (2^r - 1) / r in the 11 Chebyshev points of [-1/2, 1/2].  With its
+// roundings that is off by less than 2^-52 of the value, for as many instructions as the
+// power series to the 11th power, which leaves out 2^-46.7 of it.
 constexpr double kLarge = 0x1.8p52;
 __device__ __forceinline__ double exp2_f64(double t) {
-  constexpr Series kSeries;
+  constexpr double kPower[12] = {
+      1.0,
+      0x1.62e42fefa39efp-1, 0x1.ebfbdff82c598p-3, 0x1.c6b08d704a0c2p-5, 0x1.3b2ab6fba1ddap-7,
+      0x1.5d87fe78a5276p-10, 0x1.430913096fd9fp-13, 0x1.ffcbfc670dcd4p-17, 0x1.62bfd47773353p-20,
+      0x1.b524fae627834p-24, 0x1.e6063f7217bc6p-28, 0x1.e9d3fe3952179p-32};
   t = __builtin_fmax(t, -2000.0);
   const double sum = t + kLarge, r = t - (sum - kLarge);
-  double v = kSeries.c[11];
+  double v = kPower[11];
 #pragma unroll
-  for (int k = 10; k >= 0; --k) v = __builtin_fma(v, r, kSeries.c[k]);
+  for (int k = 10; k >= 0; --k) v = __builtin_fma(v, r, kPower[k]);
   return __builtin_ldexp(v, (int)(uint32_t)__builtin_bit_cast(uint64_t, sum));
 }
 

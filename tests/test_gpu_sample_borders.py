@@ -1,0 +1,57 @@
+"""Draws and cuts whose number lies next to the border between two tokens, nearer than 64-bit weights of less care
+would resolve.  The side is that of the definition in 50 digits, and every case is farther from its border than the
+errors that w4a16.h allows the weights can move it."""
+
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_q4_amd as w4
+from gpu_util import dev
+
+pytestmark = pytest.mark.gpu
+getcontext().prec = 50
+
+
+def call(z, u, temperature=None, top_k=None, top_p=None):
+    """Tokens of the rows z (float32 numpy), each with the settings given."""
+    n = len(z)
+    full = lambda v, t: None if v is None else torch.full((n,), v, dtype=t, device=dev())
+    tokens, _ = w4.sample(torch.from_numpy(z).to(dev()), torch.tensor(u, dtype=torch.float32, device=dev()),
+                          full(temperature, torch.float32), full(top_k, torch.int32), full(top_p, torch.float32))
+    torch.cuda.synchronize()
+    return tokens.tolist()
+
+
+def two_logits(V, first, z):
+    """Rows of V logits: z at `first`, 0 behind it at V - 1, the others at -infinity."""
+    out = np.full((1, V), -np.inf, dtype=np.float32)
+    out[0, first], out[0, V - 1] = z, 0.0
+    return out
+
+
+# z, temperature, number: w = exp(z / temperature) is about 2^-1/2, where powers of 2 by a series are at their worst
+@pytest.mark.parametrize("V,first,top_k", [(2, 0, None), (3, 0, 2), (40000, 5, None), (40000, 17000, 2)])
+@pytest.mark.parametrize("z,t,u", [("-0x1.8fa824p-2", "0x1.2a30e0p+0", "0x1.ab0428p-2"),
+                                   ("-0x1.6eb5fcp-2", "0x1.0b0776p+0", "0x1.a8f64ep-2"),
+                                   ("-0x1.498a80p-2", "0x1.e825dcp-1", "0x1.aa6680p-2")])
+def test_a_number_next_to_a_border(V, first, top_k, z, t, u):
+    z, t, u = (float.fromhex(v) for v in (z, t, u))
+    w = (Decimal(z) / Decimal(t)).exp()
+    # w is off by 2^-50 at most, and moves the difference by (1 - u) of that, 0.6 of 2^-50; roundings of the sum 1 + w
+    # and of its product with u add 2^-52
+    assert 2.0 ** -50 < w - Decimal(u) * (w + 1) < 2.0 ** -48
+    assert call(two_logits(V, first, z), [u], t, top_k) == [first]
+
+
+def test_a_top_p_next_to_a_border():
+    """1 / (1 + w) is just short of top_p: both stay, and a number behind it draws the one at the end."""
+    z, t, p = (float.fromhex(v) for v in ("-0x1.d89a94p-2", "0x1.56f91cp+0", "0x1.2ba9f0p-1"))
+    w = (Decimal(z) / Decimal(t)).exp()
+    assert 2.0 ** -50 < Decimal(p) * (w + 1) - 1 < 2.0 ** -49       # moved by 0.6 of 2^-50 and 2^-52, as above
+    for V in (3, 1500, 40000):
+        zs = np.full((1, V), -np.inf, dtype=np.float32)
+        zs[0, 0], zs[0, V - 1] = 0.0, z
+        assert call(zs, [0.9], t, None, p) == [V - 1], V
