@@ -129,9 +129,10 @@ struct Weight {
   // Sixteenths of an octave, whole ones: exact in fp32 below 2^24, and growing with z.
   __device__ __forceinline__ float steps(float z) const { return __builtin_rintf(z * (float)(16.0 * per)); }
 };
-// A weight in multiples of 2^-43 (the last bits of a number between 2^9 and 2^10).
-__device__ __forceinline__ unsigned long long fixed_of(double w) {
-  return __builtin_bit_cast(unsigned long long, w + 0x1p9) - __builtin_bit_cast(unsigned long long, 0x1p9);
+// A weight in multiples of 2^-43 (the last bits of a number between 2^9 and 2^10), or of
+// 2^-52 times another power of two.
+__device__ __forceinline__ unsigned long long fixed_of(double w, double base = 0x1p9) {
+  return __builtin_bit_cast(unsigned long long, w + base) - __builtin_bit_cast(unsigned long long, base);
 }
 
 // The settings of a row, those that are off replaced by what they do not change.
@@ -1001,8 +1002,11 @@ __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, c
     upto = find_id(s, [&](int i) { return row.key(i) == t ? 1.0 : 0.0; }, 0, row.n, -1.0, ties - 1.0, ignored);
   }
   if (set.p < 1.0) {
+    // as fine as the sum of those that may stay allows, which is at most 2^63: of up to 2048 multiples of 2^-52, of
+    // 2^20 2^-43
+    const double base = __builtin_ldexp(1.0, max(0, 32 - __builtin_clz((min(set.k, row.n) - 1) | 1) - 11));
     const auto amount = [&](uint32_t key, int i) {
-      return kept(key, i) ? fixed_of(weight(key)) : 0ull;
+      return kept(key, i) ? fixed_of(weight(key), base) : 0ull;
     };
     unsigned long long sum = 0;
     for (int i = tid; i < row.n; i += kSampleThreads) sum += amount(row.key(i), i);
@@ -1017,7 +1021,7 @@ __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, c
     const unsigned long long need = part > 1.0 ? (unsigned long long)__builtin_ceil(part) : 1ull;
     unsigned long long above;
     const uint32_t tp = radix_select(s, row, amount, need, above);
-    const unsigned long long each = fixed_of(weight(tp));
+    const unsigned long long each = fixed_of(weight(tp), base);
     if (each > 0) {
       const double ties = (double)((need - above + each - 1) / each);
       upto = find_id(s, [&](int i) { return row.key(i) == tp ? 1.0 : 0.0; }, 0, row.n, -1.0, ties - 1.0, ignored);

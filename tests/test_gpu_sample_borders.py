@@ -55,3 +55,19 @@ def test_a_top_p_next_to_a_border():
         zs = np.full((1, V), -np.inf, dtype=np.float32)
         zs[0, 0], zs[0, V - 1] = 0.0, z
         assert call(zs, [0.9], t, None, p) == [V - 1], V
+
+
+# (z, top_p, whether both stay): w = exp(z) beside 1
+@pytest.mark.parametrize("V", [5000, 131072])
+@pytest.mark.parametrize("z,p,both", [("-0x1.cdbfb2p-1", "0x1.6c3378p-1", True),
+                                      ("-0x1.348b70p-3", "0x1.133f66p-1", False),
+                                      ("-0x1.359688p-2", "0x1.26680ap-1", False)])
+def test_a_cut_next_to_a_border_among_few_allowed_tokens(V, z, p, both):
+    """Fewer allowed tokens than top_k: the cut is as fine as elsewhere."""
+    z, p = float.fromhex(z), float.fromhex(p)
+    over = Decimal(p) * (Decimal(z).exp() + 1) - 1
+    assert 2.0 ** -47 < abs(over) < 2.0 ** -46 and (over > 0) == both      # moved by 2^-50 and 2^-52 at most
+    zs = np.full((1, V), -np.inf, dtype=np.float32)
+    zs[0, 0], zs[0, V - 1] = 0.0, z
+    for k in (50, 2000):
+        assert call(zs, [0.9], None, k, p) == [V - 1 if both else 0], k
