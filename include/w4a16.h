@@ -783,9 +783,9 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
  *                matter.  Calls that overlap in time need one each.
  * Weights are 64-bit and so are their sums, into which each enters with an error of at
- * most 2^-50 of the largest weight (2^-43 where top_p keeps so many tokens that they are
- * summed in bins), so that a draw next to a border between two tokens falls on its side
- * of it.  A logit of -infinity is never drawn; beside logits of +infinity no
+ * most 2^-49 of the largest weight (vocab 2^-62 of it, if that is more, where thousands of
+ * equal or nearly equal logits lie at a cut), so that a draw next to a border between two
+ * tokens falls on its side of it.  A logit of -infinity is never drawn; beside logits of +infinity no
  * other is.  A row with a NaN, and one without a logit above -infinity: token -1, log
  * probability NaN.
  * int32 and fp32 arrays 4-byte aligned.  No output may overlap another argument

@@ -35,8 +35,10 @@
 // took 8 us more, for a stack that no row used.
 //
 // Weights are 2^((z - m) log2 e / T) in 64 bits.  Where they are added by atomics they
-// are whole multiples of 2^-52 (the candidates) or 2^-43 (the histograms) of the largest
-// one, so that the sums do not depend on the order; elsewhere sums have a fixed order.
+// are whole multiples of 2^-52 (the candidates) or 2^-49 (the histograms) of the largest
+// one, or as fine as the tokens' number allows (the radix select: of n of them 2^-63 n,
+// down to 2^-52), so that the sums do not depend on the order; elsewhere sums have a fixed
+// order.
 
 #include "common.h"
 #include "serving.h"
@@ -65,7 +67,7 @@ constexpr int kFine = 1024;                            // bins of a 16th of an o
 // rows that need it 101 us with 512, 61 with 256; one row of 52 47.5 and 52, with 128 81 when 256 took 71).
 constexpr int kRestGroups = 256;
 constexpr int kBins = 2048;                            // of the radix select
-constexpr double kFixed = 0x1p43;   // 2^20 weights of at most 1 stay below 2^64
+constexpr double kFixed = 0x1p49;   // the 2^14 weights of a chunk's histogram, of at most 1, sum to at most 2^63
 
 // 2^t for t <= 0; 0 below 2^-1074 and for a NaN.  The nearest whole number is what t
 // leaves in the low bits of a large sum; 2^r, |r| <= 1/2, is 1 + r q(r) with the q of
@@ -129,9 +131,9 @@ struct Weight {
   // Sixteenths of an octave, whole ones: exact in fp32 below 2^24, and growing with z.
   __device__ __forceinline__ float steps(float z) const { return __builtin_rintf(z * (float)(16.0 * per)); }
 };
-// A weight in multiples of 2^-43 (the last bits of a number between 2^9 and 2^10), or of
+// A weight in multiples of 2^-49 (the last bits of a number between 2^3 and 2^4), or of
 // 2^-52 times another power of two.
-__device__ __forceinline__ unsigned long long fixed_of(double w, double base = 0x1p9) {
+__device__ __forceinline__ unsigned long long fixed_of(double w, double base = 0x1p52 / kFixed) {
   return __builtin_bit_cast(unsigned long long, w + base) - __builtin_bit_cast(unsigned long long, base);
 }
 
@@ -1303,7 +1305,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rest_kernel(SampleArgs 
   if (set.sums(a.vocab)) {
     pick_share(mine.top == 0 ? 0.0 : mine.sum * weight(mine.top), set, before, all);
   }
-  // (numbers of 0 and 1 ask for the first and the last weight, where multiples of 2^-43 will not do)
+  // (numbers of 0 and 1 ask for the first and the last weight, where multiples of 2^-49 will not do)
   if (bins && set.u > 0.0 && set.u < 1.0 && whole_row(s.whole, a, w, row, r, set, weight, all)) return;
   __syncthreads();
   radix_row(s.radix, a, row, r, set, weight);

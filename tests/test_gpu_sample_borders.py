@@ -71,3 +71,28 @@ def test_a_cut_next_to_a_border_among_few_allowed_tokens(V, z, p, both):
     zs[0, 0], zs[0, V - 1] = 0.0, z
     for k in (50, 2000):
         assert call(zs, [0.9], None, k, p) == [V - 1 if both else 0], k
+
+
+@pytest.mark.parametrize("z", ["-0x1.b9ed74p+2", "-0x1.bf1844p+2", "-0x1.bb9980p+2", "-0x1.bda182p+2"])
+def test_numbers_next_to_borders_in_a_long_nucleus(z):
+    """16000 equal weights of some 2^-10, which lie halfway between multiples of 2^-43, behind the largest one: rounded
+    to these they move the draw by 2^-30 in all, a millionth of a token.  The nucleus ends among 300 lower ones."""
+    many, few, V, z = 16000, 300, 16384, float.fromhex(z)
+    wide = np.longdouble
+    exp = lambda v: wide(str(Decimal(v).exp()))
+    w, low = exp(z), exp(-9.0)
+    total = 1 + many * w + few * low
+    p = np.float32(1 - 149.5 * low / total)
+    kept = (p * total - 1 - many * w) / low                 # lower tokens that the nucleus takes: the next whole number
+    assert 0.01 < kept - np.floor(kept) < 0.99
+    total = 1 + many * w + np.ceil(kept) * low
+    i = np.arange(many)
+    sums = 1 + i * w                                        # of the ids up to i
+    u = (sums / total).astype(np.float32)
+    over = u * total - sums
+    # each weight is off by 2^-49 at most, all of them by 2^-35
+    rows = np.nonzero((np.abs(over) > 2.0 ** -33.5) & (np.abs(over) < 2.0 ** -30.5) & (i > 6000))[0]
+    assert len(rows) >= 5
+    zs = np.full((len(rows), V), -np.inf, dtype=np.float32)
+    zs[:, 0], zs[:, 1:1 + many], zs[:, 1 + many:1 + many + few] = 0.0, z, -9.0
+    assert call(zs, u[rows], None, None, float(p)) == [int(r) + (1 if over[r] > 0 else 0) for r in rows]
