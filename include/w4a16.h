@@ -709,9 +709,10 @@ int kv_cache_plan(const int32_t* seq_lens, const int32_t* new_tokens, int64_t se
  *   (a, b) -> scale * (a cos t - b sin t,  b cos t + a sin t)
  * with the pair's dimensions (j, j + rotary_dim/2) (W4_ROPE_HALF) or (2j, 2j + 1)
  * (W4_ROPE_INTERLEAVED); the dimensions behind rotary_dim stay as they are.
- * Scalings for long contexts are a matter of inv_freq and scale.  Angles are
- * reduced in 64 bits and more (an angle of 2^31 keeps 2^-22), cos and sin are
- * fp32 and the sums fp32, rounded once.  A negative position turns back.
+ * Scalings for long contexts are a matter of inv_freq and scale.  An angle is the
+ * exact product, reduced to less than a turn with an error of at most 2^-100 of it
+ * (angles up to 2^50), cos and sin are fp32 and the sums fp32, rounded once.  A
+ * negative position turns back.
  *   q, k       in  [rows] rows of heads*head_dim bf16, strides in elements
  *              (multiples of 8, at least the row's width); k nullable (k_heads 0)
  *   positions  in  [rows] int32

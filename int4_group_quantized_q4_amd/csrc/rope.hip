@@ -3,10 +3,10 @@
 //   (a, b) -> scale (a cos t - b sin t, b cos t + a sin t),  t = p f_j
 //
 // The angle is taken in turns: u = t / (2 pi) as two 64-bit terms (the product of
-// a 31-bit position and a 24-bit frequency, times 1 / (2 pi) to 106 bits), less
-// the nearest quarter turn, exactly, so that the fp32 sine and cosine are of an
-// angle within an eighth of a turn that is good to its last bit, and the quarters
-// swap and negate them.
+// a 31-bit position and a 24-bit frequency, which has 55 bits and so two terms of
+// its own, times 1 / (2 pi) to 106 bits), less the nearest quarter turn, exactly,
+// so that the fp32 sine and cosine are of an angle within an eighth of a turn that
+// is good to its last bit, and the quarters swap and negate them.
 //
 // Bound by memory for many rows: every element is read and written once (8191 rows
 // of 20 heads of 256, half of each turned: 26.8 us, 6.3 TB/s), by latency for few (a
@@ -37,9 +37,10 @@ struct RopeTile {
 
 __device__ __forceinline__ float2 cos_sin(int32_t position, float freq) {
   const double t = (double)position * (double)freq;
+  const double t_rest = __builtin_fma((double)position, (double)freq, -t);
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
   const double hi = t * kHi;
-  const double lo = __builtin_fma(t, kLo, __builtin_fma(t, kHi, -hi));
+  const double lo = __builtin_fma(t_rest, kHi, __builtin_fma(t, kLo, __builtin_fma(t, kHi, -hi)));
   const double quarter = __builtin_rint(4.0 * hi);
   const double rest = __builtin_fma(-0.25, quarter, hi) + lo;   // turns
   float s, c;
