@@ -119,6 +119,15 @@ __device__ __forceinline__ int rank_of(int k, int n, int chunk, int groups) {
   return max(1, min(rank, 7 * groups / 8));
 }
 
+// The least shift of a number below n that leaves less than 2048.  (A count of the leading zeros of 0 is not defined:
+// an n of 1.)
+__host__ __device__ constexpr int shift_of(int n) {
+  const int bits = 32 - __builtin_clz((n - 1) | 1);
+  return bits > 11 ? bits - 11 : 0;
+}
+static_assert(kSortMost == 2048 && shift_of(1) == 0 && shift_of(2048) == 0 && shift_of(2049) == 1 &&
+              shift_of(1 << 20) == 9);
+
 // A row's weights: 2^((z - m) log2 e / T).  (Beside an infinite m all but its equals
 // are infinitely far below it, and weigh 0.)
 struct Weight {
@@ -1006,7 +1015,7 @@ __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, c
   if (set.p < 1.0) {
     // as fine as the sum of those that may stay allows, which is at most 2^63: of up to 2048 multiples of 2^-52, of
     // 2^20 2^-43
-    const double base = __builtin_ldexp(1.0, max(0, 32 - __builtin_clz((min(set.k, row.n) - 1) | 1) - 11));
+    const double base = __builtin_ldexp(1.0, shift_of(min(set.k, row.n)));
     const auto amount = [&](uint32_t key, int i) {
       return kept(key, i) ? fixed_of(weight(key), base) : 0ull;
     };
@@ -1159,7 +1168,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_draw_kernel(SampleArgs 
       ready = complete || set.k < a.vocab || reached || __syncthreads_or(dropped);
     }
     if (found && ready) {
-      const int shift = max(0, 32 - __builtin_clz(a.vocab - 1) - 11);
+      const int shift = shift_of(a.vocab);
       uint64_t by_id[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
