@@ -20,6 +20,7 @@ inline int launch_status() {
   return e == hipSuccess ? W4_OK : W4_ERR_HIP;
 }
 
+// (An empty part overlaps nothing.)
 inline bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return p && q && pn && qn && a < b + qn && b < a + pn;
