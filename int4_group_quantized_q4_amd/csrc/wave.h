@@ -39,11 +39,6 @@ __device__ __forceinline__ V wave_scan(V v) {
 }
 template <typename V>
 __device__ __forceinline__ V wave_sum(V v) { return lane_value(wave_scan(v), 63); }
-// The lane before's value, 0 in the first lane.
-template <typename V>
-__device__ __forceinline__ V lane_before(V v) {   // wave_shr 1
-  return __builtin_bit_cast(V, dpp_u64<0x138>(__builtin_bit_cast(uint64_t, v)));
-}
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = max(v, dpp_u32<0xB1>(v));
