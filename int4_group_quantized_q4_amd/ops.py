@@ -905,9 +905,12 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
       "linear"  f_j / factor
       "base"    the base times factor^(rotary_dim / (rotary_dim - 2)): the slowest
                 pair's turns are divided by factor, the fastest pair's stay
-      "bands"   pairs with at least `fast` turns in the trained context stay, those
-                with at most `slow` are divided by factor, in between linearly in j;
-                scale is 1 + 0.1 ln(factor)"""
+      "bands"   the YaRN method (B. Peng et al., 2023): pairs with at least `fast` turns
+                in the trained context stay, those with at most `slow` are divided by
+                factor, in between linearly in j; scale is 1 + 0.1 ln(factor).  The
+                bounds are rounded outwards to whole pairs and kept in [0, rotary_dim
+                - 1], and bounds that meet are 0.001 apart, as models trained by the
+                method have it"""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive, got %s" % rotary_dim)
     if not factor >= 1.0:
