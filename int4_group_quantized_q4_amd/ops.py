@@ -913,8 +913,10 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
                 method have it"""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive, got %s" % rotary_dim)
-    if not factor >= 1.0:
-        raise ValueError("factor must be at least 1, got %s" % factor)
+    if not 1.0 <= factor < math.inf:
+        raise ValueError("factor must be at least 1 and finite, got %s" % factor)
+    if not 0.0 < base < math.inf:
+        raise ValueError("base must be positive and finite, got %s" % base)
     j = torch.arange(rotary_dim // 2, dtype=torch.float64)
     freq = lambda base: base ** (-2.0 * j / rotary_dim)
     if scaling is None:
@@ -927,8 +929,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
         return freq(base * factor ** (rotary_dim / (rotary_dim - 2))).float(), 1.0
     if scaling != "bands":
         raise ValueError("unknown scaling %r" % (scaling,))
-    if trained is None or not fast > slow > 0:
-        raise ValueError("bands need the trained length and fast > slow > 0")
+    if trained is None or not trained > 0 or not fast > slow > 0 or not base > 1.0:
+        raise ValueError("bands need the trained length, fast > slow > 0 and a base above 1")
     # the pair that makes r turns in the trained context
     at = lambda r: rotary_dim * math.log(trained / (2.0 * math.pi * r)) / (2.0 * math.log(base))
     lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rotary_dim - 1)
