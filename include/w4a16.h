@@ -781,8 +781,9 @@ int w4a16_lora_add(const uint16_t* x, int64_t x_stride, int64_t rows, int64_t K,
  *                last kept token of positive weight
  *   tokens       out [rows] int32
  *   logprobs     out, nullable  [rows] fp32: log of the token's share of the kept weights
- *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned; its contents do not
- *                matter.  Calls that overlap in time need one each.
+ *   ws           w4a16_sample_workspace(...) bytes, 16-byte aligned, the same with and
+ *                without filters; its contents do not matter.  Calls that overlap in
+ *                time need one each.
  * Weights are 64-bit and so are their sums, into which each enters with an error of at
  * most 2^-49 of the largest weight (vocab 2^-62 of it, if that is more, where thousands of
  * equal or nearly equal logits lie at a cut), so that a draw next to a border between two

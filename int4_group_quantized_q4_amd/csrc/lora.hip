@@ -5,10 +5,9 @@
 // is read once for each tile of its rows.  So rows of one adapter are gathered
 // into tiles: of up to 64 by a sort of the ids, of up to 16 where there are at most
 // 128 rows, among which every workgroup finds its tile's by itself.  The two products
-// run on the
-// 16x16x32 matrix cores with the factors' rows as the left and the tokens as the
-// right operand, so that a lane ends with neighbouring r, or neighbouring n, of
-// one token.
+// run on the 16x16x32 matrix cores with the factors' rows as the left and the tokens as
+// the right operand, so that a lane ends with neighbouring r, or neighbouring n, of one
+// token.
 //   shrink  h = x A^T, fp32; a workgroup's waves take pieces of K, and other
 //           workgroups parts of it where there are few tiles; the second kernel
 //           joins their sums.
@@ -18,9 +17,10 @@
 //           dimension: 3 rank / 32 steps.
 //
 // Figures, of both kernels in a graph (K 4096; rows, N, rank, adapters): 1 of 2816 by
-// 4096, rank 16: 8.6 us, two launches and as many round trips to memory.  64, 14336,
+// 4096, rank 16: 8.7 us, two launches and as many round trips to memory.  64, 14336,
 // 16, 48 of their own: 13.8 us, 25 MB, 1.8 TB/s; all of one adapter 11.6 us.  4090,
-// 14336, 64, 7: 77 us, of which the sort 7, shrink 19, expand 49 (235 MB at 4.8 TB/s).
+// 14336, 64, 7: 78 us; in a trace the sort 6, shrink 17, expand 56 (235 MB of y and out
+// at 4.2 TB/s).
 
 #include "common.h"
 #include "serving.h"
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraArgs l, L
           const int token = 16 * (g0 + g) + (m & ~1) + h, n = nb + 32 * (m & 1) + 8 * c;
           if (token < count && n < l.N) {
             u32x4* to = reinterpret_cast<u32x4*>(l.out + s_rows[token] * l.out_stride + n);
-            // past the caches where there are many rows (the second product of 4090 rows of 14336 columns: 49
-            // against 62 us); few are what the next call reads
+            // past the caches where there are many rows (the second product of 4090 rows of 14336 columns: 56
+            // against 66 us, the call 78 against 90); few are what the next call reads
             if constexpr (G > 1) __builtin_nontemporal_store(o[h], to);
             else *to = o[h];
           }

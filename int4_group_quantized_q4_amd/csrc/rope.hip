@@ -6,11 +6,14 @@
 // a 31-bit position and a 24-bit frequency, which has 55 bits and so two terms of
 // its own, times 1 / (2 pi) to 106 bits), less the nearest quarter turn, exactly,
 // so that the fp32 sine and cosine are of an angle within an eighth of a turn that
-// is good to its last bit, and the quarters swap and negate them.
+// is good to its last bit, and the quarters swap and negate them.  (In fp32, as the
+// turned elements keep 8 bits: their error is 2^-15 of that rounding.)
 //
 // Bound by memory for many rows: every element is read and written once (8191 rows
-// of 20 heads of 256, half of each turned: 26.8 us, 6.3 TB/s), by latency for few (a
-// row of 40 heads of 128 2.5 us, 64 rows 3.3).  The angles of a row are common to its
+// of 20 heads of 256, half of each turned: 34.3 us, 4.9 TB/s, where a call's rows come
+// from memory; 26.7 where it is repeated on the same 168 MB, half of whose reads the
+// last-level cache then answers), by latency for few (a row of 40 heads of 128 2.7 us,
+// 64 rows 3.4).  The angles of a row are common to its
 // heads: a workgroup takes whole rows (or a part of one) and computes each angle once,
 // into LDS.
 
@@ -23,8 +26,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 // Units, 16 dimensions of a head each, of one thread: two share an angle's cost (8191
-// rows as above 26.8 us, 32.7 with one, 27.5 with four), one where that leaves CUs
-// without work (64 rows 3.5 against 3.9 us in a graph).
+// rows as above, repeated, 26.7 us, 32.7 with one, 27.5 with four), one where that leaves
+// CUs without work (64 rows 3.5 against 3.9 us in a graph).
 constexpr int kFewUnits = 256 * kRopeThreads * 2;
 
 struct RopeTile {

@@ -1,7 +1,7 @@
 // One token a row, drawn from its logits with a given uniform number.
 //
 // The kept tokens are a first piece of the order (logit descending, id ascending),
-// so no sort of a row is needed.  Two kernels, that read the logits once:
+// so no sort of a row is needed.  Two kernels, which read the logits once:
 //   scan  a workgroup for up to 16384 logits (a row's chunks are alike in size): their largest one, the sum of their
 //         weights beside it (where the row needs the whole sum), and the
 //         candidates: all logits from a bound up that at least `rank` of them reach,
@@ -14,21 +14,27 @@
 //         only those of the bin with the border are compared (sorted are they where
 //         that bin has more than 256: ties).  A row without filters needs no
 //         candidates, only the 1024 logits in which the sums pass the number.
-// Where that piece may be too short (a nucleus of thousands of tokens) a third kernel
-// (rest) takes the row: several workgroups make histograms of its chunks' weights
+// A third one (rest) reads the rows again where that piece may be too short (a nucleus
+// of thousands of tokens): several workgroups make histograms of the row's chunks' weights
 // (and counts) over bins of a sixteenth of an octave, and the last one finds in them
-// the bin of the last kept logit, reads the row again for that bin's logits, and cuts
-// among them as above.  Where the bin holds too many (ties), a radix select over the
-// logits' order keys takes the histogram's place.
+// the bin of the last kept logit, reads the row once more for that bin's logits and one
+// chunk of it for the draw, and cuts among them as above.  Where the bin holds too many
+// (more than 2048: ties, long nuclei of the largest vocabularies) or a row has no
+// histograms (mostly by a top_k of up to 64), one workgroup's radix select over the
+// logits' order keys takes their place, and reads the row about a dozen times.
 //
-// Rows of 131072 fp32 logits, 54 to 64 of them, in us for the kernels: without filters
-// scan 11.4 (of which the 64-bit series take half: greedy rows 5.0), draw 5.6; top_k 50
-// and top_p 0.95 9.0 and 10.8; top_k 1000 9.3 and 13.7 (28.3 with all candidates
-// sorted); top_p 0.9 13.6 and 9.7; rest without rows 2 to 4, with one that needs it 52
-// (of which one CU's reading of the row takes 18), with 54 such rows 61.  (With the
+// Rows of 131072 fp32 logits, 64 of them, in us for the kernels: without filters
+// scan 11.5 (of which the 64-bit powers take half: greedy rows 5.3), draw 5.0; top_k 50
+// and top_p 0.95 8.7 and 10.9; top_k 1000 and top_p 0.9 10.2 and 14.2 (28.3 with all
+// candidates sorted); top_p 0.9 15.0 and 9.8; rest without rows 2 to 4, with one that needs
+// it 54 (of which one CU's reading of the row takes 18), with 64 such rows 64.  (With the
 // histograms made by every scan that took 19 to 36 for all rows with a long filter.)
-// 256 rows without filters: 35 and 5.3, 3.9 TB/s, the series' instructions beside the
-// loads.
+// 256 rows without filters: 34.5 and 5.3, 3.9 TB/s, the powers' instructions beside the
+// loads.  What the radix select takes is far from that: a row with fewer allowed tokens
+// than a top_k of 50, which misses the candidates because its few groups with a logit
+// make the bound high, 556 for the three kernels, 64 such rows 762; rows of 262144 with
+// temperature 1.5 and top_p 0.95, whose last bin holds some 3000 logits, 733 for one in
+// rest, 1004 for 64.
 //
 // The second kernel's time is that of fetching its code as much as of running it (a
 // workgroup passes through it once).  With the third kernel's code called from it, it
@@ -643,7 +649,7 @@ __device__ __forceinline__ void add_to_bins(const Piece<T>& piece, const Weight&
                                             uint32_t* s_count, bool counts) {
   const float ref = weight.steps(weight.m);
 #pragma unroll
-  for (int i = 0; i < kPer; i += 4) {   // four series together share their coefficients
+  for (int i = 0; i < kPer; i += 4) {   // four powers together share their coefficients
     double e[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) e[j] = exp2_f64(((double)piece.z[i + j] - weight.top) * weight.per);
@@ -996,7 +1002,8 @@ __device__ uint32_t radix_select(RadixShared& s, const R& row, const F& amount, 
   return prefix;
 }
 
-// For rows whose histograms do not say: many ties, infinities, extreme temperatures.
+// For rows that have no histograms (a top_k of up to 64, infinities, extreme temperatures,
+// numbers of 0 and 1) or whose histograms do not say (more than 2048 logits in the last bin).
 template <typename T>
 __device__ __forceinline__ void radix_row(RadixShared& s, const SampleArgs& a, const Row<T>& row, int64_t r,
                                           const Settings& set, const Weight& weight) {
